@@ -16,10 +16,10 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libquads.so")
 
-F32, BF16 = 0, 1
+F32, BF16, MXFP4 = 0, 1, 2
 GSCALE_GIVEN, WANT_SCORES = 1, 2
 OPERANDS_W4A4, OPERANDS_BF16, OPERANDS_BF16_QDQ, OPERANDS_BF16_W4 = 0, 1, 2, 3
-SCALES_ONLY = 4
+SCALES_ONLY, MX_SCALE_EVEN = 4, 8
 EPI_NONE, EPI_SWIGLU = 0, 1
 RAC_FORM_AUTO, RAC_FORM_EXACT, RAC_FORM_MERGED = 0, 1, 2
 
@@ -33,6 +33,20 @@ class QuadsError(RuntimeError):
 class _NVFP4(ctypes.Structure):
     _fields_ = [("codes", _vp), ("scales", _vp), ("gscale", _vp),
                 ("batch", _c_i64), ("rows", _c_i64), ("cols", _c_i64)]
+
+
+class _MXFP4(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp), ("batch", _c_i64), ("rows", _c_i64), ("cols", _c_i64)]
+
+
+class _MxGemmArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", _c_u32), ("flags", _c_u32), ("epilogue", _c_i32), ("y_dtype", _c_i32),
+        ("num_experts", _c_i32), ("reserved", _c_i32),
+        ("num_rows", _c_i64), ("act_rows", _c_i64), ("N", _c_i64), ("K", _c_i64),
+        ("x_codes", _vp), ("x_scales", _vp), ("w_codes", _vp), ("w_scales", _vp),
+        ("row_token", _vp), ("expert_offsets", _vp), ("y", _vp), ("y_scales", _vp),
+    ]
 
 
 class _GemmArgs(ctypes.Structure):
@@ -58,6 +72,9 @@ EXPORTS = [
     "quads_weight_qdq_workspace_bytes", "quads_weight_qdq",
     "quads_moe_route_workspace_bytes", "quads_moe_route", "quads_moe_combine",
     "quads_moe_wgrad_workspace_bytes", "quads_moe_wgrad_bf16", "quads_transpose_bf16",
+    "quads_quantize_mxfp4", "quads_dequantize_mxfp4", "quads_weight_qdq_mxfp4",
+    "quads_moe_mxfp4_gemm", "quads_moe_mxfp4_ffn_workspace_bytes", "quads_moe_mxfp4_ffn",
+    "quads_moe_gated_forward_bf16", "quads_moe_gated_backward_bf16",
 ]
 
 _lib = None
@@ -115,6 +132,23 @@ def load(path: str = LIB_PATH):
                                        ctypes.c_size_t, _vp]
     L.quads_transpose_bf16.restype = ctypes.c_int
     L.quads_transpose_bf16.argtypes = [_vp, _c_i64, _c_i64, _c_i64, _vp, _vp]
+    L.quads_quantize_mxfp4.restype = ctypes.c_int
+    L.quads_quantize_mxfp4.argtypes = [_vp, ctypes.c_int, _MXFP4, _c_u32, _vp]
+    L.quads_dequantize_mxfp4.restype = ctypes.c_int
+    L.quads_dequantize_mxfp4.argtypes = [_MXFP4, _vp, ctypes.c_int, _vp]
+    L.quads_weight_qdq_mxfp4.restype = ctypes.c_int
+    L.quads_weight_qdq_mxfp4.argtypes = [_vp, _c_i64, _c_i64, _c_i64, _vp, ctypes.POINTER(_MXFP4), _c_u32, _vp]
+    L.quads_moe_mxfp4_gemm.restype = ctypes.c_int
+    L.quads_moe_mxfp4_gemm.argtypes = [ctypes.POINTER(_MxGemmArgs), _vp]
+    L.quads_moe_mxfp4_ffn_workspace_bytes.restype = ctypes.c_size_t
+    L.quads_moe_mxfp4_ffn_workspace_bytes.argtypes = [_c_i64, _c_i64, _c_i64, _c_i64]
+    L.quads_moe_mxfp4_ffn.restype = ctypes.c_int
+    L.quads_moe_mxfp4_ffn.argtypes = [_vp, ctypes.POINTER(_MXFP4), ctypes.POINTER(_MXFP4), _vp, _vp, _c_i32, _c_i64,
+                                      _c_i64, _c_i64, _c_i64, _vp, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
+    L.quads_moe_gated_forward_bf16.restype = ctypes.c_int
+    L.quads_moe_gated_forward_bf16.argtypes = [_vp, _vp, _vp, _vp, _c_i32, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp]
+    L.quads_moe_gated_backward_bf16.restype = ctypes.c_int
+    L.quads_moe_gated_backward_bf16.argtypes = [_vp, _vp, _vp, _vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _vp]
     _lib = L
     return L
 
@@ -598,3 +632,283 @@ class QatBackward:
             fn()
         dx = self.combine.out if self.combine is not None else self.dxr_call.y
         return dx, self.dxr_call.y, self.wgrad.dw
+
+
+# ---- MXFP4 and the gated expert block -------------------------------------------
+#
+# These calls run on the stream that is current for their tensors' device,
+# whichever device is current.
+
+def _on_device(x: torch.Tensor, fn, what: str, *args):
+    """fn(*args, stream of x's device), with that device current."""
+    dev = x.device
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != 0:
+        _check(status, what)
+
+
+def _require(what: str, t: torch.Tensor, name: str, dtype, like: torch.Tensor | None = None):
+    if not t.is_cuda or not t.is_contiguous():
+        raise QuadsError(f"{what}: {name} must be contiguous and on the GPU")
+    if t.dtype != dtype:
+        raise QuadsError(f"{what}: {name} must be {dtype}, not {t.dtype}")
+    if like is not None and t.device != like.device:
+        raise QuadsError(f"{what}: {name} is on {t.device}, not {like.device}")
+
+
+def _batch_rows_cols(what: str, shape):
+    if len(shape) == 2:
+        return (1, *shape)
+    if len(shape) == 3:
+        return tuple(shape)
+    raise QuadsError(f"{what}: expected [rows, cols] or [batch, rows, cols], not {tuple(shape)}")
+
+
+_RULES = {"floor": 0, "even": MX_SCALE_EVEN}
+
+
+def _rule_flags(rule: str) -> int:
+    if rule not in _RULES:
+        raise QuadsError(f"rule must be 'floor' or 'even', not {rule!r}")
+    return _RULES[rule]
+
+
+@dataclass
+class MXFP4Tensor:
+    """Packed E2M1 codes [batch, rows, cols/2] u8 and E8M0 scales [batch, rows,
+    cols/32] u8 (batch axis omitted when batch == 1)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    batch: int
+    rows: int
+    cols: int
+
+    def c_struct(self):
+        return _MXFP4(self.codes.data_ptr(), self.scales.data_ptr(), self.batch, self.rows, self.cols)
+
+
+def empty_mxfp4(batch, rows, cols, device):
+    shape = (rows,) if batch == 1 else (batch, rows)
+    return MXFP4Tensor(torch.empty(*shape, cols // 2, dtype=torch.uint8, device=device),
+                       torch.empty(*shape, cols // 32, dtype=torch.uint8, device=device), batch, rows, cols)
+
+
+def mxfp4_tensor(codes: torch.Tensor, scales: torch.Tensor) -> MXFP4Tensor:
+    """An MXFP4Tensor over existing codes [.., rows, cols/2] and scales
+    [.., rows, cols/32] (a checkpoint's, or another library's)."""
+    _require("mxfp4_tensor", codes, "codes", torch.uint8)
+    _require("mxfp4_tensor", scales, "scales", torch.uint8, codes)
+    batch, rows, half = _batch_rows_cols("mxfp4_tensor", codes.shape)
+    if half % 16 or codes.shape[:-1] != scales.shape[:-1] or scales.shape[-1] * 16 != half:
+        raise QuadsError(f"mxfp4_tensor: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not match")
+    return MXFP4Tensor(codes, scales, batch, rows, 2 * half)
+
+
+def _require_mx(what: str, q: MXFP4Tensor, name: str, like: torch.Tensor | None = None):
+    _require(what, q.codes, name + ".codes", torch.uint8, like)
+    _require(what, q.scales, name + ".scales", torch.uint8, q.codes)
+    n = q.batch * q.rows * q.cols
+    if q.codes.numel() * 2 != n or q.scales.numel() * 32 != n:
+        raise QuadsError(f"{what}: {name}'s arrays do not hold [{q.batch}, {q.rows}, {q.cols}]")
+
+
+def quantize_mxfp4(x: torch.Tensor, rule: str = "floor", out: MXFP4Tensor | None = None) -> MXFP4Tensor:
+    """quads_quantize_mxfp4: x bf16/fp32 [rows, cols] or [batch, rows, cols],
+    cols % 32 == 0.  rule: "floor" (OCP) or "even" (see quads.h)."""
+    what = "quantize_mxfp4"
+    _require(what, x, "x", torch.float32 if x.dtype == torch.float32 else torch.bfloat16)
+    batch, rows, cols = _batch_rows_cols(what, x.shape)
+    if cols % 32:
+        raise QuadsError(f"{what}: cols ({cols}) must be a multiple of 32")
+    flags = _rule_flags(rule)
+    if out is None:
+        out = empty_mxfp4(batch, rows, cols, x.device)
+    else:
+        _require_mx(what, out, "out", x)
+        if (out.batch, out.rows, out.cols) != (batch, rows, cols):
+            raise QuadsError(f"{what}: out is [{out.batch}, {out.rows}, {out.cols}], x {tuple(x.shape)}")
+    _on_device(x, load().quads_quantize_mxfp4, what, x.data_ptr(), _dtype_code(x), out.c_struct(), flags)
+    return out
+
+
+def dequantize_mxfp4(q: MXFP4Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """quads_dequantize_mxfp4: the bf16 or fp32 values q stands for."""
+    what = "dequantize_mxfp4"
+    _require_mx(what, q, "q")
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise QuadsError(f"{what}: dtype must be bfloat16 or float32, not {dtype}")
+    shape = (*q.codes.shape[:-1], q.cols)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=q.codes.device)
+    else:
+        _require(what, out, "out", dtype, q.codes)
+        if tuple(out.shape) != shape:
+            raise QuadsError(f"{what}: out must be {shape}")
+    _on_device(out, load().quads_dequantize_mxfp4, what, q.c_struct(), out.data_ptr(), _dtype_code(out))
+    return out
+
+
+def weight_qdq_mxfp4(w: torch.Tensor, rule: str = "floor", export: bool = False, out: torch.Tensor | None = None):
+    """quads_weight_qdq_mxfp4: bf16 masters [rows, cols] or [batch, rows, cols]
+    -> (their bf16 MXFP4 values, the MXFP4Tensor with export=True, else None)."""
+    what = "weight_qdq_mxfp4"
+    _require(what, w, "w", torch.bfloat16)
+    batch, rows, cols = _batch_rows_cols(what, w.shape)
+    if cols % 32:
+        raise QuadsError(f"{what}: cols ({cols}) must be a multiple of 32")
+    flags = _rule_flags(rule)
+    if out is None:
+        out = torch.empty_like(w)
+    else:
+        _require(what, out, "out", torch.bfloat16, w)
+        if out.shape != w.shape:
+            raise QuadsError(f"{what}: out must have w's shape")
+    q = empty_mxfp4(batch, rows, cols, w.device) if export else None
+    _on_device(w, load().quads_weight_qdq_mxfp4, what, w.data_ptr(), batch, rows, cols, out.data_ptr(),
+               ctypes.byref(q.c_struct()) if q is not None else None, flags)
+    return out, q
+
+
+def _grouping(what: str, x: torch.Tensor, act_rows: int, expert_offsets, row_token, E: int):
+    """Checks the grouping tensors; -> routed row count."""
+    _require(what, expert_offsets, "expert_offsets", torch.int32, x)
+    if expert_offsets.numel() != E + 1:
+        raise QuadsError(f"{what}: expert_offsets holds {expert_offsets.numel()} values for {E} experts")
+    if row_token is None:
+        return act_rows
+    _require(what, row_token, "row_token", torch.int32, x)
+    return row_token.numel()
+
+
+def moe_mxfp4_gemm(x: MXFP4Tensor, w: MXFP4Tensor, expert_offsets: torch.Tensor,
+                   row_token: torch.Tensor | None = None, epilogue: int = EPI_NONE, y_dtype=torch.float32, y=None):
+    """quads_moe_mxfp4_gemm: routed rows of x [act_rows, K] times w [E, N, K].
+
+    y_dtype: torch.float32 / torch.bfloat16 -> [R, N]; with EPI_SWIGLU
+    torch.bfloat16 -> h [R, N/2], or MXFP4 -> h as an MXFP4Tensor."""
+    what = "moe_mxfp4_gemm"
+    _require_mx(what, x, "x")
+    _require_mx(what, w, "w", x.codes)
+    if x.batch != 1 or x.cols != w.cols:
+        raise QuadsError(f"{what}: x [{x.batch}, {x.rows}, {x.cols}] does not go with w [{w.batch}, {w.rows}, {w.cols}]")
+    dev = x.codes.device
+    R = _grouping(what, x.codes, x.rows, expert_offsets, row_token, w.batch)
+    width = w.rows // 2 if epilogue == EPI_SWIGLU else w.rows
+    a = _MxGemmArgs()
+    a.struct_size = ctypes.sizeof(_MxGemmArgs)
+    a.epilogue = epilogue
+    a.num_experts = w.batch
+    a.num_rows, a.act_rows, a.N, a.K = R, x.rows, w.rows, x.cols
+    a.x_codes, a.x_scales = x.codes.data_ptr(), x.scales.data_ptr()
+    a.w_codes, a.w_scales = w.codes.data_ptr(), w.scales.data_ptr()
+    a.row_token = None if row_token is None else row_token.data_ptr()
+    a.expert_offsets = expert_offsets.data_ptr()
+    if y_dtype == MXFP4:
+        a.y_dtype = MXFP4
+        if y is None:
+            y = empty_mxfp4(1, R, width - width % 32, dev)
+        else:
+            _require_mx(what, y, "y", x.codes)
+            if (y.batch, y.rows, y.cols) != (1, R, width):
+                raise QuadsError(f"{what}: y must be [{R}, {width}]")
+        a.y, a.y_scales = y.codes.data_ptr(), y.scales.data_ptr()
+    else:
+        if y_dtype not in (torch.float32, torch.bfloat16):
+            raise QuadsError(f"{what}: y_dtype must be float32, bfloat16 or MXFP4, not {y_dtype}")
+        a.y_dtype = BF16 if y_dtype == torch.bfloat16 else F32
+        if y is None:
+            y = torch.empty(R, width, dtype=y_dtype, device=dev)
+        else:
+            _require(what, y, "y", y_dtype, x.codes)
+            if tuple(y.shape) != (R, width):
+                raise QuadsError(f"{what}: y must be [{R}, {width}]")
+        a.y = y.data_ptr()
+    _on_device(x.codes, load().quads_moe_mxfp4_gemm, what, ctypes.byref(a))
+    return y
+
+
+def moe_mxfp4_ffn(x: torch.Tensor, w_gate_up: MXFP4Tensor, w_down: MXFP4Tensor, expert_offsets: torch.Tensor,
+                  row_token: torch.Tensor | None = None, y_dtype=torch.float32, y: torch.Tensor | None = None,
+                  ws: torch.Tensor | None = None) -> torch.Tensor:
+    """quads_moe_mxfp4_ffn: the gated expert block from bf16 activations x
+    [act_rows, H] -> y [R, H] (float32 rows for moe_combine, or bfloat16).  ws:
+    a uint8 workspace of mxfp4_ffn_workspace_bytes(...) to reuse."""
+    what = "moe_mxfp4_ffn"
+    _require(what, x, "x", torch.bfloat16)
+    _require_mx(what, w_gate_up, "w_gate_up", x)
+    _require_mx(what, w_down, "w_down", x)
+    if x.dim() != 2 or w_gate_up.rows != 2 * w_down.cols or w_gate_up.cols != x.shape[1] or w_down.rows != x.shape[1] \
+            or w_down.batch != w_gate_up.batch:
+        raise QuadsError(f"{what}: x {tuple(x.shape)} needs w_gate_up [E, 2 I, H] and w_down [E, H, I]")
+    if y_dtype not in (torch.float32, torch.bfloat16):
+        raise QuadsError(f"{what}: y_dtype must be float32 or bfloat16, not {y_dtype}")
+    L = load()
+    A, H = x.shape
+    I, E = w_down.cols, w_gate_up.batch
+    R = _grouping(what, x, A, expert_offsets, row_token, E)
+    if y is None:
+        y = torch.empty(R, H, dtype=y_dtype, device=x.device)
+    else:
+        _require(what, y, "y", y_dtype, x)
+        if tuple(y.shape) != (R, H):
+            raise QuadsError(f"{what}: y must be [{R}, {H}]")
+    if ws is None:
+        ws = _workspace(L.quads_moe_mxfp4_ffn_workspace_bytes(A, R, H, I), x.device)
+    else:
+        _require(what, ws, "ws", torch.uint8, x)
+    _on_device(x, L.quads_moe_mxfp4_ffn, what, x.data_ptr(), ctypes.byref(w_gate_up.c_struct()),
+               ctypes.byref(w_down.c_struct()), None if row_token is None else row_token.data_ptr(),
+               expert_offsets.data_ptr(), E, R, A, H, I, y.data_ptr(), BF16 if y_dtype == torch.bfloat16 else F32,
+               ws.data_ptr(), ws.numel())
+    return y
+
+
+def mxfp4_ffn_workspace_bytes(act_rows: int, num_rows: int, hidden: int, inter: int) -> int:
+    return int(load().quads_moe_mxfp4_ffn_workspace_bytes(act_rows, num_rows, hidden, inter))
+
+
+def moe_gated_forward(x: torch.Tensor, w_gate_up: torch.Tensor, expert_offsets: torch.Tensor,
+                      row_token: torch.Tensor | None = None, keep: bool = True):
+    """quads_moe_gated_forward_bf16: x bf16 [act_rows, H], w_gate_up bf16
+    [E, 2 I, H] -> (h bf16 [R, I], gate | up bf16 [R, 2 I], or None with keep=False)."""
+    what = "moe_gated_forward"
+    _require(what, x, "x", torch.bfloat16)
+    _require(what, w_gate_up, "w_gate_up", torch.bfloat16, x)
+    if x.dim() != 2 or w_gate_up.dim() != 3 or w_gate_up.shape[2] != x.shape[1] or w_gate_up.shape[1] % 2:
+        raise QuadsError(f"{what}: x {tuple(x.shape)} and w_gate_up {tuple(w_gate_up.shape)} do not match")
+    (A, H), (E, I2, _) = x.shape, w_gate_up.shape
+    R = _grouping(what, x, A, expert_offsets, row_token, E)
+    h = torch.empty(R, I2 // 2, dtype=torch.bfloat16, device=x.device)
+    gu = torch.empty(R, I2, dtype=torch.bfloat16, device=x.device) if keep else None
+    _on_device(x, load().quads_moe_gated_forward_bf16, what, x.data_ptr(), w_gate_up.data_ptr(),
+               None if row_token is None else row_token.data_ptr(), expert_offsets.data_ptr(), E, R, A, H, I2 // 2,
+               h.data_ptr(), None if gu is None else gu.data_ptr())
+    return h, gu
+
+
+def moe_gated_backward(dy: torch.Tensor, w_down: torch.Tensor, gu: torch.Tensor, expert_offsets: torch.Tensor,
+                       dgu: torch.Tensor | None = None) -> torch.Tensor:
+    """quads_moe_gated_backward_bf16: dy bf16 [R, H], w_down bf16 [E, H, I], gu
+    bf16 [R, 2 I] of the forward -> gradient of gu, bf16 [R, 2 I] (dgu may be gu)."""
+    what = "moe_gated_backward"
+    _require(what, dy, "dy", torch.bfloat16)
+    _require(what, w_down, "w_down", torch.bfloat16, dy)
+    _require(what, gu, "gu", torch.bfloat16, dy)
+    if dy.dim() != 2 or w_down.dim() != 3 or w_down.shape[1] != dy.shape[1] \
+            or tuple(gu.shape) != (dy.shape[0], 2 * w_down.shape[2]):
+        raise QuadsError(f"{what}: dy {tuple(dy.shape)}, w_down {tuple(w_down.shape)} and gu {tuple(gu.shape)} do not match")
+    (R, H), (E, _, I) = dy.shape, w_down.shape
+    _grouping(what, dy, R, expert_offsets, None, E)
+    if dgu is None:
+        dgu = torch.empty_like(gu)
+    else:
+        _require(what, dgu, "dgu", torch.bfloat16, dy)
+        if dgu.shape != gu.shape:
+            raise QuadsError(f"{what}: dgu must have gu's shape")
+    _on_device(dy, load().quads_moe_gated_backward_bf16, what, dy.data_ptr(), w_down.data_ptr(), gu.data_ptr(),
+               expert_offsets.data_ptr(), E, R, H, I, dgu.data_ptr())
+    return dgu

@@ -485,4 +485,253 @@ quads_status_t quads_transpose_bf16(const void *in_bf16, int64_t batch, int64_t 
                        "transpose");
 }
 
+// ---- MXFP4 -------------------------------------------------------------------
+
+static quads_status_t mx_shape(const char *what, int64_t batch, int64_t rows, int64_t cols) {
+  if (batch < 1 || rows < 0 || cols <= 0 || cols % 32)
+    return fail(QUADS_ERR_SHAPE, "%s: bad shape (cols must be a positive multiple of 32)", what);
+  if (!mul_ok(rows, cols, kMaxElems) || !mul_ok(batch, rows * cols, kMaxElems))
+    return fail(QUADS_ERR_SHAPE, "%s: size overflow", what);
+  return QUADS_OK;
+}
+
+quads_status_t quads_quantize_mxfp4(const void *x, quads_dtype_t dt, quads_mxfp4_t out, uint32_t flags, void *stream) {
+  if (dt != QUADS_F32 && dt != QUADS_BF16) return fail(QUADS_ERR_ARG, "quantize_mxfp4: bad dtype %d", dt);
+  if (flags & ~QUADS_MX_SCALE_EVEN) return fail(QUADS_ERR_ARG, "quantize_mxfp4: unknown flags");
+  const quads_status_t st = mx_shape("quantize_mxfp4", out.batch, out.rows, out.cols);
+  if (st != QUADS_OK) return st;
+  if (out.rows == 0) return ok();
+  if (!x || !out.codes || !out.scales) return fail(QUADS_ERR_ARG, "quantize_mxfp4: null pointer");
+  if (misaligned({x, out.codes, out.scales}))
+    return fail(QUADS_ERR_ARG, "quantize_mxfp4: arrays must be 16-byte aligned");
+  quads::MxQuantizeLaunch a{};
+  a.x = x;
+  a.x_bf16 = dt == QUADS_BF16;
+  a.even = (flags & QUADS_MX_SCALE_EVEN) != 0;
+  a.elems = out.batch * out.rows * out.cols;
+  a.codes = out.codes;
+  a.scales = out.scales;
+  return device_status(quads::launch_mx_quantize(a, static_cast<hipStream_t>(stream)), "quantize_mxfp4");
+}
+
+quads_status_t quads_dequantize_mxfp4(quads_mxfp4_t q, void *out, quads_dtype_t dt, void *stream) {
+  if (dt != QUADS_F32 && dt != QUADS_BF16) return fail(QUADS_ERR_ARG, "dequantize_mxfp4: bad dtype %d", dt);
+  const quads_status_t st = mx_shape("dequantize_mxfp4", q.batch, q.rows, q.cols);
+  if (st != QUADS_OK) return st;
+  if (q.rows == 0) return ok();
+  if (!out || !q.codes || !q.scales) return fail(QUADS_ERR_ARG, "dequantize_mxfp4: null pointer");
+  if (misaligned({out, q.codes, q.scales}))
+    return fail(QUADS_ERR_ARG, "dequantize_mxfp4: arrays must be 16-byte aligned");
+  return device_status(quads::launch_mx_dequantize(q.codes, q.scales, q.batch * q.rows * q.cols, out, dt == QUADS_BF16,
+                                                   static_cast<hipStream_t>(stream)),
+                       "dequantize_mxfp4");
+}
+
+quads_status_t quads_weight_qdq_mxfp4(const void *w_bf16, int64_t batch, int64_t rows, int64_t cols, void *w_out_bf16,
+                                      const quads_mxfp4_t *q_out, uint32_t flags, void *stream) {
+  if (flags & ~QUADS_MX_SCALE_EVEN) return fail(QUADS_ERR_ARG, "weight_qdq_mxfp4: unknown flags");
+  const quads_status_t st = mx_shape("weight_qdq_mxfp4", batch, rows, cols);
+  if (st != QUADS_OK) return st;
+  if (q_out && (q_out->batch != batch || q_out->rows != rows || q_out->cols != cols))
+    return fail(QUADS_ERR_SHAPE, "weight_qdq_mxfp4: q_out shape mismatch");
+  if (rows == 0) return ok();
+  if (!w_bf16 || !w_out_bf16 || (q_out && (!q_out->codes || !q_out->scales)))
+    return fail(QUADS_ERR_ARG, "weight_qdq_mxfp4: null pointer");
+  if (misaligned({w_bf16, w_out_bf16}) || (q_out && misaligned({q_out->codes, q_out->scales})))
+    return fail(QUADS_ERR_ARG, "weight_qdq_mxfp4: arrays must be 16-byte aligned");
+  quads::MxQuantizeLaunch a{};
+  a.x = w_bf16;
+  a.x_bf16 = true;
+  a.even = (flags & QUADS_MX_SCALE_EVEN) != 0;
+  a.elems = batch * rows * cols;
+  a.codes = q_out ? q_out->codes : nullptr;
+  a.scales = q_out ? q_out->scales : nullptr;
+  a.qdq_out = static_cast<uint16_t *>(w_out_bf16);
+  return device_status(quads::launch_mx_quantize(a, static_cast<hipStream_t>(stream)), "weight_qdq_mxfp4");
+}
+
+// Grouping and size checks shared by the MXFP4 and gated products.
+static quads_status_t grouped_shape(const char *what, int32_t E, int64_t R, int64_t A, const int32_t *row_token,
+                                    int64_t N, int64_t K) {
+  if (E < 1 || E > 1024) return fail(QUADS_ERR_SHAPE, "%s: num_experts outside [1,1024]", what);
+  if (R < 0 || A < 0 || R > (int64_t(1) << 31) - 1024 || A > (int64_t(1) << 31) - 1)
+    return fail(QUADS_ERR_SHAPE, "%s: row counts out of range", what);
+  if (N >= (int64_t(1) << 24) || K >= (int64_t(1) << 24) || !mul_ok(R, N, kMaxElems) || !mul_ok(E * N, K, kMaxElems))
+    return fail(QUADS_ERR_SHAPE, "%s: size overflow", what);
+  if (row_token == nullptr && A < R) return fail(QUADS_ERR_SHAPE, "%s: identity rows need act_rows >= num_rows", what);
+  if (R > 0 && A == 0) return fail(QUADS_ERR_SHAPE, "%s: routed rows of no activation rows", what);
+  return QUADS_OK;
+}
+
+quads_status_t quads_moe_mxfp4_gemm(const quads_moe_mxfp4_args *a, void *stream) {
+  if (!a) return fail(QUADS_ERR_ARG, "mxfp4_gemm: null args");
+  if (a->struct_size != sizeof(quads_moe_mxfp4_args))
+    return fail(QUADS_ERR_ARG, "mxfp4_gemm: struct_size %u != %zu", a->struct_size, sizeof(quads_moe_mxfp4_args));
+  if (a->flags || a->reserved) return fail(QUADS_ERR_ARG, "mxfp4_gemm: unknown flags");
+  if (a->epilogue != QUADS_EPI_NONE && a->epilogue != QUADS_EPI_SWIGLU)
+    return fail(QUADS_ERR_ARG, "mxfp4_gemm: bad epilogue");
+  const bool swiglu = a->epilogue == QUADS_EPI_SWIGLU;
+  if (swiglu ? a->y_dtype != QUADS_BF16 && a->y_dtype != QUADS_MXFP4
+             : a->y_dtype != QUADS_F32 && a->y_dtype != QUADS_BF16)
+    return fail(QUADS_ERR_ARG, "mxfp4_gemm: y_dtype %d does not go with the epilogue", a->y_dtype);
+  if (a->K <= 0 || a->K % 32) return fail(QUADS_ERR_SHAPE, "mxfp4_gemm: K must be a positive multiple of 32");
+  if (a->N <= 0 || a->N % (swiglu ? 64 : 32))
+    return fail(QUADS_ERR_SHAPE, "mxfp4_gemm: N must be a positive multiple of %d", swiglu ? 64 : 32);
+  const quads_status_t st = grouped_shape("mxfp4_gemm", a->num_experts, a->num_rows, a->act_rows, a->row_token, a->N, a->K);
+  if (st != QUADS_OK) return st;
+  if (!a->expert_offsets || !a->w_codes || !a->w_scales) return fail(QUADS_ERR_ARG, "mxfp4_gemm: null pointer");
+  if (misaligned({a->x_codes, a->x_scales, a->w_codes, a->w_scales, a->y, a->y_scales}))
+    return fail(QUADS_ERR_ARG, "mxfp4_gemm: arrays must be 16-byte aligned");
+  if (a->num_rows == 0) return ok();
+  if (!a->x_codes || !a->x_scales || !a->y || (a->y_dtype == QUADS_MXFP4 && !a->y_scales))
+    return fail(QUADS_ERR_ARG, "mxfp4_gemm: null pointer");
+  quads::MxGemmLaunch g{};
+  g.epi = !swiglu ? (a->y_dtype == QUADS_F32 ? quads::kEpiF32 : quads::kEpiBf16)
+                  : (a->y_dtype == QUADS_BF16 ? quads::kEpiSwiglu : quads::kEpiSwigluMx);
+  g.E = a->num_experts;
+  g.R = a->num_rows;
+  g.N = a->N;
+  g.K = a->K;
+  g.x_codes = a->x_codes;
+  g.x_scales = a->x_scales;
+  g.w_codes = a->w_codes;
+  g.w_scales = a->w_scales;
+  g.row_token = a->row_token;
+  g.expert_offsets = a->expert_offsets;
+  g.y = a->y;
+  g.y_scales = a->y_dtype == QUADS_MXFP4 ? a->y_scales : nullptr;
+  return device_status(quads::launch_mx_gemm(g, static_cast<hipStream_t>(stream)), "mxfp4_gemm");
+}
+
+static int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+size_t quads_moe_mxfp4_ffn_workspace_bytes(int64_t act_rows, int64_t num_rows, int64_t hidden, int64_t inter) {
+  if (act_rows < 0 || num_rows < 0 || hidden <= 0 || inter <= 0 || hidden % 32 || inter % 32 ||
+      !mul_ok(act_rows, hidden, kMaxElems) || !mul_ok(num_rows, inter, kMaxElems))
+    return 0;
+  return static_cast<size_t>(up256(act_rows * hidden / 2) + up256(act_rows * hidden / 32) +
+                             up256(num_rows * inter / 2) + up256(num_rows * inter / 32));
+}
+
+quads_status_t quads_moe_mxfp4_ffn(const void *x_bf16, const quads_mxfp4_t *w_gate_up, const quads_mxfp4_t *w_down,
+                                   const int32_t *row_token, const int32_t *expert_offsets, int32_t num_experts,
+                                   int64_t num_rows, int64_t act_rows, int64_t hidden, int64_t inter, void *y,
+                                   quads_dtype_t y_dtype, void *ws, size_t ws_bytes, void *stream) {
+  if (y_dtype != QUADS_F32 && y_dtype != QUADS_BF16) return fail(QUADS_ERR_ARG, "mxfp4_ffn: bad y_dtype %d", y_dtype);
+  if (hidden <= 0 || hidden % 32 || inter <= 0 || inter % 32)
+    return fail(QUADS_ERR_SHAPE, "mxfp4_ffn: hidden and inter must be positive multiples of 32");
+  quads_status_t st = grouped_shape("mxfp4_ffn", num_experts, num_rows, act_rows, row_token, 2 * inter, hidden);
+  if (st == QUADS_OK) st = grouped_shape("mxfp4_ffn", num_experts, num_rows, num_rows, row_token, hidden, inter);
+  if (st == QUADS_OK && !mul_ok(act_rows, hidden, kMaxElems)) st = fail(QUADS_ERR_SHAPE, "mxfp4_ffn: size overflow");
+  if (st != QUADS_OK) return st;
+  if (!w_gate_up || !w_down || !w_gate_up->codes || !w_gate_up->scales || !w_down->codes || !w_down->scales ||
+      !expert_offsets)
+    return fail(QUADS_ERR_ARG, "mxfp4_ffn: null pointer");
+  if (w_gate_up->batch != num_experts || w_gate_up->rows != 2 * inter || w_gate_up->cols != hidden ||
+      w_down->batch != num_experts || w_down->rows != hidden || w_down->cols != inter)
+    return fail(QUADS_ERR_SHAPE, "mxfp4_ffn: weights must be [E, 2 inter, hidden] and [E, hidden, inter]");
+  if (misaligned({x_bf16, w_gate_up->codes, w_gate_up->scales, w_down->codes, w_down->scales, y, ws}))
+    return fail(QUADS_ERR_ARG, "mxfp4_ffn: arrays must be 16-byte aligned");
+  if (num_rows == 0) return ok();
+  if (!x_bf16 || !y) return fail(QUADS_ERR_ARG, "mxfp4_ffn: null pointer");
+  const size_t need = quads_moe_mxfp4_ffn_workspace_bytes(act_rows, num_rows, hidden, inter);
+  if (ws == nullptr || ws_bytes < need) return fail(QUADS_ERR_WORKSPACE, "mxfp4_ffn: workspace too small (need %zu)", need);
+  uint8_t *xc = static_cast<uint8_t *>(ws), *xs = xc + up256(act_rows * hidden / 2);
+  uint8_t *hc = xs + up256(act_rows * hidden / 32), *hs = hc + up256(num_rows * inter / 2);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  quads::MxQuantizeLaunch q{};
+  q.x = x_bf16;
+  q.x_bf16 = true;
+  q.elems = act_rows * hidden;
+  q.codes = xc;
+  q.scales = xs;
+  hipError_t e = quads::launch_mx_quantize(q, s);
+  if (e != hipSuccess) return device_status(e, "mxfp4_ffn: quantize");
+  quads::MxGemmLaunch g{};
+  g.epi = quads::kEpiSwigluMx;
+  g.E = num_experts;
+  g.R = num_rows;
+  g.N = 2 * inter;
+  g.K = hidden;
+  g.x_codes = xc;
+  g.x_scales = xs;
+  g.w_codes = w_gate_up->codes;
+  g.w_scales = w_gate_up->scales;
+  g.row_token = row_token;
+  g.expert_offsets = expert_offsets;
+  g.y = hc;
+  g.y_scales = hs;
+  e = quads::launch_mx_gemm(g, s);
+  if (e != hipSuccess) return device_status(e, "mxfp4_ffn: gate_up");
+  g.epi = y_dtype == QUADS_F32 ? quads::kEpiF32 : quads::kEpiBf16;
+  g.N = hidden;
+  g.K = inter;
+  g.x_codes = hc;
+  g.x_scales = hs;
+  g.w_codes = w_down->codes;
+  g.w_scales = w_down->scales;
+  g.row_token = nullptr;
+  g.y = y;
+  g.y_scales = nullptr;
+  return device_status(quads::launch_mx_gemm(g, s), "mxfp4_ffn: down");
+}
+
+// ---- the trainer's gated block -------------------------------------------------
+
+static quads_status_t gated_shape(const char *what, int64_t hidden, int64_t inter) {
+  if (hidden <= 0 || hidden % 16 || inter <= 0 || inter % 16)
+    return fail(QUADS_ERR_SHAPE, "%s: hidden and inter must be positive multiples of 16", what);
+  return QUADS_OK;
+}
+
+quads_status_t quads_moe_gated_forward_bf16(const void *x_bf16, const void *w_gate_up_bf16, const int32_t *row_token,
+                                            const int32_t *expert_offsets, int32_t num_experts, int64_t num_rows,
+                                            int64_t act_rows, int64_t hidden, int64_t inter, void *h_bf16,
+                                            void *gu_bf16, void *stream) {
+  quads_status_t st = gated_shape("gated_forward", hidden, inter);
+  if (st == QUADS_OK) st = grouped_shape("gated_forward", num_experts, num_rows, act_rows, row_token, 2 * inter, hidden);
+  if (st != QUADS_OK) return st;
+  if (!expert_offsets || !w_gate_up_bf16) return fail(QUADS_ERR_ARG, "gated_forward: null pointer");
+  if (misaligned({x_bf16, w_gate_up_bf16, h_bf16, gu_bf16}))
+    return fail(QUADS_ERR_ARG, "gated_forward: arrays must be 16-byte aligned");
+  if (num_rows == 0) return ok();
+  if (!x_bf16 || !h_bf16) return fail(QUADS_ERR_ARG, "gated_forward: null pointer");
+  quads::GatedLaunch a{};
+  a.E = num_experts;
+  a.R = num_rows;
+  a.hidden = hidden;
+  a.inter = inter;
+  a.x = static_cast<const uint16_t *>(x_bf16);
+  a.w = static_cast<const uint16_t *>(w_gate_up_bf16);
+  a.row_token = row_token;
+  a.expert_offsets = expert_offsets;
+  a.out = static_cast<uint16_t *>(h_bf16);
+  a.pre = static_cast<uint16_t *>(gu_bf16);
+  return device_status(quads::launch_gated_forward(a, static_cast<hipStream_t>(stream)), "gated_forward");
+}
+
+quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_down_bf16, const void *gu_bf16,
+                                             const int32_t *expert_offsets, int32_t num_experts, int64_t num_rows,
+                                             int64_t hidden, int64_t inter, void *dgu_bf16, void *stream) {
+  quads_status_t st = gated_shape("gated_backward", hidden, inter);
+  if (st == QUADS_OK) st = grouped_shape("gated_backward", num_experts, num_rows, num_rows, nullptr, 2 * inter, hidden);
+  if (st != QUADS_OK) return st;
+  if (!expert_offsets || !w_down_bf16) return fail(QUADS_ERR_ARG, "gated_backward: null pointer");
+  if (misaligned({dy_bf16, w_down_bf16, gu_bf16, dgu_bf16}))
+    return fail(QUADS_ERR_ARG, "gated_backward: arrays must be 16-byte aligned");
+  if (num_rows == 0) return ok();
+  if (!dy_bf16 || !gu_bf16 || !dgu_bf16) return fail(QUADS_ERR_ARG, "gated_backward: null pointer");
+  quads::GatedLaunch a{};
+  a.E = num_experts;
+  a.R = num_rows;
+  a.hidden = hidden;
+  a.inter = inter;
+  a.x = static_cast<const uint16_t *>(dy_bf16);
+  a.w = static_cast<const uint16_t *>(w_down_bf16);
+  a.expert_offsets = expert_offsets;
+  a.out = static_cast<uint16_t *>(dgu_bf16);
+  a.gu = static_cast<const uint16_t *>(gu_bf16);
+  return device_status(quads::launch_gated_backward(a, static_cast<hipStream_t>(stream)), "gated_backward");
+}
+
 }  // extern "C"

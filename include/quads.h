@@ -416,6 +416,130 @@ quads_status_t quads_moe_wgrad_bf16(const void *dy_bf16, const void *x_bf16, con
 quads_status_t quads_transpose_bf16(const void *in_bf16, int64_t batch, int64_t rows, int64_t cols,
                                     void *out_bf16, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * MXFP4: the 4-bit format that the gfx950 matrix cores multiply as stored.
+ * OCP Microscaling encoding: blocks of 32 elements along the last axis share
+ * one E8M0 scale byte (2^(byte - 127); 255 is NaN); elements are E2M1, packed
+ * as above (element 2j in the low nibble of byte j).  There is no tensor
+ * scale.  A block with largest magnitude a takes E = floor(log2 a) - 2,
+ * clamped to [-127, 125], and its elements the E2M1 value nearest to
+ * x * 2^-E, ties to the even code, saturating at 6; the sign of a zero is
+ * kept.  With QUADS_MX_SCALE_EVEN a is first rounded to E2M1's two
+ * significant bits (a >= 1.75 * 2^floor(log2 a) takes the next E), which
+ * saturates less.  A block of zeros gets byte 0.  Unlike the NVFP4 calls,
+ * NaN and infinities are defined: their block gets byte 255 and codes 0, so
+ * all its values are NaN, and every product it enters is NaN.
+ *
+ * cols is a multiple of 32.  rows == 0 writes nothing and takes NULL arrays.
+ * Each call is one kernel without a workspace, so calls on different streams
+ * and graph captures need nothing of each other.
+ *
+ * quads_quantize_mxfp4: x [batch, rows, cols] F32 or BF16, contiguous, into
+ * `out`.  quads_dequantize_mxfp4: the values q stands for, F32 or BF16 (exact
+ * where the type holds them: always for F32-normal magnitudes and for every
+ * tensor these calls write; larger external scales give infinities).
+ * quads_weight_qdq_mxfp4: bf16 masters to the bf16 values of their MXFP4
+ * encoding (the weights a quantization-aware forward sees), and with q_out
+ * the encoding itself, equal to quads_quantize_mxfp4's.
+ * ------------------------------------------------------------------------- */
+#define QUADS_MX_SCALE_EVEN 8u
+
+typedef struct {
+  uint8_t *codes;  /* [batch, rows, cols/2] */
+  uint8_t *scales; /* [batch, rows, cols/32] E8M0 */
+  int64_t batch, rows, cols;
+} quads_mxfp4_t;
+
+quads_status_t quads_quantize_mxfp4(const void *x, quads_dtype_t dt, quads_mxfp4_t out, uint32_t flags, void *stream);
+quads_status_t quads_dequantize_mxfp4(quads_mxfp4_t q, void *out, quads_dtype_t dt, void *stream);
+quads_status_t quads_weight_qdq_mxfp4(const void *w_bf16, int64_t batch, int64_t rows, int64_t cols, void *w_out_bf16,
+                                      const quads_mxfp4_t *q_out, uint32_t flags, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * quads_moe_mxfp4_gemm -- grouped expert product of MXFP4 operands on the
+ * scaled matrix instructions, with quads_moe_w4a4_gemm's grouping:
+ *   Y[i, n] = sum_k W[e(i), n, k] X[t(i), k],   fp32 accumulation,
+ * for expert_offsets[e] <= i < expert_offsets[e + 1], t(i) = row_token[i] (or
+ * i when NULL).  y_dtype / epilogue:
+ *   EPI_NONE, QUADS_F32 or QUADS_BF16: y [num_rows, N];
+ *   EPI_SWIGLU (W rows [0, N/2) gate, [N/2, N) up), h = silu(Y_gate) * Y_up:
+ *     QUADS_BF16: y = h [num_rows, N/2]; QUADS_MXFP4: y = h's codes
+ *     [num_rows, N/4] and y_scales [num_rows, N/64], quantized from the fp32 h
+ *     (floor rule) while it is in registers: the next product's operand.
+ * K % 32 == 0; N % 32 == 0, N % 64 == 0 with EPI_SWIGLU; N, K < 2^24;
+ * num_experts in [1, 1024].  expert_offsets (device, not read by the host) is
+ * non-decreasing from 0 and ends at or below num_rows: rows behind it are
+ * left as they were.  row_token values are below act_rows.  Arrays are 16-byte
+ * aligned.  num_rows == 0: nothing is launched and y, x may be NULL.
+ * The order of every sum is fixed: repeated calls give the same bits.
+ *
+ * quads_moe_mxfp4_ffn -- the gated expert block from bf16 activations:
+ * quantizes x [act_rows, hidden] once, then the gate/up product with SwiGLU
+ * and requantization over w_gate_up [E, 2 inter, hidden], then the down
+ * product over w_down [E, hidden, inter] into y [num_rows, hidden] (F32 or
+ * BF16), one routed row each (quads_moe_combine sums F32 rows to tokens).
+ * The same bits as the three calls.  hidden % 32 == 0, inter % 32 == 0.
+ * ws: quads_moe_mxfp4_ffn_workspace_bytes(act_rows, num_rows, hidden, inter)
+ * bytes (both quantized activations); calls in flight at the same time need
+ * a workspace each.
+ * ------------------------------------------------------------------------- */
+#define QUADS_MXFP4 2 /* quads_moe_mxfp4_args.y_dtype */
+
+typedef struct {
+  uint32_t struct_size; /* sizeof(quads_moe_mxfp4_args) */
+  uint32_t flags;       /* 0 */
+  int32_t epilogue;     /* QUADS_EPI_NONE | QUADS_EPI_SWIGLU */
+  int32_t y_dtype;      /* QUADS_F32 | QUADS_BF16 | QUADS_MXFP4 */
+  int32_t num_experts;
+  int32_t reserved;     /* 0 */
+  int64_t num_rows, act_rows, N, K;
+  const uint8_t *x_codes, *x_scales; /* [act_rows, K/2], [act_rows, K/32] */
+  const uint8_t *w_codes, *w_scales; /* [E, N, K/2], [E, N, K/32] */
+  const int32_t *row_token;          /* [num_rows] or NULL */
+  const int32_t *expert_offsets;     /* [E + 1] */
+  void *y;
+  uint8_t *y_scales;                 /* QUADS_MXFP4 only */
+} quads_moe_mxfp4_args;
+
+quads_status_t quads_moe_mxfp4_gemm(const quads_moe_mxfp4_args *a, void *stream);
+
+size_t quads_moe_mxfp4_ffn_workspace_bytes(int64_t act_rows, int64_t num_rows, int64_t hidden, int64_t inter);
+quads_status_t quads_moe_mxfp4_ffn(const void *x_bf16, const quads_mxfp4_t *w_gate_up, const quads_mxfp4_t *w_down,
+                                   const int32_t *row_token, const int32_t *expert_offsets, int32_t num_experts,
+                                   int64_t num_rows, int64_t act_rows, int64_t hidden, int64_t inter, void *y,
+                                   quads_dtype_t y_dtype, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The trainer's gated block in bf16, differentiable.  With W_gate_up [E, 2
+ * inter, hidden] (gate rows, then up rows) as the forward sees it (bf16
+ * masters or their QDQ values; the gradient passes the QDQ unchanged):
+ *
+ * quads_moe_gated_forward_bf16: for routed row i of expert e
+ *   [g | u] = W_gate_up[e] x[t(i)]  (fp32 accumulation),  h = silu(g) u,
+ * h [num_rows, inter] bf16 rounded once from fp32; gu [num_rows, 2 inter]
+ * bf16 receives g and u for the backward (NULL: not kept).
+ *
+ * quads_moe_gated_backward_bf16: from dy [num_rows, hidden] bf16, the gradient
+ * of y[i] = W_down[e] h[i] (W_down [E, hidden, inter]),
+ *   dh = W_down[e]^T dy[i],  s = 1 / (1 + e^-g),
+ *   d u = dh g s,   d g = dh u s (1 + g (1 - s)),
+ * written as dgu [num_rows, 2 inter] bf16, each rounded once; dh itself is
+ * never stored and the transposed weights are never formed.  dgu may be gu.
+ * The remaining gradients are existing calls: dW_gate_up =
+ * quads_moe_wgrad_bf16(dgu, x), dW_down = quads_moe_wgrad_bf16(dy, h), dx by
+ * the bf16-operand GEMM of dgu over W_gate_up^T.
+ *
+ * hidden and inter are multiples of 16, below 2^24.  Grouping, alignment,
+ * empty calls and rows behind the last expert as in quads_moe_mxfp4_gemm.
+ * ------------------------------------------------------------------------- */
+quads_status_t quads_moe_gated_forward_bf16(const void *x_bf16, const void *w_gate_up_bf16, const int32_t *row_token,
+                                            const int32_t *expert_offsets, int32_t num_experts, int64_t num_rows,
+                                            int64_t act_rows, int64_t hidden, int64_t inter, void *h_bf16,
+                                            void *gu_bf16, void *stream);
+quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_down_bf16, const void *gu_bf16,
+                                             const int32_t *expert_offsets, int32_t num_experts, int64_t num_rows,
+                                             int64_t hidden, int64_t inter, void *dgu_bf16, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

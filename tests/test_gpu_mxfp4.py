@@ -1,0 +1,352 @@
+"""MXFP4 quantizer, grouped product and gated expert block on the GPU against
+the 64-bit oracle.
+
+Tolerances.  A product of two MXFP4 values is exact in fp32, so an fp32 output
+is off by its K - 1 additions alone: at most K 2^-24 sum |w x| to first order,
+whatever their order.  A bf16 store adds half a step, 2^-8 |y|.  silu is a few
+fp32 ulp (2^-21 here), and |silu'| <= 1.1."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from fp4_quantized_moe_amd import _lib as Q
+from oracle import mxfp4_oracle as M
+from gpu_util import host
+
+pytestmark = pytest.mark.gpu
+
+
+def bf16(x):
+    return torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(torch.bfloat16)
+
+
+def check_codes(q, x, rule):
+    codes, scales = M.quantize(x, rule)
+    assert np.array_equal(host(q.scales).reshape(scales.shape), scales)
+    assert np.array_equal(M.unpack(host(q.codes)).reshape(codes.shape), codes)
+
+
+# ---- codec -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("rule", ["floor", "even"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", [(1, 32), (3, 96), (257, 2048), (5, 7, 160), (33, 4128)])
+def test_quantize(shape, dtype, rule):
+    gen = torch.Generator().manual_seed(sum(shape))
+    x = (torch.randn(shape, generator=gen) * torch.exp2(torch.randint(-30, 30, (*shape[:-1], 1), generator=gen))).to(dtype)
+    x[..., 5] = 0.0
+    x[..., 6] = -0.0
+    q = Q.quantize_mxfp4(x.cuda(), rule=rule)
+    check_codes(q, x.double().numpy(), rule)
+    values = M.dequantize(*M.quantize(x.double().numpy(), rule))
+    for t in (torch.bfloat16, torch.float32):
+        assert np.array_equal(host(Q.dequantize_mxfp4(q, t).double()), values)
+
+
+@pytest.mark.parametrize("rule", ["floor", "even"])
+def test_every_bf16_magnitude(rule):
+    """Every finite bf16 pattern as an element under every block exponent that it can meet near the
+    rounding points, and as the block's largest value."""
+    bits = torch.arange(0, 0x7F80, dtype=torch.int32)
+    v = bits.to(torch.int16).view(torch.bfloat16)
+    n = v.numel()
+    blocks = torch.zeros(2 * n, 32, dtype=torch.bfloat16)
+    blocks[:n, 0], blocks[:n, 1] = v, -v  # alone: the largest
+    for k in range(7):  # below a larger value of the same block
+        up = (v.double() * 2.0 ** k).clamp(max=3e38).to(torch.bfloat16)
+        blocks[n:, 4 * k], blocks[n:, 4 * k + 1] = v, -v
+        if k == 3:
+            blocks[n:, 31] = up
+    q = Q.quantize_mxfp4(blocks.cuda(), rule=rule)
+    check_codes(q, blocks.double().numpy(), rule)
+
+
+def test_fp32_rounding_points():
+    """Values one fp32 step on either side of each rounding point and of each scale border."""
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 8.0], np.float32)
+    rows = []
+    for e in (-126, -125, -124, -60, 0, 50, 124):
+        for top in (4.0, 6.99999, 7.0, 7.99999):
+            x = np.zeros(32, np.float32)
+            pts = np.ldexp(mids[:7], e - 2).astype(np.float32)
+            x[:7], x[7:14], x[14:21] = pts, np.nextafter(pts, np.float32(0)), np.nextafter(pts, np.float32(1e38))
+            x[21:28] = -pts
+            x[31] = np.ldexp(np.float32(top), e - 2)
+            rows.append(x)
+    x = np.stack(rows)
+    for rule in ("floor", "even"):
+        check_codes(Q.quantize_mxfp4(torch.from_numpy(x).cuda(), rule=rule), x.astype(np.float64), rule)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_nan_inf(dtype):
+    x = torch.randn(6, 96, generator=torch.Generator().manual_seed(0)).to(dtype)
+    x[0, 3], x[1, 40], x[2, 95], x[3, 0] = float("nan"), float("inf"), -float("inf"), -float("nan")
+    q = Q.quantize_mxfp4(x.cuda())
+    check_codes(q, x.double().numpy(), "floor")
+    d = host(Q.dequantize_mxfp4(q, torch.float32))
+    bad = np.zeros((6, 3), bool)
+    bad[0, 0] = bad[1, 1] = bad[2, 2] = bad[3, 0] = True
+    assert np.array_equal(np.isnan(d), np.repeat(bad, 32, 1))
+
+
+def test_dequantize_every_scale():
+    """Every scale byte times every code: exact in fp32 (2^127 * 6 overflows to inf, as rounding does)."""
+    scales = torch.arange(256, dtype=torch.uint8)[:, None]
+    codes = torch.from_numpy(M.pack(np.tile(np.arange(16, dtype=np.uint8), (256, 2))))
+    q = Q.mxfp4_tensor(codes.cuda(), scales.cuda())
+    want = M.dequantize(M.unpack(codes.numpy()), scales.numpy())
+    with np.errstate(over="ignore"):
+        want32 = want.astype(np.float32)
+    assert np.array_equal(host(Q.dequantize_mxfp4(q, torch.float32)), want32, equal_nan=True)
+    got = host(Q.dequantize_mxfp4(q, torch.bfloat16).float())
+    assert np.array_equal(got, torch.from_numpy(want32).to(torch.bfloat16).float().numpy(), equal_nan=True)
+
+
+@pytest.mark.parametrize("rule", ["floor", "even"])
+@pytest.mark.parametrize("shape", [(1, 32), (130, 800), (3, 40, 256)])
+def test_weight_qdq(shape, rule):
+    w = (torch.randn(shape, generator=torch.Generator().manual_seed(1)) * 0.02).to(torch.bfloat16).cuda()
+    out, q = Q.weight_qdq_mxfp4(w, rule=rule, export=True)
+    want = Q.quantize_mxfp4(w, rule=rule)
+    assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
+    assert torch.equal(out, Q.dequantize_mxfp4(want))
+    assert torch.equal(Q.weight_qdq_mxfp4(w, rule=rule)[0], out)
+    keep = w.clone()
+    Q.weight_qdq_mxfp4(w, rule=rule, out=w)  # in place
+    assert torch.equal(w, out) and not torch.equal(keep, out)
+
+
+def test_no_rows():
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    q = Q.quantize_mxfp4(x)
+    assert q.codes.shape == (0, 32) and Q.dequantize_mxfp4(q).shape == (0, 64)
+    assert Q.weight_qdq_mxfp4(x)[0].shape == (0, 64)
+
+
+# ---- grouped product --------------------------------------------------------------
+
+def make(seed, counts, N, K, gather=True, act_rows=None):
+    """Random operands with the given rows per expert."""
+    rng = np.random.default_rng(seed)
+    offsets = np.concatenate(([0], np.cumsum(counts))).astype(np.int32)
+    R = int(offsets[-1])
+    A = act_rows or (max(1, R // 2) if gather else R)
+    token = rng.integers(0, A, R).astype(np.int32) if gather else None
+    x = rng.standard_normal((A, K)) * np.where(rng.random(K) < 0.02, 30, 1)
+    w = rng.standard_normal((len(counts), N, K)) * 0.02
+    xc, xs = M.quantize(x)
+    wc, ws = M.quantize(w)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    return {"x": M.dequantize(xc, xs), "w": M.dequantize(wc, ws), "offsets": offsets, "token": token,
+            "xq": Q.mxfp4_tensor(dev(M.pack(xc)), dev(xs)),
+            "wq": Q.mxfp4_tensor(dev(M.pack(wc)), dev(ws)),
+            "do": dev(offsets), "dt": dev(token) if gather else None}
+
+
+def reference(d):
+    y = M.grouped(d["x"], d["w"], d["offsets"], d["token"])
+    tol = d["x"].shape[1] * 2.0 ** -24 * M.grouped(d["x"], d["w"], d["offsets"], d["token"], magnitude=True)
+    return y, tol
+
+
+# rows per expert; N; K: single tokens, empty experts, odd sizes, whole tiles, long contractions
+SHAPES = [
+    ([1], 32, 32), ([1], 128, 256), ([0, 1, 0], 64, 96), ([3, 0, 2], 96, 160), ([64], 512, 256),
+    ([33, 0, 31, 1], 160, 1056), ([17] * 9, 256, 512), ([130, 5, 0, 257], 192, 384), ([300], 320, 128),
+    ([512, 255, 1], 512, 768), ([700, 30], 544, 1024), ([40] * 3, 64, 8192), ([1, 2, 0, 4], 2048, 2048),
+    ([16] * 70, 128, 256), ([2048], 256, 640),
+]
+
+
+@pytest.mark.parametrize("counts, N, K", SHAPES)
+def test_gemm(counts, N, K):
+    d = make(N + K, counts, N, K)
+    want, tol = reference(d)
+    y = Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"], d["dt"])
+    assert (np.abs(host(y) - want) <= tol).all()
+    yb = Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"], d["dt"], y_dtype=torch.bfloat16)
+    assert torch.equal(yb, y.to(torch.bfloat16))  # the same sums, rounded once
+    assert torch.equal(Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"], d["dt"]), y)
+
+
+@pytest.mark.parametrize("counts, N, K", [([5, 0, 40], 96, 96), ([300, 7], 256, 256)])
+def test_gemm_identity_rows(counts, N, K):
+    d = make(3, counts, N, K, gather=False)
+    want, tol = reference(d)
+    assert (np.abs(host(Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"])) - want) <= tol).all()
+
+
+def check_h(codes, scales, h, err):
+    """The bytes must be a quantization of values within err of h: the scale between those of the
+    largest magnitude -+ err, each code between the codes of h -+ err under that scale."""
+    lo_s = M.block_bytes((np.abs(h) - err).clip(0).reshape(*scales.shape, 32).max(-1))
+    hi_s = M.block_bytes((np.abs(h) + err).reshape(*scales.shape, 32).max(-1))
+    assert ((scales >= lo_s) & (scales <= hi_s)).all()
+    v = M.dequantize(codes, scales)
+    lo = M.dequantize(*M.quantize(h - err, scales=scales))
+    hi = M.dequantize(*M.quantize(h + err, scales=scales))
+    assert ((v >= lo) & (v <= hi)).all()
+    return float(np.mean(lo != hi))
+
+
+def swiglu_reference(d):
+    gu, tol = reference(d)
+    h = M.gated(gu)
+    g, u = np.split(gu, 2, 1)
+    tg, tu = np.split(tol, 2, 1)
+    return h, 1.1 * tg * (np.abs(u) + tu) + np.abs(M.silu(g)) * tu + 2.0 ** -21 * np.abs(h)
+
+
+@pytest.mark.parametrize("counts, N, K", [s for s in SHAPES if s[1] % 64 == 0])
+def test_swiglu(counts, N, K):
+    d = make(N + K + 1, counts, N, K)
+    h, err = swiglu_reference(d)
+    y = Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"], d["dt"], epilogue=Q.EPI_SWIGLU, y_dtype=torch.bfloat16)
+    assert (np.abs(host(y.double()) - h) <= err + 2.0 ** -8 * np.abs(h) + 2.0 ** -133).all()
+    q = Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"], d["dt"], epilogue=Q.EPI_SWIGLU, y_dtype=Q.MXFP4)
+    open_codes = check_h(M.unpack(host(q.codes)), host(q.scales), h, err)
+    # The check pins nearly every code: sum |w x| / |y| is about sqrt(2 K / pi) for random signs, so err / |h| is about
+    # d = K 2^-24 sqrt(2 K / pi) from each of g and u, and the rounding points lie about a third of a value apart: a
+    # code is open for a share of 2 * 2 d * 3 (0.0006 at K = 256, 0.42 at the longest contraction here, 8192).
+    assert open_codes < 12 * K * 2.0 ** -24 * (2 * K / np.pi) ** 0.5 + 0.005
+
+
+def test_rows_behind_the_last_expert_stay():
+    d = make(7, [20, 0, 13], 128, 256, gather=True)
+    token = torch.cat((d["dt"], d["dt"][:9]))
+    y = torch.full((42, 128), 7.0, device="cuda")
+    Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"], token, y=y)
+    want, tol = reference(d)
+    assert (np.abs(host(y[:33]) - want) <= tol).all()
+    assert bool((y[33:] == 7.0).all())
+    q = Q.empty_mxfp4(1, 42, 64, "cuda")
+    q.codes.fill_(0xAB)
+    q.scales.fill_(0xCD)
+    Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"], token, epilogue=Q.EPI_SWIGLU, y_dtype=Q.MXFP4, y=q)
+    assert bool((q.codes[33:] == 0xAB).all()) and bool((q.scales[33:] == 0xCD).all())
+
+
+@pytest.mark.parametrize("K", [96, 256])
+def test_nan_reaches_its_rows_alone(K):
+    """A NaN block of one activation row makes that row NaN; one of a weight row that column."""
+    d = make(9, [40], 128, K, gather=False)
+    d["xq"].scales[11, K // 32 - 1] = 255
+    d["wq"].scales[0, 50, 0] = 255
+    y = host(Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"]))
+    want, tol = reference(d)
+    nan = np.zeros((40, 128), bool)
+    nan[11], nan[:, 50] = True, True
+    assert np.array_equal(np.isnan(y), nan)
+    assert (np.abs(y - want)[~nan] <= tol[~nan]).all()
+    # gate column 50 lies in the second block of h
+    q = Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"], epilogue=Q.EPI_SWIGLU, y_dtype=Q.MXFP4)
+    s = host(q.scales)
+    assert np.array_equal(s == 255, np.stack((np.arange(40) == 11, np.ones(40, bool)), 1))
+    assert (host(q.codes)[np.repeat(s == 255, 16, 1)] == 0).all()
+
+
+@pytest.mark.parametrize("ex, ew", [(-100, -100), (90, 30), (-120, 120)])
+def test_extreme_scales(ex, ew):
+    """Scales far from 1: results on fp32's range, underflow to zero, no NaN."""
+    d = make(12, [33], 64, 256, gather=False)
+    d["xq"].scales.copy_((d["xq"].scales.int() + ex).clamp(0, 254).to(torch.uint8))
+    d["wq"].scales.copy_((d["wq"].scales.int() + ew).clamp(0, 254).to(torch.uint8))
+    x = M.dequantize(M.unpack(host(d["xq"].codes)), host(d["xq"].scales))
+    w = M.dequantize(M.unpack(host(d["wq"].codes)), host(d["wq"].scales))
+    want = x @ w[0].T if w.ndim == 3 else x @ w.T
+    tol = 256 * 2.0 ** -24 * (np.abs(x) @ np.abs(w.reshape(64, 256)).T) + 256 * 2.0 ** -126
+    assert (np.abs(host(Q.moe_mxfp4_gemm(d["xq"], d["wq"], d["do"])) - want) <= tol).all()
+
+
+# ---- the gated block ---------------------------------------------------------------
+
+def ffn_operands(seed, counts, H, I, act_rows=None):
+    rng = np.random.default_rng(seed)
+    offsets = np.concatenate(([0], np.cumsum(counts))).astype(np.int32)
+    R, E = int(offsets[-1]), len(counts)
+    A = act_rows or max(1, R // 2)
+    x = bf16(rng.standard_normal((A, H))).cuda()
+    wg = Q.quantize_mxfp4(bf16(rng.standard_normal((E, 2 * I, H)) * 0.05).cuda())
+    wd = Q.quantize_mxfp4(bf16(rng.standard_normal((E, H, I)) * 0.05).cuda())
+    token = torch.from_numpy(rng.integers(0, A, R).astype(np.int32)).cuda()
+    return x, wg, wd, torch.from_numpy(offsets).cuda(), token
+
+
+@pytest.mark.parametrize("counts, H, I", [([1], 64, 32), ([2, 0, 5, 1], 256, 128), ([70, 0, 200], 416, 96),
+                                          ([300, 513], 512, 256), ([9] * 20, 1024, 384)])
+def test_ffn_is_its_three_calls(counts, H, I):
+    x, wg, wd, offs, token = ffn_operands(H, counts, H, I)
+    h = Q.moe_mxfp4_gemm(Q.quantize_mxfp4(x), wg, offs, token, epilogue=Q.EPI_SWIGLU, y_dtype=Q.MXFP4)
+    for t in (torch.float32, torch.bfloat16):
+        want = Q.moe_mxfp4_gemm(h, wd, offs, y_dtype=t)
+        assert torch.equal(Q.moe_mxfp4_ffn(x, wg, wd, offs, token, y_dtype=t), want)
+    # against the oracle from the GPU's own h on, whose codes test_swiglu pins
+    hv = M.dequantize(M.unpack(host(h.codes)), host(h.scales))
+    wv = M.dequantize(M.unpack(host(wd.codes)), host(wd.scales)).reshape(len(counts), H, I)
+    o = host(offs)
+    tol = I * 2.0 ** -24 * M.grouped(hv, wv, o, magnitude=True)
+    assert (np.abs(host(Q.moe_mxfp4_ffn(x, wg, wd, offs, token)) - M.grouped(hv, wv, o)) <= tol).all()
+
+
+def test_layer_route_to_combine():
+    """The MoE layer as it is served: route, the gated block, combine."""
+    rng = np.random.default_rng(5)
+    T, E, top, H, I = 50, 8, 2, 256, 128
+    logits = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).cuda()
+    ids, wt, offs, token, inv = Q.moe_route(logits, top)
+    x, wg, wd, _, _ = ffn_operands(6, [1] * E, H, I, act_rows=T)
+    y = Q.moe_mxfp4_ffn(x, wg, wd, offs, token)
+    out = Q.moe_combine(y, inv, wt)
+    assert out.shape == (T, H)
+    rows, w, at = host(y).astype(np.float64), host(wt).astype(np.float64), host(inv)
+    want = (rows[at] * w[..., None]).sum(1)
+    assert (np.abs(host(out) - want) <= 2 * 2.0 ** -24 * (np.abs(rows[at]) * w[..., None]).sum(1) + 1e-30).all()
+    # each routed row is the block of its own expert alone
+    e = int(ids[3, 1])
+    one = Q.moe_mxfp4_ffn(x[3:4].contiguous(), Q.mxfp4_tensor(wg.codes[e], wg.scales[e]),
+                          Q.mxfp4_tensor(wd.codes[e], wd.scales[e]),
+                          torch.tensor([0, 1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(one[0], y[int(inv[3, 1])])
+
+
+def test_graph_and_streams():
+    """A captured block replayed between eager calls on another stream, each with its own workspace."""
+    x, wg, wd, offs, token = ffn_operands(8, [30, 0, 90], 256, 128)
+    want = Q.moe_mxfp4_ffn(x, wg, wd, offs, token)
+    ws = torch.empty(Q.mxfp4_ffn_workspace_bytes(x.shape[0], 120, 256, 128), dtype=torch.uint8, device="cuda")
+    y = torch.empty_like(want)
+    x2 = (x.float() * 0.5).to(torch.bfloat16)
+    want2 = Q.moe_mxfp4_ffn(x2, wg, wd, offs, token)
+    buf = x.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        Q.moe_mxfp4_ffn(buf, wg, wd, offs, token, y=y, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Q.moe_mxfp4_ffn(buf, wg, wd, offs, token, y=y, ws=ws)
+    for src, w in ((x, want), (x2, want2), (x, want), (x2, want2)):
+        buf.copy_(src)
+        y.zero_()
+        graph.replay()
+        assert torch.equal(Q.moe_mxfp4_ffn(src, wg, wd, offs, token), w)
+        torch.cuda.synchronize()
+        assert torch.equal(y, w)
+
+
+def test_empty_calls():
+    x, wg, wd, _, _ = ffn_operands(8, [2, 1], 64, 32)
+    offs = torch.zeros(3, dtype=torch.int32, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert Q.moe_mxfp4_ffn(x, wg, wd, offs, none).shape == (0, 64)
+    assert Q.moe_mxfp4_gemm(Q.quantize_mxfp4(x), wg, offs, none).shape == (0, 64)
+
+
+def test_short_workspace_is_refused():
+    x, wg, wd, offs, token = ffn_operands(8, [2, 1], 64, 32)
+    with pytest.raises(Q.QuadsError, match="workspace"):
+        Q.moe_mxfp4_ffn(x, wg, wd, offs, token, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
