@@ -5,7 +5,7 @@
 // The forward keeps [g | u] in bf16 (288 GB of HBM hold them; recomputing the
 // projection would cost twice the backward's own product).  dh exists in the
 // accumulators only: the backward's epilogue reads g and u and writes d g, d u.
-#include "grouped_direct.hpp"
+#include "grouped_staged.hpp"
 #include "launch.hpp"
 
 namespace quads {
@@ -34,6 +34,10 @@ GroupedParams params(const GatedLaunch &a, bool backward) {
 
 hipError_t launch_gated_forward(const GatedLaunch &a, hipStream_t stream) {
   if (a.R == 0) return hipSuccess;
+  if (a.R >= 128 * a.E)
+    return launch_staged<StagedCfg<kOpBf16, 256, 256, 2, 2>, kEpiSwiglu>(params(a, false), a.R, stream);
+  if (a.R > 16 * a.E)
+    return launch_staged<StagedCfg<kOpBf16, 128, 128, 2, 2>, kEpiSwiglu>(params(a, false), a.R, stream);
   return launch_direct<kOpBf16, kEpiSwiglu>(params(a, false), a.R, stream);
 }
 

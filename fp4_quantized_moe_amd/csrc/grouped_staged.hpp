@@ -1,0 +1,223 @@
+// LDS-staged grouped GEMM for MXFP4 and bf16 operands whose contraction runs
+// along both operands' rows (weights [E, N, K]).
+//
+// A stage is 128 bytes of K (256 MXFP4 or 64 bf16 elements) of TN weight and
+// TM routed rows; two stages in LDS.  128 bytes are one cache line, so every
+// staging instruction reads whole lines (8 rows of 8 chunks).  Row r keeps its
+// chunk c in slot c ^ (r % 8): the 8 rows a fragment read touches together
+// then lie in 8 different 16-byte bank groups, and the permutation is applied
+// to the source address of the DMA, within the line.
+//
+// One stage is four MFMA steps; in step s lanes 0-31 contract chunk s and
+// lanes 32-63 chunk 4 + s, so a lane's four MXFP4 block scales of the stage
+// are one dword, whose byte s the matrix instruction selects.
+//
+// Pipeline: step s + 1's fragments are read while step s is multiplied.  The
+// last step of a stage is held back: its fragments are in registers, so after
+// one barrier the stage's LDS is free (the DMA of the next but one stage
+// starts) and the next stage has landed (its first fragments are read under
+// the held-back step's MFMAs).  One barrier a stage, no exposed LDS latency.
+#pragma once
+
+#include <type_traits>
+
+#include "dma.hpp"
+#include "grouped_direct.hpp"
+
+namespace quads {
+
+// Zeros that the staging reads in the place of chunks and scales behind K.
+__device__ __attribute__((aligned(16))) uint32_t g_zero_chunk[4];
+
+template <int OP_, int TM_, int TN_, int WM_, int WN_>
+struct StagedCfg {
+  static constexpr int OP = OP_, TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+  static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+  static constexpr int MI = TM / WM / 32, NI = TN / WN / 32;  // 32 x 32 tiles of a wave
+  static constexpr int ROWS = TM + TN;
+  static constexpr int LOADS = ROWS / 8 / WAVES;       // staging instructions of a wave and stage
+  static constexpr int WLOADS = TN / 8 / WAVES;        // the weights' part of them
+  static constexpr bool MX = OP == kOpMx;
+  static constexpr int SLOADS = MX ? ROWS / 32 / WAVES : 0;  // scale instructions (32 rows each)
+  static constexpr int STAGE = ROWS * 128 + (MX ? ROWS * 8 : 0);
+  static_assert(TN % (8 * WAVES) == 0 && TM % (8 * WAVES) == 0 && (!MX || ROWS % (32 * WAVES) == 0), "staging split");
+};
+
+template <class C, int EPI>
+__device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt &t, int32_t n0, uint8_t *lds) {
+  constexpr bool PAIR = EPI == kEpiSwiglu || EPI == kEpiSwigluMx;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+  const int wn = wave / C::WM, wm = wave % C::WM;
+
+  // Weight row of tile row r.  With a gate/up pair the first half of each
+  // wave's rows are gate columns, the second half the same up columns.
+  const auto weight_row = [&](int r) -> int64_t {
+    if constexpr (PAIR) {
+      constexpr int PER = C::TN / C::WN, HALF = PER / 2;
+      const int q = r % PER;
+      const int32_t col = min(n0 + (r / PER) * HALF + q % HALF, p.width - 1);
+      return col + (q >= HALF ? p.width : 0);
+    }
+    return min(n0 + r, p.N - 1);
+  };
+  const auto source = [&](int r) -> int64_t {
+    return source_row(p, t.r0 + min(r, t.rows - 1));
+  };
+
+  const uint8_t *from[C::LOADS];
+  const int lr = lane >> 3, chunk = (lane & 7) ^ (lr & 7);
+#pragma unroll
+  for (int j = 0; j < C::LOADS; ++j) {
+    if (j < C::WLOADS)
+      from[j] = p.w + t.e * p.w_expert + weight_row((j * C::WAVES + wave) * 8 + lr) * p.w_row + 16 * chunk;
+    else
+      from[j] = p.x + source(((j - C::WLOADS) * C::WAVES + wave) * 8 + lr) * p.x_row + 16 * chunk;
+  }
+  const uint8_t *sfrom[C::SLOADS + 1];
+#pragma unroll
+  for (int j = 0; j < C::SLOADS; ++j) {
+    const int r = (j * C::WAVES + wave) * 32 + (lane >> 1);
+    if (r < C::TN)
+      sfrom[j] = p.w_scales + (static_cast<int64_t>(t.e) * p.N + weight_row(r)) * p.chunks + 4 * (lane & 1);
+    else
+      sfrom[j] = p.x_scales + source(r - C::TN) * p.chunks + 4 * (lane & 1);
+  }
+
+  const int stages = (p.chunks + 7) / 8;
+  const auto fetch = [&](int s) {  // called once for each stage, in order
+    uint8_t *base = lds + (s & 1) * C::STAGE;
+    const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_chunk);
+    const bool in = 8 * s + chunk < p.chunks, sin = 8 * s + 4 * (lane & 1) < p.chunks;
+#pragma unroll
+    for (int j = 0; j < C::LOADS; ++j) {
+      dma(in ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
+      from[j] += 128;
+    }
+#pragma unroll
+    for (int j = 0; j < C::SLOADS; ++j) {
+      dma(sin ? sfrom[j] : zero, base + C::ROWS * 128 + (j * C::WAVES + wave) * 256, 4);
+      sfrom[j] += 8;
+    }
+  };
+
+  // Fragment addresses: row (lane % 32) of a 32-row group, chunk 4 half + s.
+  const int fr = lane & 31;
+  const int arow = wn * (C::TN / C::WN) + fr, brow = C::TN + wm * (C::TM / C::WM) + fr;
+  struct Frag {
+    uint4 a[C::NI], b[C::MI];
+  };
+  struct Scales {
+    uint32_t a[C::NI], b[C::MI];
+  };
+  const auto read = [&](Frag &f, const uint8_t *base, int s) {
+    const int slot = 16 * ((4 * half + s) ^ (fr & 7));
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) f.a[i] = *reinterpret_cast<const uint4 *>(base + (arow + 32 * i) * 128 + slot);
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i) f.b[i] = *reinterpret_cast<const uint4 *>(base + (brow + 32 * i) * 128 + slot);
+  };
+  const auto read_scales = [&](Scales &f, const uint8_t *base) {
+    if constexpr (C::MX) {
+      const uint8_t *sc = base + C::ROWS * 128 + 4 * half;
+#pragma unroll
+      for (int i = 0; i < C::NI; ++i) f.a[i] = *reinterpret_cast<const uint32_t *>(sc + (arow + 32 * i) * 8);
+#pragma unroll
+      for (int i = 0; i < C::MI; ++i) f.b[i] = *reinterpret_cast<const uint32_t *>(sc + (brow + 32 * i) * 8);
+    }
+  };
+
+  f32x16 acc[C::NI][C::MI];
+#pragma unroll
+  for (int i = 0; i < C::NI; ++i)
+#pragma unroll
+    for (int k = 0; k < C::MI; ++k) acc[i][k] = f32x16{};
+  Scales sc;
+  const auto multiply = [&](const Frag &f, auto step) {
+    constexpr int S = decltype(step)::value;
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i)
+#pragma unroll
+      for (int k = 0; k < C::MI; ++k) {
+        if constexpr (C::MX)
+          acc[i][k] = mfma_mx<S>(f.a[i], f.b[k], acc[i][k], sc.a[i], sc.b[k]);
+        else
+          acc[i][k] = mfma_bf16(f.a[i], f.b[k], acc[i][k]);
+      }
+  };
+  const auto c0 = std::integral_constant<int, 0>{};
+  const auto c1 = std::integral_constant<int, 1>{};
+  const auto c2 = std::integral_constant<int, 2>{};
+  const auto c3 = std::integral_constant<int, 3>{};
+
+  // Stages behind the last are fetched as zeros into LDS that no one reads
+  // again: the loop has no branches (with them the compiler keeps a second
+  // copy of the accumulators).
+  fetch(0);
+  fetch(1);
+  wait_vm<C::LOADS + C::SLOADS>();
+  barrier_no_fence();
+  Frag f0, f1;
+  read(f0, lds, 0);
+  read_scales(sc, lds);
+  for (int s = 0; s < stages; ++s) {
+    const uint8_t *cur = lds + (s & 1) * C::STAGE, *nxt = lds + ((s + 1) & 1) * C::STAGE;
+    read(f1, cur, 1);
+    multiply(f0, c0);
+    __builtin_amdgcn_sched_barrier(0);  // keep one step's fragments in flight, not the whole stage's
+    read(f0, cur, 2);
+    multiply(f1, c1);
+    __builtin_amdgcn_sched_barrier(0);
+    read(f1, cur, 3);
+    multiply(f0, c2);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_lgkm0();  // step 3's fragments are in registers: this wave is done with the stage's LDS
+    wait_vm<0>();  // and its part of the next stage has landed
+    barrier_no_fence();
+    fetch(s + 2);
+    Scales next;
+    read(f0, nxt, 0);
+    read_scales(next, nxt);
+    multiply(f1, c3);
+    sc = next;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  wait_vm<0>();
+
+  constexpr int PAIRS = PAIR ? C::NI / 2 : C::NI;
+#pragma unroll
+  for (int k = 0; k < C::MI; ++k) {
+    const int32_t m = wm * (C::TM / C::WM) + 32 * k + fr;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i)
+      store_tile<EPI>(p, acc[i][k], acc[PAIR ? i + PAIRS : i][k], static_cast<int64_t>(t.r0) + m, m < t.rows,
+                      n0 + (wn * PAIRS + i) * 32);
+  }
+}
+
+// One tile a workgroup.  Dispatch is round-robin over the 8 XCDs; each XCD
+// takes a contiguous eighth of the tiles (columns fastest), so the tiles that
+// share an expert's weights and a row tile's activations share an L2.
+template <class C, int EPI>
+__global__ __launch_bounds__(C::THREADS, 1) void k_grouped_staged(GroupedParams p, int col_tiles) {
+  __shared__ __attribute__((aligned(128))) uint8_t lds[2 * C::STAGE];
+  const TileAt all = find_tile<C::TM>(p.offsets, p.E, 0x7FFFFFFF);
+  const int64_t tiles = static_cast<int64_t>(all.total) * col_tiles, per = (tiles + 7) / 8;
+  const int64_t at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per || at >= tiles) return;
+  const TileAt t = find_tile<C::TM>(p.offsets, p.E, static_cast<int>(at / col_tiles));
+  constexpr int COLS = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? C::TN / 2 : C::TN;
+  staged_tile<C, EPI>(p, t, static_cast<int32_t>(at % col_tiles) * COLS, lds);
+}
+
+template <class C, int EPI>
+hipError_t launch_staged(const GroupedParams &p, int64_t R, hipStream_t stream) {
+  constexpr int COLS = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? C::TN / 2 : C::TN;
+  const int64_t cols = (p.width + COLS - 1) / COLS;
+  const int64_t grid = (max_row_tiles(R, p.E, C::TM) * cols + 7) / 8 * 8;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((k_grouped_staged<C, EPI>), dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), 0, stream, p,
+                     static_cast<int>(cols));
+  return hipGetLastError();
+}
+
+}  // namespace quads

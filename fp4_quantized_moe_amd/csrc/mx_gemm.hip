@@ -2,7 +2,7 @@
 //   Y[i, n] = sum_k W[e(i), n, k] X[t(i), k],  W and X e2m1 * 2^E in blocks of 32.
 // v_mfma_scale_f32_32x32x64_f8f6f4 multiplies the codes as stored, scales each
 // 32-element block product by 2^(E_w + E_x) and accumulates in fp32.
-#include "grouped_direct.hpp"
+#include "grouped_staged.hpp"
 #include "launch.hpp"
 
 namespace quads {
@@ -30,6 +30,11 @@ GroupedParams params(const MxGemmLaunch &a) {
 template <int EPI>
 hipError_t run(const MxGemmLaunch &a, hipStream_t stream) {
   const GroupedParams p = params(a);
+  // The staged kernel reads scales by dwords: K % 128.
+  if (a.K % 128 == 0 && a.R > 16 * a.E) {
+    if (a.R >= 128 * a.E) return launch_staged<StagedCfg<kOpMx, 256, 256, 2, 2>, EPI>(p, a.R, stream);
+    return launch_staged<StagedCfg<kOpMx, 128, 128, 2, 2>, EPI>(p, a.R, stream);
+  }
   return launch_direct<kOpMx, EPI>(p, a.R, stream);
 }
 
