@@ -43,6 +43,10 @@ hipError_t launch_gated_forward(const GatedLaunch &a, hipStream_t stream) {
 
 hipError_t launch_gated_backward(const GatedLaunch &a, hipStream_t stream) {
   if (a.R == 0) return hipSuccess;
+  if (a.R >= 128 * a.E)
+    return launch_staged<StagedCfg<kOpBf16T, 256, 256, 2, 2>, kEpiGatedBwd>(params(a, true), a.R, stream);
+  if (a.R > 16 * a.E)
+    return launch_staged<StagedCfg<kOpBf16T, 128, 128, 2, 2>, kEpiGatedBwd>(params(a, true), a.R, stream);
   return launch_direct<kOpBf16T, kEpiGatedBwd>(params(a, true), a.R, stream);
 }
 

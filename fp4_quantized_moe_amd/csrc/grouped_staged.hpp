@@ -1,5 +1,6 @@
-// LDS-staged grouped GEMM for MXFP4 and bf16 operands whose contraction runs
-// along both operands' rows (weights [E, N, K]).
+// LDS-staged grouped GEMM for MXFP4 and bf16 operands.  The contraction runs
+// along the rows of the routed operand and along the weights' rows (weights
+// [E, N, K]) or, with kOpBf16T, down their columns (weights [E, K, N]).
 //
 // A stage is 128 bytes of K (256 MXFP4 or 64 bf16 elements) of TN weight and
 // TM routed rows; two stages in LDS.  128 bytes are one cache line, so every
@@ -7,6 +8,12 @@
 // chunk c in slot c ^ (r % 8): the 8 rows a fragment read touches together
 // then lie in 8 different 16-byte bank groups, and the permutation is applied
 // to the source address of the DMA, within the line.
+//
+// With kOpBf16T the weights' part of a stage is 64 rows k of TN columns, and
+// fragments are gathered by the transposing LDS read: a group of 16 lanes
+// reads 4 rows of 16 columns, and each lane receives one column's 4 values.
+// Chunk c of row k sits in slot c ^ 4 (k % 4), so that the 4 rows of a group
+// and the two groups of a 32-column fragment lie in different banks.
 //
 // One stage is four MFMA steps; in step s lanes 0-31 contract chunk s and
 // lanes 32-63 chunk 4 + s, so a lane's four MXFP4 block scales of the stage
@@ -37,11 +44,21 @@ struct StagedCfg {
   static constexpr int ROWS = TM + TN;
   static constexpr int LOADS = ROWS / 8 / WAVES;       // staging instructions of a wave and stage
   static constexpr int WLOADS = TN / 8 / WAVES;        // the weights' part of them
-  static constexpr bool MX = OP == kOpMx;
+  static constexpr bool MX = OP == kOpMx, TRANS = OP == kOpBf16T;
+  static constexpr int KROWS = 512 / TN;  // kOpBf16T: weight rows of one staging instruction
   static constexpr int SLOADS = MX ? ROWS / 32 / WAVES : 0;  // scale instructions (32 rows each)
   static constexpr int STAGE = ROWS * 128 + (MX ? ROWS * 8 : 0);
+  static_assert(WAVES * KROWS % 4 == 0 || !TRANS, "slots of kOpBf16T");
   static_assert(TN % (8 * WAVES) == 0 && TM % (8 * WAVES) == 0 && (!MX || ROWS % (32 * WAVES) == 0), "staging split");
 };
+
+// Transposing LDS read of 16-bit values (see above).
+__device__ __forceinline__ uint2 read_tr(const uint8_t *at) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(const_cast<uint8_t *>(at)));
+  return __builtin_bit_cast(uint2, v);
+}
 
 template <class C, int EPI>
 __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt &t, int32_t n0, uint8_t *lds) {
@@ -66,9 +83,16 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
 
   const uint8_t *from[C::LOADS];
   const int lr = lane >> 3, chunk = (lane & 7) ^ (lr & 7);
+  // kOpBf16T: weight row of the stage and column chunk that this lane stages.
+  // Instructions are 4 rows or a multiple apart, so the slot does not depend on j.
+  const int lk = lane / (64 / C::KROWS), wk = wave * C::KROWS + lk;
+  const int wchunk = (lane % (64 / C::KROWS)) ^ ((wk & 3) << 2);
+  const bool wcol = n0 + 8 * wchunk < p.width;
 #pragma unroll
   for (int j = 0; j < C::LOADS; ++j) {
-    if (j < C::WLOADS)
+    if (j < C::WLOADS && C::TRANS)
+      from[j] = p.w + t.e * p.w_expert + (wk + j * C::WAVES * C::KROWS) * p.w_row + 2 * (n0 + 8 * wchunk);
+    else if (j < C::WLOADS)
       from[j] = p.w + t.e * p.w_expert + weight_row((j * C::WAVES + wave) * 8 + lr) * p.w_row + 16 * chunk;
     else
       from[j] = p.x + source(((j - C::WLOADS) * C::WAVES + wave) * 8 + lr) * p.x_row + 16 * chunk;
@@ -90,8 +114,14 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
     const bool in = 8 * s + chunk < p.chunks, sin = 8 * s + 4 * (lane & 1) < p.chunks;
 #pragma unroll
     for (int j = 0; j < C::LOADS; ++j) {
-      dma(in ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
-      from[j] += 128;
+      if (C::TRANS && j < C::WLOADS) {
+        const bool win = wcol && 64 * s + wk + j * C::WAVES * C::KROWS < 8 * p.chunks;
+        dma(win ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
+        from[j] += 64 * p.w_row;
+      } else {
+        dma(in ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
+        from[j] += 128;
+      }
     }
 #pragma unroll
     for (int j = 0; j < C::SLOADS; ++j) {
@@ -103,6 +133,15 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
   // Fragment addresses: row (lane % 32) of a 32-row group, chunk 4 half + s.
   const int fr = lane & 31;
   const int arow = wn * (C::TN / C::WN) + fr, brow = C::TN + wm * (C::TM / C::WM) + fr;
+  // kOpBf16T: lane 16 g + 4 j + b of a transposing read addresses row j and
+  // columns 16 (g % 2) + 4 b .. + 3 of the fragment's 32, in half g / 2.
+  int tcol[C::NI];
+#pragma unroll
+  for (int i = 0; i < C::NI; ++i) {
+    const int j = (lane >> 2) & 3;
+    const int c = (wn * (C::TN / C::WN) + 32 * i) / 8 + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+    tcol[i] = (32 * half + j) * (2 * C::TN) + 16 * (c ^ (j << 2)) + 8 * (lane & 1);
+  }
   struct Frag {
     uint4 a[C::NI], b[C::MI];
   };
@@ -112,7 +151,15 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
   const auto read = [&](Frag &f, const uint8_t *base, int s) {
     const int slot = 16 * ((4 * half + s) ^ (fr & 7));
 #pragma unroll
-    for (int i = 0; i < C::NI; ++i) f.a[i] = *reinterpret_cast<const uint4 *>(base + (arow + 32 * i) * 128 + slot);
+    for (int i = 0; i < C::NI; ++i) {
+      if constexpr (C::TRANS) {
+        const uint8_t *at = base + tcol[i] + 8 * s * (2 * C::TN);
+        const uint2 lo = read_tr(at), hi = read_tr(at + 4 * (2 * C::TN));
+        f.a[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        f.a[i] = *reinterpret_cast<const uint4 *>(base + (arow + 32 * i) * 128 + slot);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < C::MI; ++i) f.b[i] = *reinterpret_cast<const uint4 *>(base + (brow + 32 * i) * 128 + slot);
   };
