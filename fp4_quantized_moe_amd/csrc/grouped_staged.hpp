@@ -27,6 +27,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "dma.hpp"
 #include "grouped_direct.hpp"
@@ -35,6 +36,16 @@ namespace quads {
 
 // Zeros that the staging reads in the place of chunks and scales behind K.
 __device__ __attribute__((aligned(16))) uint32_t g_zero_chunk[4];
+
+template <class F, int... I>
+__device__ __forceinline__ void each_index(F &&f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+// f(integral_constant<int, 0>), ..., f(integral_constant<int, N - 1>).
+template <int N, class F>
+__device__ __forceinline__ void each(F &&f) {
+  each_index(static_cast<F &&>(f), std::make_integer_sequence<int, N>{});
+}
 
 template <int OP_, int TM_, int TN_, int WM_, int WN_>
 struct StagedCfg {
@@ -48,6 +59,9 @@ struct StagedCfg {
   static constexpr int KROWS = 512 / TN;  // kOpBf16T: weight rows of one staging instruction
   static constexpr int SLOADS = MX ? ROWS / 32 / WAVES : 0;  // scale instructions (32 rows each)
   static constexpr int STAGE = ROWS * 128 + (MX ? ROWS * 8 : 0);
+  static constexpr int ALL = LOADS + SLOADS;
+  static constexpr int LATE = ALL / 2;  // staging instructions issued in a stage's last step; the others in the next step
+  static_assert(!MX || (TN % (32 * WAVES) == 0 && TM % (32 * WAVES) == 0), "a scale instruction reads one operand");
   static_assert(WAVES * KROWS % 4 == 0 || !TRANS, "slots of kOpBf16T");
   static_assert(TN % (8 * WAVES) == 0 && TM % (8 * WAVES) == 0 && (!MX || ROWS % (32 * WAVES) == 0), "staging split");
 };
@@ -77,21 +91,19 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
     }
     return min(n0 + r, p.N - 1);
   };
-  const auto source = [&](int r) -> int64_t {
-    return source_row(p, t.r0 + min(r, t.rows - 1));
-  };
+  const auto source = [&](int r) -> int64_t { return source_row(p, t.r0 + min(r, t.rows - 1)); };
 
+  // This lane's staging sources; each moves on by one stage when it is used.
   const uint8_t *from[C::LOADS];
   const int lr = lane >> 3, chunk = (lane & 7) ^ (lr & 7);
   // kOpBf16T: weight row of the stage and column chunk that this lane stages.
   // Instructions are 4 rows or a multiple apart, so the slot does not depend on j.
   const int lk = lane / (64 / C::KROWS), wk = wave * C::KROWS + lk;
-  const int wchunk = (lane % (64 / C::KROWS)) ^ ((wk & 3) << 2);
-  const bool wcol = n0 + 8 * wchunk < p.width;
+  const int wcol = min(n0 + 8 * ((lane % (64 / C::KROWS)) ^ ((wk & 3) << 2)), p.width - 8);
 #pragma unroll
   for (int j = 0; j < C::LOADS; ++j) {
     if (j < C::WLOADS && C::TRANS)
-      from[j] = p.w + t.e * p.w_expert + (wk + j * C::WAVES * C::KROWS) * p.w_row + 2 * (n0 + 8 * wchunk);
+      from[j] = p.w + t.e * p.w_expert + (wk + j * C::WAVES * C::KROWS) * p.w_row + 2 * wcol;
     else if (j < C::WLOADS)
       from[j] = p.w + t.e * p.w_expert + weight_row((j * C::WAVES + wave) * 8 + lr) * p.w_row + 16 * chunk;
     else
@@ -107,26 +119,23 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
       sfrom[j] = p.x_scales + source(r - C::TN) * p.chunks + 4 * (lane & 1);
   }
 
+  // Instruction j of stage s (the scales' behind the operands').  Lanes whose
+  // chunk lies behind K stage zeros (a scale byte 0 is 2^-127).
   const int stages = (p.chunks + 7) / 8;
-  const auto fetch = [&](int s) {  // called once for each stage, in order
+  const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_chunk);
+  const auto fetch_one = [&](int s, auto jc) {
+    constexpr int j = decltype(jc)::value;
     uint8_t *base = lds + (s & 1) * C::STAGE;
-    const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_chunk);
-    const bool in = 8 * s + chunk < p.chunks, sin = 8 * s + 4 * (lane & 1) < p.chunks;
-#pragma unroll
-    for (int j = 0; j < C::LOADS; ++j) {
-      if (C::TRANS && j < C::WLOADS) {
-        const bool win = wcol && 64 * s + wk + j * C::WAVES * C::KROWS < 8 * p.chunks;
-        dma(win ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
-        from[j] += 64 * p.w_row;
-      } else {
-        dma(in ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
-        from[j] += 128;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < C::SLOADS; ++j) {
-      dma(sin ? sfrom[j] : zero, base + C::ROWS * 128 + (j * C::WAVES + wave) * 256, 4);
-      sfrom[j] += 8;
+    if constexpr (j >= C::LOADS) {
+      constexpr int k = j - C::LOADS;
+      dma(8 * s + 4 * (lane & 1) < p.chunks ? sfrom[k] : zero, base + C::ROWS * 128 + (k * C::WAVES + wave) * 256, 4);
+      sfrom[k] += 8;
+    } else if constexpr (C::TRANS && j < C::WLOADS) {
+      dma(64 * s + wk + j * C::WAVES * C::KROWS < 8 * p.chunks ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
+      from[j] += 64 * p.w_row;
+    } else {
+      dma(8 * s + chunk < p.chunks ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
+      from[j] += 128;
     }
   };
 
@@ -148,30 +157,32 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
   struct Scales {
     uint32_t a[C::NI], b[C::MI];
   };
-  const auto read = [&](Frag &f, const uint8_t *base, int s) {
-    const int slot = 16 * ((4 * half + s) ^ (fr & 7));
-#pragma unroll
-    for (int i = 0; i < C::NI; ++i) {
+  // Item r of a step's fragment reads, in the order the products need them:
+  // a[0], all of b, then the other a; behind them a stage's scales.
+  const auto read_item = [&](Frag &f, Scales &sf, const uint8_t *base, int s, auto rc) {
+    constexpr int r = decltype(rc)::value;
+    constexpr int FRAGS = C::NI + C::MI;
+    if constexpr (r >= FRAGS) {
+      constexpr int k = r - FRAGS;
+      const uint8_t *sb = base + C::ROWS * 128 + 4 * half;
+      if constexpr (k < C::NI)
+        sf.a[k] = *reinterpret_cast<const uint32_t *>(sb + (arow + 32 * k) * 8);
+      else
+        sf.b[k - C::NI] = *reinterpret_cast<const uint32_t *>(sb + (brow + 32 * (k - C::NI)) * 8);
+    } else if constexpr (r >= 1 && r <= C::MI) {
+      f.b[r - 1] = *reinterpret_cast<const uint4 *>(base + (brow + 32 * (r - 1)) * 128 + 16 * ((4 * half + s) ^ (fr & 7)));
+    } else {
+      constexpr int i = r == 0 ? 0 : r - C::MI;
       if constexpr (C::TRANS) {
         const uint8_t *at = base + tcol[i] + 8 * s * (2 * C::TN);
         const uint2 lo = read_tr(at), hi = read_tr(at + 4 * (2 * C::TN));
         f.a[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
       } else {
-        f.a[i] = *reinterpret_cast<const uint4 *>(base + (arow + 32 * i) * 128 + slot);
+        f.a[i] = *reinterpret_cast<const uint4 *>(base + (arow + 32 * i) * 128 + 16 * ((4 * half + s) ^ (fr & 7)));
       }
     }
-#pragma unroll
-    for (int i = 0; i < C::MI; ++i) f.b[i] = *reinterpret_cast<const uint4 *>(base + (brow + 32 * i) * 128 + slot);
   };
-  const auto read_scales = [&](Scales &f, const uint8_t *base) {
-    if constexpr (C::MX) {
-      const uint8_t *sc = base + C::ROWS * 128 + 4 * half;
-#pragma unroll
-      for (int i = 0; i < C::NI; ++i) f.a[i] = *reinterpret_cast<const uint32_t *>(sc + (arow + 32 * i) * 8);
-#pragma unroll
-      for (int i = 0; i < C::MI; ++i) f.b[i] = *reinterpret_cast<const uint32_t *>(sc + (brow + 32 * i) * 8);
-    }
-  };
+  constexpr int FRAGS = C::NI + C::MI, SLOTS = C::NI * C::MI;
 
   f32x16 acc[C::NI][C::MI];
 #pragma unroll
@@ -179,54 +190,60 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
 #pragma unroll
     for (int k = 0; k < C::MI; ++k) acc[i][k] = f32x16{};
   Scales sc;
-  const auto multiply = [&](const Frag &f, auto step) {
-    constexpr int S = decltype(step)::value;
-#pragma unroll
-    for (int i = 0; i < C::NI; ++i)
-#pragma unroll
-      for (int k = 0; k < C::MI; ++k) {
-        if constexpr (C::MX)
-          acc[i][k] = mfma_mx<S>(f.a[i], f.b[k], acc[i][k], sc.a[i], sc.b[k]);
-        else
-          acc[i][k] = mfma_bf16(f.a[i], f.b[k], acc[i][k]);
-      }
+  // One step: its products of `f`, with the reads of `g` (step gs of the stage
+  // at gbase; with SCALES that stage's scales too) and staging instructions
+  // [D0, D1) of stage ds between them, in exactly this order.  Left to itself
+  // the compiler puts the reads last, where the next step waits for them.
+  const auto step = [&](auto sel, const Frag &f, Frag &g, Scales &gsc, const uint8_t *gbase, int gs, auto scales, int ds,
+                        auto d0, auto d1) {
+    constexpr int S = decltype(sel)::value, D0 = decltype(d0)::value, DN = decltype(d1)::value - D0;
+    constexpr int READS = FRAGS + (C::MX && decltype(scales)::value ? FRAGS : 0);
+    constexpr int RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
+    each<SLOTS>([&](auto slot) {
+      constexpr int n = decltype(slot)::value, i = n / C::MI, k = n % C::MI;
+      if constexpr (C::MX)
+        acc[i][k] = mfma_mx<S>(f.a[i], f.b[k], acc[i][k], sc.a[i], sc.b[k]);
+      else
+        acc[i][k] = mfma_bf16(f.a[i], f.b[k], acc[i][k]);
+      each<RPS>([&](auto q) {
+        constexpr int r = n * RPS + decltype(q)::value;
+        if constexpr (r < READS) read_item(g, gsc, gbase, gs, std::integral_constant<int, r>{});
+      });
+      each<DPS>([&](auto q) {
+        constexpr int d = n * DPS + decltype(q)::value;
+        if constexpr (d < DN) fetch_one(ds, std::integral_constant<int, D0 + d>{});
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
   const auto c0 = std::integral_constant<int, 0>{};
   const auto c1 = std::integral_constant<int, 1>{};
   const auto c2 = std::integral_constant<int, 2>{};
   const auto c3 = std::integral_constant<int, 3>{};
+  const auto late = std::integral_constant<int, C::LATE>{};
+  const auto all = std::integral_constant<int, C::ALL>{};
 
-  // Stages behind the last are fetched as zeros into LDS that no one reads
-  // again: the loop has no branches (with them the compiler keeps a second
-  // copy of the accumulators).
-  fetch(0);
-  fetch(1);
-  wait_vm<C::LOADS + C::SLOADS>();
+  // Stages behind the last are fetched as zeros that no one uses, so the loop
+  // is one block of code without branches: with one inside, the compiler sinks
+  // the products past all the reads.
+  each<C::ALL>([&](auto j) { fetch_one(0, j); });
+  each<C::LATE>([&](auto j) { fetch_one(1, j); });
+  wait_vm<C::LATE>();
   barrier_no_fence();
   Frag f0, f1;
-  read(f0, lds, 0);
-  read_scales(sc, lds);
+  each<FRAGS + (C::MX ? FRAGS : 0)>([&](auto r) { read_item(f0, sc, lds, 0, r); });
   for (int s = 0; s < stages; ++s) {
-    const uint8_t *cur = lds + (s & 1) * C::STAGE, *nxt = lds + ((s + 1) & 1) * C::STAGE;
-    read(f1, cur, 1);
-    multiply(f0, c0);
-    __builtin_amdgcn_sched_barrier(0);  // keep one step's fragments in flight, not the whole stage's
-    read(f0, cur, 2);
-    multiply(f1, c1);
-    __builtin_amdgcn_sched_barrier(0);
-    read(f1, cur, 3);
-    multiply(f0, c2);
-    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t *cur = lds + (s & 1) * C::STAGE;
+    const uint8_t *nxt = lds + ((s + 1) & 1) * C::STAGE;
+    step(c0, f0, f1, sc, cur, 1, c0, s + 1, late, all);
+    step(c1, f1, f0, sc, cur, 2, c0, 0, c0, c0);
+    step(c2, f0, f1, sc, cur, 3, c0, 0, c0, c0);
     wait_lgkm0();  // step 3's fragments are in registers: this wave is done with the stage's LDS
     wait_vm<0>();  // and its part of the next stage has landed
     barrier_no_fence();
-    fetch(s + 2);
     Scales next;
-    read(f0, nxt, 0);
-    read_scales(next, nxt);
-    multiply(f1, c3);
-    sc = next;
-    __builtin_amdgcn_sched_barrier(0);
+    step(c3, f1, f0, next, nxt, 0, c1, s + 2, c0, late);
+    if constexpr (C::MX) sc = next;
   }
   wait_vm<0>();
 

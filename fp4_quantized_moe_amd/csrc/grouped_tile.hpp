@@ -94,6 +94,9 @@ __device__ __forceinline__ TileAt find_tile(const int32_t *offsets, int E, int i
     at += n;
     first = last;
   }
+  t.e = __builtin_amdgcn_readfirstlane(t.e);  // the same in every lane: into scalar registers
+  t.r0 = __builtin_amdgcn_readfirstlane(t.r0);
+  t.rows = __builtin_amdgcn_readfirstlane(t.rows);
   return t;
 }
 
