@@ -47,9 +47,9 @@ __device__ __forceinline__ void each(F &&f) {
   each_index(static_cast<F &&>(f), std::make_integer_sequence<int, N>{});
 }
 
-template <int OP_, int TM_, int TN_, int WM_, int WN_>
+template <int OP_, int TM_, int TN_, int WM_, int WN_, int STAGES_>
 struct StagedCfg {
-  static constexpr int OP = OP_, TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+  static constexpr int OP = OP_, TM = TM_, TN = TN_, WM = WM_, WN = WN_, STAGES = STAGES_;
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int MI = TM / WM / 32, NI = TN / WN / 32;  // 32 x 32 tiles of a wave
   static constexpr int ROWS = TM + TN;
@@ -60,7 +60,6 @@ struct StagedCfg {
   static constexpr int SLOADS = MX ? ROWS / 32 / WAVES : 0;  // scale instructions (32 rows each)
   static constexpr int STAGE = ROWS * 128 + (MX ? ROWS * 8 : 0);
   static constexpr int ALL = LOADS + SLOADS;
-  static constexpr int LATE = ALL / 2;  // staging instructions issued in a stage's last step; the others in the next step
   static_assert(!MX || (TN % (32 * WAVES) == 0 && TM % (32 * WAVES) == 0), "a scale instruction reads one operand");
   static_assert(WAVES * KROWS % 4 == 0 || !TRANS, "slots of kOpBf16T");
   static_assert(TN % (8 * WAVES) == 0 && TM % (8 * WAVES) == 0 && (!MX || ROWS % (32 * WAVES) == 0), "staging split");
@@ -72,6 +71,190 @@ __device__ __forceinline__ uint2 read_tr(const uint8_t *at) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(const_cast<uint8_t *>(at)));
   return __builtin_bit_cast(uint2, v);
+}
+
+// ---- epilogue ----------------------------------------------------------------
+//
+// A lane's four consecutive columns are 8 or 16 bytes of one row: stored from
+// registers, an instruction touches 32 rows in 16-byte pieces (measured: the
+// down projection's 537 MB of bf16 took 190 of its 352 us that way).  Each
+// wave turns 32-row blocks around in LDS of its own instead and stores whole
+// 128-byte lines, 8 rows an instruction.  Block row r keeps its 16-byte chunk
+// c in slot c ^ (r / 2 % chunks); a wave's LDS accesses are in order, so no
+// barrier is needed.
+
+constexpr int kTurnBytes = 4096;  // 32 rows of 128 bytes
+
+template <int RB>  // bytes of a block row: 64 or 128
+__device__ __forceinline__ int turn_at(int row, int c) {
+  return row * RB + 16 * (c ^ ((row >> 1) & (RB / 16 - 1)));
+}
+
+// One 32 x 32 tile as bf16 columns [32 i, 32 i + 32) of the block.
+template <int RB>
+__device__ __forceinline__ void turn_put_bf16(uint8_t *turn, int i, const float (&v)[16]) {
+  const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint2 *>(turn + turn_at<RB>(fr, 4 * i + q) + 8 * half) =
+        make_uint2(pack_bf16(v[4 * q], v[4 * q + 1]), pack_bf16(v[4 * q + 2], v[4 * q + 3]));
+}
+
+// The block's rows < rows to out (stride bytes apart); bytes at and behind
+// `limit` of a row lie behind the last column and are not stored.
+template <int RB>
+__device__ __forceinline__ void turn_store(const uint8_t *turn, uint8_t *out, int64_t stride, int rows, int limit) {
+  constexpr int CH = RB / 16, PER = 64 / CH;  // rows of one instruction
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < 32 / PER; ++j) {
+    const int row = j * PER + lane / CH, c = (lane % CH) ^ ((row >> 1) & (CH - 1));
+    const uint4 v = *reinterpret_cast<const uint4 *>(turn + row * RB + 16 * (lane % CH));
+    if (row < rows && 16 * c < limit) *reinterpret_cast<uint4 *>(out + row * stride + 16 * c) = v;
+  }
+}
+
+// The reverse: global rows into the block (rows and columns outside: not loaded).
+template <int RB>
+struct TurnLoad {
+  static constexpr int CH = RB / 16, PER = 64 / CH, N = 32 / PER;
+  uint4 v[N];
+  __device__ __forceinline__ void load(const uint8_t *in, int64_t stride, int rows, int limit) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int row = j * PER + lane / CH, c = (lane % CH) ^ ((row >> 1) & (CH - 1));
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (row < rows && 16 * c < limit) v[j] = *reinterpret_cast<const uint4 *>(in + row * stride + 16 * c);
+    }
+  }
+  __device__ __forceinline__ void put(uint8_t *turn) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < N; ++j) *reinterpret_cast<uint4 *>(turn + (j * PER + lane / CH) * RB + 16 * (lane % CH)) = v[j];
+  }
+};
+
+// This lane's 16 values of the block's tile i.
+template <int RB>
+__device__ __forceinline__ void turn_get_bf16(const uint8_t *turn, int i, float (&v)[16]) {
+  const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(turn + turn_at<RB>(fr, 4 * i + q) + 8 * half);
+    v[4 * q] = __uint_as_float(w.x << 16);
+    v[4 * q + 1] = __uint_as_float(w.x & 0xFFFF0000u);
+    v[4 * q + 2] = __uint_as_float(w.y << 16);
+    v[4 * q + 3] = __uint_as_float(w.y & 0xFFFF0000u);
+  }
+}
+
+// A wave's accumulators a[i] (i-th 32 columns) of 32 rows: row0 is the first
+// row's index in the output, rows how many exist, n0 the wave's first column.
+template <int EPI, int NI>
+__device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16 (&a)[NI], uint8_t *turn, int64_t row0,
+                                            int rows, int32_t n0) {
+  if (rows <= 0) return;
+  float v[16];
+  if constexpr (EPI == kEpiF32) {
+    const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4 *>(turn + turn_at<128>(fr, 2 * q + half)) =
+            make_float4(a[i][4 * q], a[i][4 * q + 1], a[i][4 * q + 2], a[i][4 * q + 3]);
+      const int32_t n = n0 + 32 * i;
+      turn_store<128>(turn, static_cast<uint8_t *>(p.y) + 4 * (row0 * p.width + n), 4 * static_cast<int64_t>(p.width),
+                      rows, 4 * (p.width - n));
+    }
+  } else if constexpr (EPI == kEpiBf16) {
+#pragma unroll
+    for (int i = 0; i < NI; i += 2) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = a[i + t][r];
+        turn_put_bf16<128>(turn, t, v);
+      }
+      const int32_t n = n0 + 32 * i;
+      turn_store<128>(turn, static_cast<uint8_t *>(p.y) + 2 * (row0 * p.width + n), 2 * static_cast<int64_t>(p.width),
+                      rows, 2 * (p.width - n));
+    }
+  } else if constexpr (EPI == kEpiSwiglu) {
+    constexpr int PAIRS = NI / 2, RB = 64 * PAIRS;
+    const int64_t stride = 2 * static_cast<int64_t>(p.width);
+    const int limit = 2 * (p.width - n0);
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v[r] = silu(a[i][r]) * a[PAIRS + i][r];
+      turn_put_bf16<RB>(turn, i, v);
+    }
+    turn_store<RB>(turn, static_cast<uint8_t *>(p.y) + row0 * stride + 2 * n0, stride, rows, limit);
+    if (p.y2) {
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[r] = a[part * PAIRS + i][r];
+          turn_put_bf16<RB>(turn, i, v);
+        }
+        turn_store<RB>(turn, static_cast<uint8_t *>(p.y2) + row0 * 2 * stride + part * stride + 2 * n0, 2 * stride, rows,
+                       limit);
+      }
+    }
+  } else if constexpr (EPI == kEpiSwigluMx) {
+    constexpr int PAIRS = NI / 2;
+    const int lane = threadIdx.x & 63, fr = lane & 31;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v[r] = silu(a[i][r]) * a[PAIRS + i][r];
+      store_mx_block(v, true, turn + fr * 16 * PAIRS + 16 * i, turn + 32 * 16 * PAIRS + fr * PAIRS + i);
+    }
+    const int row = lane / PAIRS, i = lane % PAIRS;
+    const uint4 c = *reinterpret_cast<const uint4 *>(turn + 16 * (lane & (32 * PAIRS - 1)));
+    const uint8_t s = turn[32 * 16 * PAIRS + (lane & (32 * PAIRS - 1))];
+    if (lane < 32 * PAIRS && row < rows && n0 + 32 * i < p.width) {
+      *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.y) + (row0 + row) * (p.width >> 1) + (n0 >> 1) + 16 * i) = c;
+      static_cast<uint8_t *>(p.y2)[(row0 + row) * (p.width >> 5) + (n0 >> 5) + i] = s;
+    }
+  } else {  // kEpiGatedBwd: a is dh; dg and du take the place of g and u
+    const int64_t stride = 4 * static_cast<int64_t>(p.width);  // bytes of a row [gate | up]
+#pragma unroll
+    for (int i = 0; i < NI; i += 2) {
+      const int32_t n = n0 + 32 * i;
+      const int limit = 2 * (p.width - n);
+      const int64_t at = row0 * stride + 2 * n;
+      const uint8_t *in = reinterpret_cast<const uint8_t *>(p.gu) + at;
+      uint8_t *out = static_cast<uint8_t *>(p.y) + at;
+      TurnLoad<128> lg, lu;
+      lg.load(in, stride, rows, limit);
+      lu.load(in + 2 * static_cast<int64_t>(p.width), stride, rows, limit);
+      float g[2][16], u[2][16];
+      lg.put(turn);
+      turn_get_bf16<128>(turn, 0, g[0]);
+      turn_get_bf16<128>(turn, 1, g[1]);
+      lu.put(turn);
+      turn_get_bf16<128>(turn, 0, u[0]);
+      turn_get_bf16<128>(turn, 1, u[1]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float d = a[i + t][r];
+          gated_grad(d, g[t][r], u[t][r]);
+        }
+      turn_put_bf16<128>(turn, 0, g[0]);
+      turn_put_bf16<128>(turn, 1, g[1]);
+      turn_store<128>(turn, out, stride, rows, limit);
+      turn_put_bf16<128>(turn, 0, u[0]);
+      turn_put_bf16<128>(turn, 1, u[1]);
+      turn_store<128>(turn, out + 2 * static_cast<int64_t>(p.width), stride, rows, limit);
+    }
+  }
 }
 
 template <class C, int EPI>
@@ -95,7 +278,7 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
 
   // This lane's staging sources; each moves on by one stage when it is used.
   const uint8_t *from[C::LOADS];
-  const int lr = lane >> 3, chunk = (lane & 7) ^ (lr & 7);
+  const int lr = lane >> 3, chunk = (lane & 7) ^ ((4 * wave + (lr >> 1)) & 7);
   // kOpBf16T: weight row of the stage and column chunk that this lane stages.
   // Instructions are 4 rows or a multiple apart, so the slot does not depend on j.
   const int lk = lane / (64 / C::KROWS), wk = wave * C::KROWS + lk;
@@ -123,9 +306,8 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
   // chunk lies behind K stage zeros (a scale byte 0 is 2^-127).
   const int stages = (p.chunks + 7) / 8;
   const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_chunk);
-  const auto fetch_one = [&](int s, auto jc) {
+  const auto fetch_one = [&](int s, uint8_t *base, auto jc) {
     constexpr int j = decltype(jc)::value;
-    uint8_t *base = lds + (s & 1) * C::STAGE;
     if constexpr (j >= C::LOADS) {
       constexpr int k = j - C::LOADS;
       dma(8 * s + 4 * (lane & 1) < p.chunks ? sfrom[k] : zero, base + C::ROWS * 128 + (k * C::WAVES + wave) * 256, 4);
@@ -170,7 +352,7 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
       else
         sf.b[k - C::NI] = *reinterpret_cast<const uint32_t *>(sb + (brow + 32 * (k - C::NI)) * 8);
     } else if constexpr (r >= 1 && r <= C::MI) {
-      f.b[r - 1] = *reinterpret_cast<const uint4 *>(base + (brow + 32 * (r - 1)) * 128 + 16 * ((4 * half + s) ^ (fr & 7)));
+      f.b[r - 1] = *reinterpret_cast<const uint4 *>(base + (brow + 32 * (r - 1)) * 128 + 16 * ((4 * half + s) ^ ((fr >> 1) & 7)));
     } else {
       constexpr int i = r == 0 ? 0 : r - C::MI;
       if constexpr (C::TRANS) {
@@ -178,7 +360,7 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
         const uint2 lo = read_tr(at), hi = read_tr(at + 4 * (2 * C::TN));
         f.a[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
       } else {
-        f.a[i] = *reinterpret_cast<const uint4 *>(base + (arow + 32 * i) * 128 + 16 * ((4 * half + s) ^ (fr & 7)));
+        f.a[i] = *reinterpret_cast<const uint4 *>(base + (arow + 32 * i) * 128 + 16 * ((4 * half + s) ^ ((fr >> 1) & 7)));
       }
     }
   };
@@ -191,13 +373,13 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
     for (int k = 0; k < C::MI; ++k) acc[i][k] = f32x16{};
   Scales sc;
   // One step: its products of `f`, with the reads of `g` (step gs of the stage
-  // at gbase; with SCALES that stage's scales too) and staging instructions
-  // [D0, D1) of stage ds between them, in exactly this order.  Left to itself
+  // at gbase) and, in a stage's last step, the next stage's scales and the
+  // staging of stage ds between them, in exactly this order.  Left to itself
   // the compiler puts the reads last, where the next step waits for them.
-  const auto step = [&](auto sel, const Frag &f, Frag &g, Scales &gsc, const uint8_t *gbase, int gs, auto scales, int ds,
-                        auto d0, auto d1) {
-    constexpr int S = decltype(sel)::value, D0 = decltype(d0)::value, DN = decltype(d1)::value - D0;
-    constexpr int READS = FRAGS + (C::MX && decltype(scales)::value ? FRAGS : 0);
+  const auto step = [&](auto sel, const Frag &f, Frag &g, Scales &gsc, const uint8_t *gbase, int gs, auto last, int ds,
+                        uint8_t *dbase) {
+    constexpr int S = decltype(sel)::value, DN = decltype(last)::value ? C::ALL : 0;
+    constexpr int READS = FRAGS + (C::MX && decltype(last)::value ? FRAGS : 0);
     constexpr int RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
     each<SLOTS>([&](auto slot) {
       constexpr int n = decltype(slot)::value, i = n / C::MI, k = n % C::MI;
@@ -211,7 +393,7 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
       });
       each<DPS>([&](auto q) {
         constexpr int d = n * DPS + decltype(q)::value;
-        if constexpr (d < DN) fetch_one(ds, std::integral_constant<int, D0 + d>{});
+        if constexpr (d < DN) fetch_one(ds, dbase, std::integral_constant<int, d>{});
       });
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -220,41 +402,40 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
   const auto c1 = std::integral_constant<int, 1>{};
   const auto c2 = std::integral_constant<int, 2>{};
   const auto c3 = std::integral_constant<int, 3>{};
-  const auto late = std::integral_constant<int, C::LATE>{};
-  const auto all = std::integral_constant<int, C::ALL>{};
-
   // Stages behind the last are fetched as zeros that no one uses, so the loop
   // is one block of code without branches: with one inside, the compiler sinks
   // the products past all the reads.
-  each<C::ALL>([&](auto j) { fetch_one(0, j); });
-  each<C::LATE>([&](auto j) { fetch_one(1, j); });
-  wait_vm<C::LATE>();
+#pragma unroll
+  for (int s = 0; s < C::STAGES; ++s) each<C::ALL>([&](auto j) { fetch_one(s, lds + s * C::STAGE, j); });
+  wait_vm<(C::STAGES - 1) * C::ALL>();
   barrier_no_fence();
   Frag f0, f1;
   each<FRAGS + (C::MX ? FRAGS : 0)>([&](auto r) { read_item(f0, sc, lds, 0, r); });
+  uint8_t *cur = lds;
   for (int s = 0; s < stages; ++s) {
-    const uint8_t *cur = lds + (s & 1) * C::STAGE;
-    const uint8_t *nxt = lds + ((s + 1) & 1) * C::STAGE;
-    step(c0, f0, f1, sc, cur, 1, c0, s + 1, late, all);
-    step(c1, f1, f0, sc, cur, 2, c0, 0, c0, c0);
-    step(c2, f0, f1, sc, cur, 3, c0, 0, c0, c0);
+    uint8_t *nxt = cur == lds + (C::STAGES - 1) * C::STAGE ? lds : cur + C::STAGE;
+    step(c0, f0, f1, sc, cur, 1, c0, 0, cur);
+    step(c1, f1, f0, sc, cur, 2, c0, 0, cur);
+    step(c2, f0, f1, sc, cur, 3, c0, 0, cur);
     wait_lgkm0();  // step 3's fragments are in registers: this wave is done with the stage's LDS
-    wait_vm<0>();  // and its part of the next stage has landed
+    wait_vm<(C::STAGES - 2) * C::ALL>();  // and its part of the next stage has landed
     barrier_no_fence();
     Scales next;
-    step(c3, f1, f0, next, nxt, 0, c1, s + 2, c0, late);
+    step(c3, f1, f0, next, nxt, 0, c1, s + C::STAGES, cur);
     if constexpr (C::MX) sc = next;
+    cur = nxt;
   }
   wait_vm<0>();
 
-  constexpr int PAIRS = PAIR ? C::NI / 2 : C::NI;
+  uint8_t *turn = lds + C::STAGES * C::STAGE + wave * kTurnBytes;
 #pragma unroll
   for (int k = 0; k < C::MI; ++k) {
-    const int32_t m = wm * (C::TM / C::WM) + 32 * k + fr;
+    f32x16 col[C::NI];
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i)
-      store_tile<EPI>(p, acc[i][k], acc[PAIR ? i + PAIRS : i][k], static_cast<int64_t>(t.r0) + m, m < t.rows,
-                      n0 + (wn * PAIRS + i) * 32);
+    for (int i = 0; i < C::NI; ++i) col[i] = acc[i][k];
+    const int m = wm * (C::TM / C::WM) + 32 * k;
+    store_block<EPI, C::NI>(p, col, turn, static_cast<int64_t>(t.r0) + m, t.rows - m,
+                            n0 + wn * (C::TN / C::WN) / (PAIR ? 2 : 1));
   }
 }
 
@@ -263,7 +444,7 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
 // share an expert's weights and a row tile's activations share an L2.
 template <class C, int EPI>
 __global__ __launch_bounds__(C::THREADS, 1) void k_grouped_staged(GroupedParams p, int col_tiles) {
-  __shared__ __attribute__((aligned(128))) uint8_t lds[2 * C::STAGE];
+  __shared__ __attribute__((aligned(128))) uint8_t lds[C::STAGES * C::STAGE + C::WAVES * kTurnBytes];
   const TileAt all = find_tile<C::TM>(p.offsets, p.E, 0x7FFFFFFF);
   const int64_t tiles = static_cast<int64_t>(all.total) * col_tiles, per = (tiles + 7) / 8;
   const int64_t at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);

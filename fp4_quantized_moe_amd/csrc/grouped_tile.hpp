@@ -163,6 +163,14 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * 1.44269504088896341f));
 }
 
+// Gradients of h = silu(g) u from d = dh, in place of g and u: with
+// s = sigmoid(g), d gate = d u s (1 + g (1 - s)) and d up = d g s.
+__device__ __forceinline__ void gated_grad(float d, float &g, float &u) {
+  const float s = sigmoid(g), z = g;
+  g = d * u * (s * (1.0f + z * (1.0f - s)));
+  u = d * (z * s);
+}
+
 // Stores one 32 (columns n0 ..) x 32 (rows) tile: `a` is the accumulator
 // (the gate's with the SwiGLU epilogues, whose up projection is `b`).  `row`
 // is the lane's routed row, row_ok whether the tile has it.  Columns are
@@ -204,25 +212,18 @@ __device__ __forceinline__ void store_tile(const GroupedParams &p, const f32x16 
               make_uint2(pack_bf16(b[4 * q], b[4 * q + 1]), pack_bf16(b[4 * q + 2], b[4 * q + 3]));
         }
       } else {
-        // dh in the accumulator; with s = sigmoid(g): d up = dh g s,
-        // d gate = dh u s (1 + g (1 - s)).
         const int64_t at = row * 2 * p.width + n;
         const uint2 gw = *reinterpret_cast<const uint2 *>(p.gu + at);
         const uint2 uw = *reinterpret_cast<const uint2 *>(p.gu + at + p.width);
-        const float g[4] = {__uint_as_float(gw.x << 16), __uint_as_float(gw.x & 0xFFFF0000u),
-                            __uint_as_float(gw.y << 16), __uint_as_float(gw.y & 0xFFFF0000u)};
-        const float u[4] = {__uint_as_float(uw.x << 16), __uint_as_float(uw.x & 0xFFFF0000u),
-                            __uint_as_float(uw.y << 16), __uint_as_float(uw.y & 0xFFFF0000u)};
-        float dg[4], du[4];
+        float g[4] = {__uint_as_float(gw.x << 16), __uint_as_float(gw.x & 0xFFFF0000u),
+                      __uint_as_float(gw.y << 16), __uint_as_float(gw.y & 0xFFFF0000u)};
+        float u[4] = {__uint_as_float(uw.x << 16), __uint_as_float(uw.x & 0xFFFF0000u),
+                      __uint_as_float(uw.y << 16), __uint_as_float(uw.y & 0xFFFF0000u)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float s = sigmoid(g[i]), d = a[4 * q + i];
-          du[i] = d * (g[i] * s);
-          dg[i] = d * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
-        }
+        for (int i = 0; i < 4; ++i) gated_grad(a[4 * q + i], g[i], u[i]);
         uint16_t *o = static_cast<uint16_t *>(p.y) + at;
-        *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
-        *reinterpret_cast<uint2 *>(o + p.width) = make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
+        *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]));
+        *reinterpret_cast<uint2 *>(o + p.width) = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
       }
     }
   }
