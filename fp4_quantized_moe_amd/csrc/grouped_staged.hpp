@@ -47,9 +47,11 @@ __device__ __forceinline__ void each(F &&f) {
   each_index(static_cast<F &&>(f), std::make_integer_sequence<int, N>{});
 }
 
-template <int OP_, int TM_, int TN_, int WM_, int WN_, int STAGES_>
+constexpr int kTurnBytes = 4096;  // a wave's epilogue block: 32 rows of 128 bytes
+
+template <int OP_, int TM_, int TN_, int WM_, int WN_>
 struct StagedCfg {
-  static constexpr int OP = OP_, TM = TM_, TN = TN_, WM = WM_, WN = WN_, STAGES = STAGES_;
+  static constexpr int OP = OP_, TM = TM_, TN = TN_, WM = WM_, WN = WN_;
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int MI = TM / WM / 32, NI = TN / WN / 32;  // 32 x 32 tiles of a wave
   static constexpr int ROWS = TM + TN;
@@ -58,10 +60,14 @@ struct StagedCfg {
   static constexpr bool MX = OP == kOpMx, TRANS = OP == kOpBf16T;
   static constexpr int KROWS = 512 / TN;  // kOpBf16T: weight rows of one staging instruction
   static constexpr int SLOADS = MX ? ROWS / 32 / WAVES : 0;  // scale instructions (32 rows each)
+  static constexpr int TURN = 2 * (ROWS * 128 + (MX ? ROWS * 8 : 0));  // LDS: two stages, then the epilogue's blocks,
+  static constexpr int TOKENS = TURN + WAVES * kTurnBytes;             // then the next tile's token ids
+  static constexpr int LDS = TOKENS + 256 * WAVES;
   static constexpr int STAGE = ROWS * 128 + (MX ? ROWS * 8 : 0);
   static constexpr int ALL = LOADS + SLOADS;
   static_assert(!MX || (TN % (32 * WAVES) == 0 && TM % (32 * WAVES) == 0), "a scale instruction reads one operand");
   static_assert(WAVES * KROWS % 4 == 0 || !TRANS, "slots of kOpBf16T");
+  static_assert(64 * WAVES >= TM, "token ids of a tile");
   static_assert(TN % (8 * WAVES) == 0 && TM % (8 * WAVES) == 0 && (!MX || ROWS % (32 * WAVES) == 0), "staging split");
 };
 
@@ -83,8 +89,6 @@ __device__ __forceinline__ uint2 read_tr(const uint8_t *at) {
 // c in slot c ^ (r / 2 % chunks); a wave's LDS accesses are in order, so no
 // barrier is needed.
 
-constexpr int kTurnBytes = 4096;  // 32 rows of 128 bytes
-
 template <int RB>  // bytes of a block row: 64 or 128
 __device__ __forceinline__ int turn_at(int row, int c) {
   return row * RB + 16 * (c ^ ((row >> 1) & (RB / 16 - 1)));
@@ -92,8 +96,8 @@ __device__ __forceinline__ int turn_at(int row, int c) {
 
 // One 32 x 32 tile as bf16 columns [32 i, 32 i + 32) of the block.
 template <int RB>
-__device__ __forceinline__ void turn_put_bf16(uint8_t *turn, int i, const float (&v)[16]) {
-  const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+__device__ __forceinline__ void turn_put_bf16(uint8_t *turn, int lane, int i, const float (&v)[16]) {
+  const int half = lane >> 5, fr = lane & 31;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     *reinterpret_cast<uint2 *>(turn + turn_at<RB>(fr, 4 * i + q) + 8 * half) =
@@ -103,15 +107,15 @@ __device__ __forceinline__ void turn_put_bf16(uint8_t *turn, int i, const float 
 // The block's rows < rows to out (stride bytes apart); bytes at and behind
 // `limit` of a row lie behind the last column and are not stored.
 template <int RB>
-__device__ __forceinline__ void turn_store(const uint8_t *turn, uint8_t *out, int64_t stride, int rows, int limit) {
+__device__ __forceinline__ void turn_store(const uint8_t *turn, int lane, uint8_t *out, int64_t stride, int rows, int limit) {
   constexpr int CH = RB / 16, PER = 64 / CH;  // rows of one instruction
-  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int j = 0; j < 32 / PER; ++j) {
     const int row = j * PER + lane / CH, c = (lane % CH) ^ ((row >> 1) & (CH - 1));
     const uint4 v = *reinterpret_cast<const uint4 *>(turn + row * RB + 16 * (lane % CH));
     if (row < rows && 16 * c < limit) *reinterpret_cast<uint4 *>(out + row * stride + 16 * c) = v;
   }
+  __builtin_amdgcn_sched_barrier(0);  // block after block: all accumulators at once do not fit the other registers
 }
 
 // The reverse: global rows into the block (rows and columns outside: not loaded).
@@ -119,8 +123,7 @@ template <int RB>
 struct TurnLoad {
   static constexpr int CH = RB / 16, PER = 64 / CH, N = 32 / PER;
   uint4 v[N];
-  __device__ __forceinline__ void load(const uint8_t *in, int64_t stride, int rows, int limit) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ void load(const uint8_t *in, int lane, int64_t stride, int rows, int limit) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int row = j * PER + lane / CH, c = (lane % CH) ^ ((row >> 1) & (CH - 1));
@@ -128,8 +131,7 @@ struct TurnLoad {
       if (row < rows && 16 * c < limit) v[j] = *reinterpret_cast<const uint4 *>(in + row * stride + 16 * c);
     }
   }
-  __device__ __forceinline__ void put(uint8_t *turn) const {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ void put(uint8_t *turn, int lane) const {
 #pragma unroll
     for (int j = 0; j < N; ++j) *reinterpret_cast<uint4 *>(turn + (j * PER + lane / CH) * RB + 16 * (lane % CH)) = v[j];
   }
@@ -137,8 +139,8 @@ struct TurnLoad {
 
 // This lane's 16 values of the block's tile i.
 template <int RB>
-__device__ __forceinline__ void turn_get_bf16(const uint8_t *turn, int i, float (&v)[16]) {
-  const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+__device__ __forceinline__ void turn_get_bf16(const uint8_t *turn, int lane, int i, float (&v)[16]) {
+  const int half = lane >> 5, fr = lane & 31;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const uint2 w = *reinterpret_cast<const uint2 *>(turn + turn_at<RB>(fr, 4 * i + q) + 8 * half);
@@ -149,15 +151,23 @@ __device__ __forceinline__ void turn_get_bf16(const uint8_t *turn, int i, float 
   }
 }
 
+// The lane's number, computed anew: what is derived from it is not kept in
+// registers from before the loops, which have none to spare.
+__device__ __forceinline__ int fresh_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // A wave's accumulators a[i] (i-th 32 columns) of 32 rows: row0 is the first
 // row's index in the output, rows how many exist, n0 the wave's first column.
 template <int EPI, int NI>
-__device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16 (&a)[NI], uint8_t *turn, int64_t row0,
+__device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16 (&a)[NI], uint8_t *turn, int lane, int64_t row0,
                                             int rows, int32_t n0) {
   if (rows <= 0) return;
   float v[16];
   if constexpr (EPI == kEpiF32) {
-    const int lane = threadIdx.x & 63, half = lane >> 5, fr = lane & 31;
+    const int half = lane >> 5, fr = lane & 31;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
 #pragma unroll
@@ -165,7 +175,7 @@ __device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16
         *reinterpret_cast<float4 *>(turn + turn_at<128>(fr, 2 * q + half)) =
             make_float4(a[i][4 * q], a[i][4 * q + 1], a[i][4 * q + 2], a[i][4 * q + 3]);
       const int32_t n = n0 + 32 * i;
-      turn_store<128>(turn, static_cast<uint8_t *>(p.y) + 4 * (row0 * p.width + n), 4 * static_cast<int64_t>(p.width),
+      turn_store<128>(turn, lane, static_cast<uint8_t *>(p.y) + 4 * (row0 * p.width + n), 4 * static_cast<int64_t>(p.width),
                       rows, 4 * (p.width - n));
     }
   } else if constexpr (EPI == kEpiBf16) {
@@ -175,10 +185,10 @@ __device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16
       for (int t = 0; t < 2; ++t) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] = a[i + t][r];
-        turn_put_bf16<128>(turn, t, v);
+        turn_put_bf16<128>(turn, lane, t, v);
       }
       const int32_t n = n0 + 32 * i;
-      turn_store<128>(turn, static_cast<uint8_t *>(p.y) + 2 * (row0 * p.width + n), 2 * static_cast<int64_t>(p.width),
+      turn_store<128>(turn, lane, static_cast<uint8_t *>(p.y) + 2 * (row0 * p.width + n), 2 * static_cast<int64_t>(p.width),
                       rows, 2 * (p.width - n));
     }
   } else if constexpr (EPI == kEpiSwiglu) {
@@ -189,9 +199,9 @@ __device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16
     for (int i = 0; i < PAIRS; ++i) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) v[r] = silu(a[i][r]) * a[PAIRS + i][r];
-      turn_put_bf16<RB>(turn, i, v);
+      turn_put_bf16<RB>(turn, lane, i, v);
     }
-    turn_store<RB>(turn, static_cast<uint8_t *>(p.y) + row0 * stride + 2 * n0, stride, rows, limit);
+    turn_store<RB>(turn, lane, static_cast<uint8_t *>(p.y) + row0 * stride + 2 * n0, stride, rows, limit);
     if (p.y2) {
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
@@ -199,20 +209,20 @@ __device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16
         for (int i = 0; i < PAIRS; ++i) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) v[r] = a[part * PAIRS + i][r];
-          turn_put_bf16<RB>(turn, i, v);
+          turn_put_bf16<RB>(turn, lane, i, v);
         }
-        turn_store<RB>(turn, static_cast<uint8_t *>(p.y2) + row0 * 2 * stride + part * stride + 2 * n0, 2 * stride, rows,
+        turn_store<RB>(turn, lane, static_cast<uint8_t *>(p.y2) + row0 * 2 * stride + part * stride + 2 * n0, 2 * stride, rows,
                        limit);
       }
     }
   } else if constexpr (EPI == kEpiSwigluMx) {
     constexpr int PAIRS = NI / 2;
-    const int lane = threadIdx.x & 63, fr = lane & 31;
+    const int fr = lane & 31;
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) v[r] = silu(a[i][r]) * a[PAIRS + i][r];
-      store_mx_block(v, true, turn + fr * 16 * PAIRS + 16 * i, turn + 32 * 16 * PAIRS + fr * PAIRS + i);
+      store_mx_block(v, lane, true, turn + fr * 16 * PAIRS + 16 * i, turn + 32 * 16 * PAIRS + fr * PAIRS + i);
     }
     const int row = lane / PAIRS, i = lane % PAIRS;
     const uint4 c = *reinterpret_cast<const uint4 *>(turn + 16 * (lane & (32 * PAIRS - 1)));
@@ -221,6 +231,7 @@ __device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16
       *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.y) + (row0 + row) * (p.width >> 1) + (n0 >> 1) + 16 * i) = c;
       static_cast<uint8_t *>(p.y2)[(row0 + row) * (p.width >> 5) + (n0 >> 5) + i] = s;
     }
+    __builtin_amdgcn_sched_barrier(0);
   } else {  // kEpiGatedBwd: a is dh; dg and du take the place of g and u
     const int64_t stride = 4 * static_cast<int64_t>(p.width);  // bytes of a row [gate | up]
 #pragma unroll
@@ -231,15 +242,15 @@ __device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16
       const uint8_t *in = reinterpret_cast<const uint8_t *>(p.gu) + at;
       uint8_t *out = static_cast<uint8_t *>(p.y) + at;
       TurnLoad<128> lg, lu;
-      lg.load(in, stride, rows, limit);
-      lu.load(in + 2 * static_cast<int64_t>(p.width), stride, rows, limit);
+      lg.load(in, lane, stride, rows, limit);
+      lu.load(in + 2 * static_cast<int64_t>(p.width), lane, stride, rows, limit);
       float g[2][16], u[2][16];
-      lg.put(turn);
-      turn_get_bf16<128>(turn, 0, g[0]);
-      turn_get_bf16<128>(turn, 1, g[1]);
-      lu.put(turn);
-      turn_get_bf16<128>(turn, 0, u[0]);
-      turn_get_bf16<128>(turn, 1, u[1]);
+      lg.put(turn, lane);
+      turn_get_bf16<128>(turn, lane, 0, g[0]);
+      turn_get_bf16<128>(turn, lane, 1, g[1]);
+      lu.put(turn, lane);
+      turn_get_bf16<128>(turn, lane, 0, u[0]);
+      turn_get_bf16<128>(turn, lane, 1, u[1]);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -247,78 +258,138 @@ __device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16
           const float d = a[i + t][r];
           gated_grad(d, g[t][r], u[t][r]);
         }
-      turn_put_bf16<128>(turn, 0, g[0]);
-      turn_put_bf16<128>(turn, 1, g[1]);
-      turn_store<128>(turn, out, stride, rows, limit);
-      turn_put_bf16<128>(turn, 0, u[0]);
-      turn_put_bf16<128>(turn, 1, u[1]);
-      turn_store<128>(turn, out + 2 * static_cast<int64_t>(p.width), stride, rows, limit);
+      turn_put_bf16<128>(turn, lane, 0, g[0]);
+      turn_put_bf16<128>(turn, lane, 1, g[1]);
+      turn_store<128>(turn, lane, out, stride, rows, limit);
+      turn_put_bf16<128>(turn, lane, 0, u[0]);
+      turn_put_bf16<128>(turn, lane, 1, u[1]);
+      turn_store<128>(turn, lane, out + 2 * static_cast<int64_t>(p.width), stride, rows, limit);
     }
   }
 }
 
+// One workgroup's tiles.  Tiles are numbered columns fastest, each XCD owns a
+// contiguous eighth (workgroups are dealt to the 8 XCDs in turn), so that the
+// tiles running together on an XCD share an expert's weights and few row
+// tiles in its L2; a workgroup takes every step-th tile of its XCD's.
+struct StagedTile {
+  int e;         // expert, or -1: no tile
+  int32_t r0, rows, n0;
+};
+
 template <class C, int EPI>
-__device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt &t, int32_t n0, uint8_t *lds) {
+__device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *lds, uint32_t col_tiles) {
   constexpr bool PAIR = EPI == kEpiSwiglu || EPI == kEpiSwigluMx;
+  constexpr int COLS = PAIR ? C::TN / 2 : C::TN;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
   const int wn = wave / C::WM, wm = wave % C::WM;
 
-  // Weight row of tile row r.  With a gate/up pair the first half of each
-  // wave's rows are gate columns, the second half the same up columns.
-  const auto weight_row = [&](int r) -> int64_t {
-    if constexpr (PAIR) {
-      constexpr int PER = C::TN / C::WN, HALF = PER / 2;
-      const int q = r % PER;
-      const int32_t col = min(n0 + (r / PER) * HALF + q % HALF, p.width - 1);
-      return col + (q >= HALF ? p.width : 0);
+  // The tiles of this workgroup: at, at + step, ... below end.
+  typedef const __attribute__((address_space(4))) int32_t uniform_i32;  // read by scalar loads
+  uniform_i32 *offsets = (uniform_i32 *)reinterpret_cast<uintptr_t>(p.offsets);
+  StagedTile t;
+  uint32_t at, end;
+  const uint32_t step_tiles = gridDim.x / 8;
+  int32_t before, first, last;  // expert t.e: row tiles before it, its rows
+  {
+    const int32_t total = find_tile<C::TM>(p.offsets, p.E, 0x7FFFFFFF).total;
+    const uint32_t tiles = total * col_tiles, per = (tiles + 7) / 8;
+    at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    end = min(tiles, ((blockIdx.x & 7) + 1) * per);
+    if (at >= end) return;
+    const TileAt f = find_tile<C::TM>(p.offsets, p.E, static_cast<int>(at / col_tiles));
+    t.e = f.e;
+    t.r0 = f.r0;
+    t.rows = f.rows;
+    t.n0 = static_cast<int32_t>(at % col_tiles) * COLS;
+    before = f.before;
+    first = offsets[f.e];
+    last = offsets[f.e + 1];
+  }
+  const auto advance = [&](StagedTile &u, int e) {  // the next tile, whose expert is e or a later one
+    at += step_tiles;
+    u.e = -1;
+    u.r0 = u.rows = u.n0 = 0;
+    if (at >= end) return;
+    const int32_t rt = static_cast<int32_t>(at / col_tiles);
+    int32_t n = (last - first + C::TM - 1) / C::TM;
+    while (rt >= before + n) {
+      before += n;
+      ++e;
+      first = last;
+      last = offsets[e + 1];
+      n = (last - first + C::TM - 1) / C::TM;
     }
-    return min(n0 + r, p.N - 1);
+    u.e = e;
+    u.r0 = first + (rt - before) * C::TM;
+    u.rows = min(last - u.r0, static_cast<int32_t>(C::TM));
+    u.n0 = static_cast<int32_t>(at % col_tiles) * COLS;
   };
-  const auto source = [&](int r) -> int64_t { return source_row(p, t.r0 + min(r, t.rows - 1)); };
 
   // This lane's staging sources; each moves on by one stage when it is used.
-  const uint8_t *from[C::LOADS];
-  const int lr = lane >> 3, chunk = (lane & 7) ^ ((4 * wave + (lr >> 1)) & 7);
+  const uint8_t *from[C::LOADS], *sfrom[C::SLOADS + 1];
+  const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_chunk);
+  const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
   // kOpBf16T: weight row of the stage and column chunk that this lane stages.
   // Instructions are 4 rows or a multiple apart, so the slot does not depend on j.
-  const int lk = lane / (64 / C::KROWS), wk = wave * C::KROWS + lk;
-  const int wcol = min(n0 + 8 * ((lane % (64 / C::KROWS)) ^ ((wk & 3) << 2)), p.width - 8);
+  const int wk = wave * C::KROWS + lane / (64 / C::KROWS);
+  int32_t limit = p.chunks;  // chunks of the staged tile (0: there is none, and zeros are staged)
+  const auto aim = [&](const StagedTile &u, auto token) {
+    const int lane = fresh_lane(), lr = lane >> 3, chunk = (lane & 7) ^ ((4 * wave + (lr >> 1)) & 7);
+    const int wk = wave * C::KROWS + lane / (64 / C::KROWS);
+    // Weight row of tile row r.  With a gate/up pair the first half of each
+    // wave's rows are gate columns, the second half the same up columns.
+    const auto weight_row = [&](int r) -> int64_t {
+      if constexpr (PAIR) {
+        constexpr int PER = C::TN / C::WN, HALF = PER / 2;
+        const int q = r % PER;
+        const int32_t col = min(u.n0 + (r / PER) * HALF + q % HALF, p.width - 1);
+        return col + (q >= HALF ? p.width : 0);
+      }
+      return min(u.n0 + r, p.N - 1);
+    };
+    const uint8_t *we = p.w + u.e * p.w_expert;
+    const int wcol = min(u.n0 + 8 * ((lane % (64 / C::KROWS)) ^ ((wk & 3) << 2)), p.width - 8);
 #pragma unroll
-  for (int j = 0; j < C::LOADS; ++j) {
-    if (j < C::WLOADS && C::TRANS)
-      from[j] = p.w + t.e * p.w_expert + (wk + j * C::WAVES * C::KROWS) * p.w_row + 2 * wcol;
-    else if (j < C::WLOADS)
-      from[j] = p.w + t.e * p.w_expert + weight_row((j * C::WAVES + wave) * 8 + lr) * p.w_row + 16 * chunk;
-    else
-      from[j] = p.x + source(((j - C::WLOADS) * C::WAVES + wave) * 8 + lr) * p.x_row + 16 * chunk;
-  }
-  const uint8_t *sfrom[C::SLOADS + 1];
+    for (int j = 0; j < C::LOADS; ++j) {
+      if (j < C::WLOADS && C::TRANS)
+        from[j] = we + (wk + j * C::WAVES * C::KROWS) * p.w_row + 2 * wcol;
+      else if (j < C::WLOADS)
+        from[j] = we + weight_row((j * C::WAVES + wave) * 8 + lr) * p.w_row + 16 * chunk;
+      else
+        from[j] = p.x + token(((j - C::WLOADS) * C::WAVES + wave) * 8 + lr) * p.x_row + 16 * chunk;
+    }
 #pragma unroll
-  for (int j = 0; j < C::SLOADS; ++j) {
-    const int r = (j * C::WAVES + wave) * 32 + (lane >> 1);
-    if (r < C::TN)
-      sfrom[j] = p.w_scales + (static_cast<int64_t>(t.e) * p.N + weight_row(r)) * p.chunks + 4 * (lane & 1);
-    else
-      sfrom[j] = p.x_scales + source(r - C::TN) * p.chunks + 4 * (lane & 1);
-  }
+    for (int j = 0; j < C::SLOADS; ++j) {
+      const int r = (j * C::WAVES + wave) * 32 + (lane >> 1);
+      if (j * C::WAVES * 32 < C::TN)
+        sfrom[j] = p.w_scales + (static_cast<int64_t>(u.e) * p.N + weight_row(r)) * p.chunks + 4 * (lane & 1);
+      else
+        sfrom[j] = p.x_scales + token(r - C::TN) * p.chunks + 4 * (lane & 1);
+    }
+  };
 
   // Instruction j of stage s (the scales' behind the operands').  Lanes whose
   // chunk lies behind K stage zeros (a scale byte 0 is 2^-127).
-  const int stages = (p.chunks + 7) / 8;
-  const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_chunk);
   const auto fetch_one = [&](int s, uint8_t *base, auto jc) {
     constexpr int j = decltype(jc)::value;
     if constexpr (j >= C::LOADS) {
       constexpr int k = j - C::LOADS;
-      dma(8 * s + 4 * (lane & 1) < p.chunks ? sfrom[k] : zero, base + C::ROWS * 128 + (k * C::WAVES + wave) * 256, 4);
+      dma(8 * s + 4 * (lane & 1) < limit ? sfrom[k] : zero, base + C::ROWS * 128 + (k * C::WAVES + wave) * 256, 4);
       sfrom[k] += 8;
     } else if constexpr (C::TRANS && j < C::WLOADS) {
-      dma(64 * s + wk + j * C::WAVES * C::KROWS < 8 * p.chunks ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
+      dma(64 * s + wk + j * C::WAVES * C::KROWS < 8 * limit ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
       from[j] += 64 * p.w_row;
     } else {
-      dma(8 * s + chunk < p.chunks ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
+      dma(8 * s + chunk < limit ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
       from[j] += 128;
     }
+  };
+  // Token ids of a tile's rows into LDS: wave w brings rows 64 w ...
+  int32_t *tokens = reinterpret_cast<int32_t *>(lds + C::TOKENS);
+  const auto fetch_tokens = [&](const StagedTile &u) {
+    if (p.row_token == nullptr || u.e < 0) return;
+    dma(p.row_token + u.r0 + min(64 * wave + lane, u.rows - 1), tokens + 64 * wave, 4);
   };
 
   // Fragment addresses: row (lane % 32) of a 32-row group, chunk 4 half + s.
@@ -339,11 +410,11 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
   struct Scales {
     uint32_t a[C::NI], b[C::MI];
   };
+  constexpr int FRAGS = C::NI + C::MI, SLOTS = C::NI * C::MI;
   // Item r of a step's fragment reads, in the order the products need them:
   // a[0], all of b, then the other a; behind them a stage's scales.
   const auto read_item = [&](Frag &f, Scales &sf, const uint8_t *base, int s, auto rc) {
     constexpr int r = decltype(rc)::value;
-    constexpr int FRAGS = C::NI + C::MI;
     if constexpr (r >= FRAGS) {
       constexpr int k = r - FRAGS;
       const uint8_t *sb = base + C::ROWS * 128 + 4 * half;
@@ -356,30 +427,26 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
     } else {
       constexpr int i = r == 0 ? 0 : r - C::MI;
       if constexpr (C::TRANS) {
-        const uint8_t *at = base + tcol[i] + 8 * s * (2 * C::TN);
-        const uint2 lo = read_tr(at), hi = read_tr(at + 4 * (2 * C::TN));
+        const uint8_t *src = base + tcol[i] + 8 * s * (2 * C::TN);
+        const uint2 lo = read_tr(src), hi = read_tr(src + 4 * (2 * C::TN));
         f.a[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
       } else {
         f.a[i] = *reinterpret_cast<const uint4 *>(base + (arow + 32 * i) * 128 + 16 * ((4 * half + s) ^ ((fr >> 1) & 7)));
       }
     }
   };
-  constexpr int FRAGS = C::NI + C::MI, SLOTS = C::NI * C::MI;
 
   f32x16 acc[C::NI][C::MI];
-#pragma unroll
-  for (int i = 0; i < C::NI; ++i)
-#pragma unroll
-    for (int k = 0; k < C::MI; ++k) acc[i][k] = f32x16{};
   Scales sc;
+  Frag f0, f1;
   // One step: its products of `f`, with the reads of `g` (step gs of the stage
   // at gbase) and, in a stage's last step, the next stage's scales and the
   // staging of stage ds between them, in exactly this order.  Left to itself
   // the compiler puts the reads last, where the next step waits for them.
-  const auto step = [&](auto sel, const Frag &f, Frag &g, Scales &gsc, const uint8_t *gbase, int gs, auto last, int ds,
+  const auto step = [&](auto sel, const Frag &f, Frag &g, Scales &gsc, const uint8_t *gbase, int gs, int ds,
                         uint8_t *dbase) {
-    constexpr int S = decltype(sel)::value, DN = decltype(last)::value ? C::ALL : 0;
-    constexpr int READS = FRAGS + (C::MX && decltype(last)::value ? FRAGS : 0);
+    constexpr int S = decltype(sel)::value, DN = S == 3 ? C::ALL : 0;
+    constexpr int READS = FRAGS + (C::MX && S == 3 ? FRAGS : 0);
     constexpr int RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
     each<SLOTS>([&](auto slot) {
       constexpr int n = decltype(slot)::value, i = n / C::MI, k = n % C::MI;
@@ -398,68 +465,111 @@ __device__ __forceinline__ void staged_tile(const GroupedParams &p, const TileAt
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  const auto c0 = std::integral_constant<int, 0>{};
-  const auto c1 = std::integral_constant<int, 1>{};
-  const auto c2 = std::integral_constant<int, 2>{};
-  const auto c3 = std::integral_constant<int, 3>{};
-  // Stages behind the last are fetched as zeros that no one uses, so the loop
-  // is one block of code without branches: with one inside, the compiler sinks
-  // the products past all the reads.
-#pragma unroll
-  for (int s = 0; s < C::STAGES; ++s) each<C::ALL>([&](auto j) { fetch_one(s, lds + s * C::STAGE, j); });
-  wait_vm<(C::STAGES - 1) * C::ALL>();
-  barrier_no_fence();
-  Frag f0, f1;
-  each<FRAGS + (C::MX ? FRAGS : 0)>([&](auto r) { read_item(f0, sc, lds, 0, r); });
+  // One stage; meanwhile stage `ds` of whatever is aimed at goes into its LDS.
   uint8_t *cur = lds;
-  for (int s = 0; s < stages; ++s) {
-    uint8_t *nxt = cur == lds + (C::STAGES - 1) * C::STAGE ? lds : cur + C::STAGE;
-    step(c0, f0, f1, sc, cur, 1, c0, 0, cur);
-    step(c1, f1, f0, sc, cur, 2, c0, 0, cur);
-    step(c2, f0, f1, sc, cur, 3, c0, 0, cur);
+  const auto stage = [&](int ds) {
+    uint8_t *nxt = lds + (cur == lds ? C::STAGE : 0);
+    step(std::integral_constant<int, 0>{}, f0, f1, sc, cur, 1, 0, cur);
+    step(std::integral_constant<int, 1>{}, f1, f0, sc, cur, 2, 0, cur);
+    step(std::integral_constant<int, 2>{}, f0, f1, sc, cur, 3, 0, cur);
     wait_lgkm0();  // step 3's fragments are in registers: this wave is done with the stage's LDS
-    wait_vm<(C::STAGES - 2) * C::ALL>();  // and its part of the next stage has landed
+    wait_vm<0>();  // and its part of the next stage has landed
     barrier_no_fence();
     Scales next;
-    step(c3, f1, f0, next, nxt, 0, c1, s + C::STAGES, cur);
+    step(std::integral_constant<int, 3>{}, f1, f0, next, nxt, 0, ds, cur);
     if constexpr (C::MX) sc = next;
     cur = nxt;
-  }
-  wait_vm<0>();
+  };
 
-  uint8_t *turn = lds + C::STAGES * C::STAGE + wave * kTurnBytes;
+  const int stages = max((p.chunks + 7) / 8, 2);  // at least both buffers: one of zeros for a short K
+  aim(t, [&](int r) -> int64_t { return source_row(p, t.r0 + min(r, t.rows - 1)); });
+  each<C::ALL>([&](auto j) { fetch_one(0, lds, j); });
+  each<C::ALL>([&](auto j) { fetch_one(1, lds + C::STAGE, j); });
+  StagedTile nt;
+  advance(nt, t.e);
+  wait_vm<C::ALL>();
+  barrier_no_fence();
+  each<FRAGS + (C::MX ? FRAGS : 0)>([&](auto r) { read_item(f0, sc, lds, 0, r); });
+  fetch_tokens(nt);
+
 #pragma unroll
-  for (int k = 0; k < C::MI; ++k) {
-    f32x16 col[C::NI];
+  for (int i = 0; i < C::NI; ++i)
 #pragma unroll
-    for (int i = 0; i < C::NI; ++i) col[i] = acc[i][k];
-    const int m = wm * (C::TM / C::WM) + 32 * k;
-    store_block<EPI, C::NI>(p, col, turn, static_cast<int64_t>(t.r0) + m, t.rows - m,
-                            n0 + wn * (C::TN / C::WN) / (PAIR ? 2 : 1));
+    for (int k = 0; k < C::MI; ++k) acc[i][k] = f32x16{};
+  // A stage is one block of code without branches: with one inside, the
+  // compiler sinks the products past all the reads.
+  // Names every accumulator as an accumulation register where the loops meet
+  // (no instruction): the compiler otherwise carries them in ordinary
+  // registers and copies all of them twice a stage.
+  const auto pin = [&] {
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i)
+#pragma unroll
+      for (int k = 0; k < C::MI; ++k) asm volatile("" : "+a"(acc[i][k]));
+  };
+  while (true) {
+    for (int s = 2; s < stages; ++s) {
+      pin();
+      stage(s);
+    }
+    pin();
+    if (stages == 2) {  // no barrier since the tokens were sent for
+      wait_vm<0>();
+      barrier_no_fence();
+    }
+    // The last two stages bring the next tile's first two.
+    limit = nt.e < 0 ? 0 : p.chunks;
+    if (nt.e >= 0)
+      aim(nt, [&](int r) -> int64_t {
+        const int m = min(r, nt.rows - 1);
+        return p.row_token ? tokens[m] : nt.r0 + m;
+      });
+    for (int s = 0; s < 2; ++s) {
+      pin();
+      stage(s);
+    }
+    pin();
+    uint8_t *turn = lds + C::TURN + wave * kTurnBytes;
+    const int fl = fresh_lane();
+#pragma unroll
+    for (int k = 0; k < C::MI; ++k) {
+      f32x16 col[C::NI];
+#pragma unroll
+      for (int i = 0; i < C::NI; ++i) {
+        asm volatile("" : "+a"(acc[i][k]));  // not read before its turn
+        col[i] = acc[i][k];
+      }
+      const int m = wm * (C::TM / C::WM) + 32 * k;
+      store_block<EPI, C::NI>(p, col, turn, fl, static_cast<int64_t>(t.r0) + m, t.rows - m,
+                              t.n0 + wn * (C::TN / C::WN) / (PAIR ? 2 : 1));
+#pragma unroll
+      for (int i = 0; i < C::NI; ++i) acc[i][k] = f32x16{};
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (nt.e < 0) break;
+    t = nt;
+    advance(nt, t.e);
+    fetch_tokens(nt);
   }
+  wait_vm<0>();  // nothing of this workgroup writes LDS after its end
 }
 
-// One tile a workgroup.  Dispatch is round-robin over the 8 XCDs; each XCD
-// takes a contiguous eighth of the tiles (columns fastest), so the tiles that
-// share an expert's weights and a row tile's activations share an L2.
 template <class C, int EPI>
 __global__ __launch_bounds__(C::THREADS, 1) void k_grouped_staged(GroupedParams p, int col_tiles) {
-  __shared__ __attribute__((aligned(128))) uint8_t lds[C::STAGES * C::STAGE + C::WAVES * kTurnBytes];
-  const TileAt all = find_tile<C::TM>(p.offsets, p.E, 0x7FFFFFFF);
-  const int64_t tiles = static_cast<int64_t>(all.total) * col_tiles, per = (tiles + 7) / 8;
-  const int64_t at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= per || at >= tiles) return;
-  const TileAt t = find_tile<C::TM>(p.offsets, p.E, static_cast<int>(at / col_tiles));
-  constexpr int COLS = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? C::TN / 2 : C::TN;
-  staged_tile<C, EPI>(p, t, static_cast<int32_t>(at % col_tiles) * COLS, lds);
+  __shared__ __attribute__((aligned(128))) uint8_t lds[C::LDS];
+  staged_tiles<C, EPI>(p, lds, static_cast<uint32_t>(col_tiles));
 }
 
+// Workgroups: as many as run at once (PER_CU on each of the 256 CUs), or one
+// for each tile if there are fewer.
 template <class C, int EPI>
 hipError_t launch_staged(const GroupedParams &p, int64_t R, hipStream_t stream) {
   constexpr int COLS = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? C::TN / 2 : C::TN;
+  constexpr int PER_CU = C::LDS <= 81920 ? 2 : 1;
   const int64_t cols = (p.width + COLS - 1) / COLS;
-  const int64_t grid = (max_row_tiles(R, p.E, C::TM) * cols + 7) / 8 * 8;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const int64_t tiles = (max_row_tiles(R, p.E, C::TM) * cols + 7) / 8 * 8;
+  if (tiles > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const int64_t grid = tiles < 256 * PER_CU ? tiles : 256 * PER_CU;
   hipLaunchKernelGGL((k_grouped_staged<C, EPI>), dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), 0, stream, p,
                      static_cast<int>(cols));
   return hipGetLastError();

@@ -48,6 +48,7 @@ struct TileAt {
   int32_t r0;     // first routed row
   int32_t rows;   // rows of this tile (1 .. TM)
   int32_t total;  // row tiles of all experts
+  int32_t before;  // row tiles of the experts before e
 };
 
 // Row tile `index` of the grouping: experts' rows are cut into tiles of TM.
@@ -76,6 +77,7 @@ __device__ __forceinline__ TileAt find_tile(const int32_t *offsets, int E, int i
   t.e = -1;
   t.r0 = 0;
   t.rows = 0;
+  t.before = 0;
   if (index >= t.total) return t;
   const uint64_t past = __ballot(sum > index);
   const int owner = __builtin_ctzll(past);
@@ -87,6 +89,7 @@ __device__ __forceinline__ TileAt find_tile(const int32_t *offsets, int E, int i
     const int32_t n = (last - first + TM - 1) / TM;
     if (index < at + n) {
       t.e = e;
+      t.before = at;
       t.r0 = first + (index - at) * TM;
       t.rows = min(last - t.r0, static_cast<int32_t>(TM));
       break;
@@ -97,6 +100,7 @@ __device__ __forceinline__ TileAt find_tile(const int32_t *offsets, int E, int i
   t.e = __builtin_amdgcn_readfirstlane(t.e);  // the same in every lane: into scalar registers
   t.r0 = __builtin_amdgcn_readfirstlane(t.r0);
   t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+  t.before = __builtin_amdgcn_readfirstlane(t.before);
   return t;
 }
 
@@ -132,7 +136,7 @@ __device__ __forceinline__ uint2 both_halves(uint32_t v) {
 
 // Requantizes one 32-column block of 32 rows held as h[16] per lane.  Codes
 // go to `codes` + 16 bytes of the block, the scale byte to *scale.
-__device__ __forceinline__ void store_mx_block(const float (&h)[16], bool row_ok, uint8_t *codes, uint8_t *scale) {
+__device__ __forceinline__ void store_mx_block(const float (&h)[16], int lane, bool row_ok, uint8_t *codes, uint8_t *scale) {
   uint32_t a = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) a = max(a, __float_as_uint(h[i]) & 0x7FFFFFFFu);
@@ -153,7 +157,7 @@ __device__ __forceinline__ void store_mx_block(const float (&h)[16], bool row_ok
   const auto r = __builtin_amdgcn_permlane32_swap(lo, hi, false, false);
   const uint32_t d0 = (r[0] & 0xFFFFu) | (r[1] << 16), d1 = (r[0] >> 16) | (r[1] & 0xFFFF0000u);
   if (row_ok) {
-    const int half = (threadIdx.x & 63) >> 5;
+    const int half = lane >> 5;
     *reinterpret_cast<uint2 *>(codes + 8 * half) = make_uint2(d0, d1);
     if (half == 0) *scale = static_cast<uint8_t>(s);
   }
@@ -184,7 +188,7 @@ __device__ __forceinline__ void store_tile(const GroupedParams &p, const f32x16 
 #pragma unroll
     for (int i = 0; i < 16; ++i) h[i] = silu(a[i]) * b[i];
     if (n0 >= p.width) return;
-    store_mx_block(h, row_ok, static_cast<uint8_t *>(p.y) + row * (p.width >> 1) + (n0 >> 1),
+    store_mx_block(h, threadIdx.x & 63, row_ok, static_cast<uint8_t *>(p.y) + row * (p.width >> 1) + (n0 >> 1),
                    static_cast<uint8_t *>(p.y2) + row * (p.width >> 5) + (n0 >> 5));
   } else {
     if (!row_ok) return;
