@@ -1,9 +1,22 @@
-// Grouped GEMM without LDS: every wave computes one 32 x 32 tile (two with a
-// SwiGLU epilogue) and loads its MFMA fragments straight from memory.  Right
-// for every size the entry points accept; used where the staged kernels do
-// not apply.
+// Grouped GEMM that streams its operands from memory into the MFMA fragments,
+// for few rows per expert (decode) and for every size that the staged kernel
+// does not take.  Bound: reading the weights once.
+//
+// An item is 32 routed rows of an expert times two 32-column tiles (the gate
+// and up tile of the same columns with the SwiGLU epilogues).  A workgroup's
+// four waves split its contraction: wave w takes the stages w, w + 4, ... of
+// 128 bytes, so that together they read 512 contiguous bytes of every weight
+// row.  In a stage lanes 0-31 take the first 64 bytes of their row and lanes
+// 32-63 the second: every line is read whole by four consecutive loads.  The
+// partial sums meet in LDS and are added in wave order, by another wave for
+// each item in turn.
+//
+// Workgroups stay (two a CU) and take consecutive items, mostly the columns of
+// one row tile.  Each wave has its next stage in flight while it multiplies
+// one, across items and their barrier too: what keeps HBM busy.
 #pragma once
 
+#include "dma.hpp"
 #include "grouped_tile.hpp"
 
 namespace quads {
@@ -14,58 +27,185 @@ enum GroupedOperands {
   kOpBf16T = 2  // bf16 rows, weights [E, K, N] (contraction along the weights' rows)
 };
 
-constexpr int kDirectWaves = 4;
+constexpr int kSplit = 4;  // waves of a workgroup
+
+// A lane's operands of one stage: four 16-byte chunks of each row, and their
+// scales as one dword.
+struct DirectStage {
+  uint4 a[4], a2[4], b[4];
+  uint32_t sa, sa2, sb;
+};
 
 template <int OP, int EPI>
-__global__ __launch_bounds__(64 * kDirectWaves) void k_grouped_direct(GroupedParams p, int col_groups) {
-  const TileAt t = find_tile<32>(p.offsets, p.E, static_cast<int>(blockIdx.x / col_groups));
-  if (t.e < 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-  const int32_t n0 = (static_cast<int32_t>(blockIdx.x % col_groups) * kDirectWaves + wave) * 32;
-  if (n0 >= p.width) return;
+__global__ __launch_bounds__(64 * kSplit, 2) void k_grouped_direct(GroupedParams p, int col_groups) {
   constexpr bool PAIR = EPI == kEpiSwiglu || EPI == kEpiSwigluMx;
-  const int32_t n = min(n0 + (lane & 31), p.width - 1);
-  const int64_t row = t.r0 + min(lane & 31, t.rows - 1);
-  const int64_t src = source_row(p, static_cast<int32_t>(row));
-  const uint8_t *xr = p.x + src * p.x_row;
-  const uint8_t *we = p.w + t.e * p.w_expert;
-  const int64_t up = static_cast<int64_t>(p.width) * p.w_row;
-  const uint8_t *wr = OP == kOpBf16T ? we + 2 * static_cast<int64_t>(n) : we + n * p.w_row;
-  const uint8_t *xs = nullptr, *ws = nullptr;
-  if constexpr (OP == kOpMx) {
+  constexpr int COLS = PAIR ? 32 : 64;
+  __shared__ float partial[2][kSplit][32][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+
+  // This workgroup's items: at .. end - 1.  Workgroups are dealt to the 8 XCDs
+  // in turn; neighbouring items share an XCD's L2.
+  const uint32_t items = count_tiles<32>(p.offsets, p.E) * static_cast<uint32_t>(col_groups);
+  const uint32_t per = (items + gridDim.x - 1) / gridDim.x;
+  uint32_t at = ((blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3)) * per;
+  const uint32_t end = min(items, at + per);
+  if (at >= end) return;
+  uint32_t tile = at / col_groups, group = at % col_groups;
+  const TileAt t0 = find_tile<32>(p.offsets, p.E, static_cast<int>(tile));
+  Walker walk(p.offsets, t0);
+  int32_t r0 = t0.r0, rows = t0.rows;
+
+  const int stages = (p.chunks + 7) / 8, rounds = (stages + kSplit - 1) / kSplit;
+  const bool dwords = p.chunks % 4 == 0;  // scale rows are dword-aligned
+
+  // Sources of the item that is being loaded.
+  const uint8_t *xr, *xs, *wr, *wr2, *ws, *ws2;
+  const auto aim_rows = [&] {
+    const int64_t src = source_row(p, r0 + min(lane & 31, rows - 1));
+    xr = p.x + src * p.x_row;
     xs = p.x_scales + src * p.chunks;
-    ws = p.w_scales + (static_cast<int64_t>(t.e) * p.N + n) * p.chunks;
-  }
-  f32x16 acc = {}, acc2 = {};
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const int steps = (p.chunks + 1) / 2;
-  for (int s = 0; s < steps; ++s) {
-    const int c = 2 * s + half;
-    const bool in = c < p.chunks;
-    const int cc = in ? c : 0;
-    uint4 b = *reinterpret_cast<const uint4 *>(xr + 16 * static_cast<int64_t>(cc)), a, a2 = zero;
+  };
+  const auto aim_columns = [&] {
+    const int32_t n = static_cast<int32_t>(group) * COLS + (lane & 31);
+    const int64_t a = min(n, p.width - 1), b = PAIR ? a + p.width : min(n + 32, p.width - 1);
+    const uint8_t *we = p.w + walk.e * p.w_expert;
     if constexpr (OP == kOpBf16T) {
-      uint32_t h[8];
+      wr = we + 2 * a;
+      wr2 = we + 2 * b;
+    } else {
+      wr = we + a * p.w_row;
+      wr2 = we + b * p.w_row;
+      ws = p.w_scales + (static_cast<int64_t>(walk.e) * p.N + a) * p.chunks;
+      ws2 = p.w_scales + (static_cast<int64_t>(walk.e) * p.N + b) * p.chunks;
+    }
+  };
+
+  // Chunks behind K are zeros with scale 2^0; the load is of chunk 0.
+  const auto load = [&](DirectStage &r, int s) {
+    const int c0 = 8 * s + 4 * half;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = *reinterpret_cast<const uint16_t *>(wr + (8 * static_cast<int64_t>(cc) + j) * p.w_row);
-      a = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-    } else {
-      a = *reinterpret_cast<const uint4 *>(wr + 16 * static_cast<int64_t>(cc));
-      if constexpr (PAIR) a2 = *reinterpret_cast<const uint4 *>(wr + up + 16 * static_cast<int64_t>(cc));
+    for (int j = 0; j < 4; ++j) {
+      const bool in = c0 + j < p.chunks;
+      const int64_t c = in ? c0 + j : 0;
+      const uint4 b = *reinterpret_cast<const uint4 *>(xr + 16 * c);
+      r.b[j] = in ? b : zero;
+      if constexpr (OP == kOpBf16T) {
+        uint32_t h[8], g[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          h[i] = *reinterpret_cast<const uint16_t *>(wr + (8 * c + i) * p.w_row);
+          g[i] = *reinterpret_cast<const uint16_t *>(wr2 + (8 * c + i) * p.w_row);
+        }
+        r.a[j] = in ? make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16) : zero;
+        r.a2[j] = in ? make_uint4(g[0] | g[1] << 16, g[2] | g[3] << 16, g[4] | g[5] << 16, g[6] | g[7] << 16) : zero;
+      } else {
+        const uint4 a = *reinterpret_cast<const uint4 *>(wr + 16 * c);
+        const uint4 a2 = *reinterpret_cast<const uint4 *>(wr2 + 16 * c);
+        r.a[j] = in ? a : zero;
+        r.a2[j] = in ? a2 : zero;
+      }
     }
-    if (!in) a = a2 = b = zero;
     if constexpr (OP == kOpMx) {
-      uint32_t sb = xs[cc], sa = ws[cc], sa2 = 0;
-      if constexpr (PAIR) sa2 = ws[static_cast<int64_t>(p.width) * p.chunks + cc];
-      if (!in) sa = sa2 = sb = 127;  // 2^0
-      acc = mfma_mx<0>(a, b, acc, sa, sb);
-      if constexpr (PAIR) acc2 = mfma_mx<0>(a2, b, acc2, sa2, sb);
-    } else {
-      acc = mfma_bf16(a, b, acc);
-      if constexpr (PAIR) acc2 = mfma_bf16(a2, b, acc2);
+      constexpr uint32_t ones = 0x7F7F7F7Fu;
+      if (dwords) {
+        const bool in = c0 < p.chunks;
+        const int c = in ? c0 : 0;
+        const uint32_t sb = *reinterpret_cast<const uint32_t *>(xs + c), sa = *reinterpret_cast<const uint32_t *>(ws + c),
+                       sa2 = *reinterpret_cast<const uint32_t *>(ws2 + c);
+        r.sb = in ? sb : ones;
+        r.sa = in ? sa : ones;
+        r.sa2 = in ? sa2 : ones;
+      } else {
+        r.sa = r.sb = r.sa2 = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = c0 + j < p.chunks;
+          const int c = in ? c0 + j : 0;
+          r.sb |= (in ? xs[c] : 127u) << (8 * j);
+          r.sa |= (in ? ws[c] : 127u) << (8 * j);
+          r.sa2 |= (in ? ws2[c] : 127u) << (8 * j);
+        }
+      }
     }
+  };
+  f32x16 acc = {}, acc2 = {};
+  const auto multiply = [&](const DirectStage &r) {
+    if constexpr (OP == kOpMx) {
+      acc = mfma_mx<0>(r.a[0], r.b[0], acc, r.sa, r.sb);
+      acc2 = mfma_mx<0>(r.a2[0], r.b[0], acc2, r.sa2, r.sb);
+      acc = mfma_mx<1>(r.a[1], r.b[1], acc, r.sa, r.sb);
+      acc2 = mfma_mx<1>(r.a2[1], r.b[1], acc2, r.sa2, r.sb);
+      acc = mfma_mx<2>(r.a[2], r.b[2], acc, r.sa, r.sb);
+      acc2 = mfma_mx<2>(r.a2[2], r.b[2], acc2, r.sa2, r.sb);
+      acc = mfma_mx<3>(r.a[3], r.b[3], acc, r.sa, r.sb);
+      acc2 = mfma_mx<3>(r.a2[3], r.b[3], acc2, r.sa2, r.sb);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc = mfma_bf16(r.a[j], r.b[j], acc);
+        acc2 = mfma_bf16(r.a2[j], r.b[j], acc2);
+      }
+    }
+  };
+
+  int round = 0, count = 0;
+  // Multiplies `now`, the stage of this round, with the following one (the
+  // next item's first behind the last round) on its way into `next`.  False
+  // after the last item.
+  const auto step = [&](const DirectStage &now, DirectStage &next) -> bool {
+    const bool item_done = round + 1 == rounds;
+    const int64_t out_row = static_cast<int64_t>(r0) + (lane & 31);
+    const bool row_ok = (lane & 31) < rows;
+    const int32_t n0 = static_cast<int32_t>(group) * COLS;
+    const bool more = at + 1 < end;
+    if (!item_done) {
+      load(next, wave + (round + 1) * kSplit);
+    } else if (more) {
+      if (++group == static_cast<uint32_t>(col_groups)) {
+        group = 0;
+        walk.to<32>(static_cast<int32_t>(++tile), r0, rows);
+        aim_rows();
+      }
+      aim_columns();
+      load(next, wave);
+    }
+    multiply(now);
+    ++round;
+    if (!item_done) return true;
+    // Two buffers: one barrier an item suffices, since whoever adds up an
+    // item's sums joins the next item's barrier after that.
+    float(*sum)[32][64] = partial[count & 1];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      sum[wave][i][lane] = acc[i];
+      sum[wave][16 + i][lane] = acc2[i];
+    }
+    wait_lgkm0();
+    barrier_no_fence();
+    if (wave == (count & (kSplit - 1))) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        acc[i] = ((sum[0][i][lane] + sum[1][i][lane]) + sum[2][i][lane]) + sum[3][i][lane];
+        acc2[i] = ((sum[0][16 + i][lane] + sum[1][16 + i][lane]) + sum[2][16 + i][lane]) + sum[3][16 + i][lane];
+      }
+      store_tile<EPI>(p, acc, acc2, out_row, row_ok, n0);
+      if constexpr (!PAIR) store_tile<EPI>(p, acc2, acc, out_row, row_ok, n0 + 32);
+    }
+    acc = f32x16{};
+    acc2 = f32x16{};
+    round = 0;
+    ++count;
+    ++at;
+    return more;
+  };
+
+  DirectStage s0, s1;
+  aim_rows();
+  aim_columns();
+  load(s0, wave);
+  while (step(s0, s1) && step(s1, s0)) {
   }
-  store_tile<EPI>(p, acc, acc2, t.r0 + (lane & 31), (lane & 31) < t.rows, n0);
 }
 
 // Most row tiles of TM rows that R rows in E groups can give.
@@ -73,11 +213,13 @@ inline int64_t max_row_tiles(int64_t R, int E, int TM) { return R / TM + (R < E 
 
 template <int OP, int EPI>
 hipError_t launch_direct(const GroupedParams &p, int64_t R, hipStream_t stream) {
-  const int64_t groups = (p.width + 32 * kDirectWaves - 1) / (32 * kDirectWaves);
-  const int64_t grid = max_row_tiles(R, p.E, 32) * groups;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((k_grouped_direct<OP, EPI>), dim3(static_cast<unsigned>(grid)), dim3(64 * kDirectWaves), 0, stream,
-                     p, static_cast<int>(groups));
+  constexpr int COLS = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? 32 : 64;
+  const int64_t groups = (p.width + COLS - 1) / COLS;
+  const int64_t items = (max_row_tiles(R, p.E, 32) * groups + 7) / 8 * 8;
+  if (items > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const int64_t grid = items < 512 ? items : 512;  // two workgroups on each of the 256 CUs
+  hipLaunchKernelGGL((k_grouped_direct<OP, EPI>), dim3(static_cast<unsigned>(grid)), dim3(64 * kSplit), 0, stream, p,
+                     static_cast<int>(groups));
   return hipGetLastError();
 }
 

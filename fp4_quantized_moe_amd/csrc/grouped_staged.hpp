@@ -47,6 +47,7 @@ __device__ __forceinline__ void each(F &&f) {
   each_index(static_cast<F &&>(f), std::make_integer_sequence<int, N>{});
 }
 
+constexpr int D3 = 12, D0 = 4;
 constexpr int kTurnBytes = 4096;  // a wave's epilogue block: 32 rows of 128 bytes
 
 template <int OP_, int TM_, int TN_, int WM_, int WN_>
@@ -65,6 +66,9 @@ struct StagedCfg {
   static constexpr int LDS = TOKENS + 256 * WAVES;
   static constexpr int STAGE = ROWS * 128 + (MX ? ROWS * 8 : 0);
   static constexpr int ALL = LOADS + SLOADS;
+  // Staging instructions issued in a stage's last step, in the next stage's
+  // first and in its second.
+  static constexpr int IN3 = ALL * D3 / 16, IN0 = ALL * D0 / 16, IN1 = ALL - IN3 - IN0;
   static_assert(!MX || (TN % (32 * WAVES) == 0 && TM % (32 * WAVES) == 0), "a scale instruction reads one operand");
   static_assert(WAVES * KROWS % 4 == 0 || !TRANS, "slots of kOpBf16T");
   static_assert(64 * WAVES >= TM, "token ids of a tile");
@@ -285,44 +289,19 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   const int wn = wave / C::WM, wm = wave % C::WM;
 
   // The tiles of this workgroup: at, at + step, ... below end.
-  typedef const __attribute__((address_space(4))) int32_t uniform_i32;  // read by scalar loads
-  uniform_i32 *offsets = (uniform_i32 *)reinterpret_cast<uintptr_t>(p.offsets);
-  StagedTile t;
-  uint32_t at, end;
-  const uint32_t step_tiles = gridDim.x / 8;
-  int32_t before, first, last;  // expert t.e: row tiles before it, its rows
-  {
-    const int32_t total = find_tile<C::TM>(p.offsets, p.E, 0x7FFFFFFF).total;
-    const uint32_t tiles = total * col_tiles, per = (tiles + 7) / 8;
-    at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    end = min(tiles, ((blockIdx.x & 7) + 1) * per);
-    if (at >= end) return;
-    const TileAt f = find_tile<C::TM>(p.offsets, p.E, static_cast<int>(at / col_tiles));
-    t.e = f.e;
-    t.r0 = f.r0;
-    t.rows = f.rows;
-    t.n0 = static_cast<int32_t>(at % col_tiles) * COLS;
-    before = f.before;
-    first = offsets[f.e];
-    last = offsets[f.e + 1];
-  }
-  const auto advance = [&](StagedTile &u, int e) {  // the next tile, whose expert is e or a later one
+  const uint32_t tiles = count_tiles<C::TM>(p.offsets, p.E) * col_tiles, per = (tiles + 7) / 8;
+  const uint32_t step_tiles = gridDim.x / 8, end = min(tiles, ((blockIdx.x & 7) + 1) * per);
+  uint32_t at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (at >= end) return;
+  const TileAt t0 = find_tile<C::TM>(p.offsets, p.E, static_cast<int>(at / col_tiles));
+  Walker walk(p.offsets, t0);
+  StagedTile t{t0.e, t0.r0, t0.rows, static_cast<int32_t>(at % col_tiles) * COLS};
+  const auto advance = [&](StagedTile &u) {
     at += step_tiles;
-    u.e = -1;
-    u.r0 = u.rows = u.n0 = 0;
+    u = StagedTile{-1, 0, 0, 0};
     if (at >= end) return;
-    const int32_t rt = static_cast<int32_t>(at / col_tiles);
-    int32_t n = (last - first + C::TM - 1) / C::TM;
-    while (rt >= before + n) {
-      before += n;
-      ++e;
-      first = last;
-      last = offsets[e + 1];
-      n = (last - first + C::TM - 1) / C::TM;
-    }
-    u.e = e;
-    u.r0 = first + (rt - before) * C::TM;
-    u.rows = min(last - u.r0, static_cast<int32_t>(C::TM));
+    walk.to<C::TM>(static_cast<int32_t>(at / col_tiles), u.r0, u.rows);
+    u.e = walk.e;
     u.n0 = static_cast<int32_t>(at % col_tiles) * COLS;
   };
 
@@ -445,7 +424,9 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   // the compiler puts the reads last, where the next step waits for them.
   const auto step = [&](auto sel, const Frag &f, Frag &g, Scales &gsc, const uint8_t *gbase, int gs, int ds,
                         uint8_t *dbase) {
-    constexpr int S = decltype(sel)::value, DN = S == 3 ? C::ALL : 0;
+    constexpr int S = decltype(sel)::value;
+    constexpr int DN = S == 3 ? C::IN3 : S == 0 ? C::IN0 : S == 1 ? C::IN1 : 0;
+    constexpr int DF = S == 3 ? 0 : S == 0 ? C::IN3 : C::IN3 + C::IN0;
     constexpr int READS = FRAGS + (C::MX && S == 3 ? FRAGS : 0);
     constexpr int RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
     each<SLOTS>([&](auto slot) {
@@ -460,17 +441,20 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
       });
       each<DPS>([&](auto q) {
         constexpr int d = n * DPS + decltype(q)::value;
-        if constexpr (d < DN) fetch_one(ds, dbase, std::integral_constant<int, d>{});
+        if constexpr (d < DN) fetch_one(ds, dbase, std::integral_constant<int, DF + d>{});
       });
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  // One stage; meanwhile stage `ds` of whatever is aimed at goes into its LDS.
+  // One stage.  The rest of stage `now`, which the last step before began to
+  // bring, goes on in its first steps, and stage `ds` begins in its last;
+  // `between` may aim at another tile.
   uint8_t *cur = lds;
-  const auto stage = [&](int ds) {
+  const auto stage = [&](int now, int ds, auto between) {
     uint8_t *nxt = lds + (cur == lds ? C::STAGE : 0);
-    step(std::integral_constant<int, 0>{}, f0, f1, sc, cur, 1, 0, cur);
-    step(std::integral_constant<int, 1>{}, f1, f0, sc, cur, 2, 0, cur);
+    step(std::integral_constant<int, 0>{}, f0, f1, sc, cur, 1, now, nxt);
+    step(std::integral_constant<int, 1>{}, f1, f0, sc, cur, 2, now, nxt);
+    between();
     step(std::integral_constant<int, 2>{}, f0, f1, sc, cur, 3, 0, cur);
     wait_lgkm0();  // step 3's fragments are in registers: this wave is done with the stage's LDS
     wait_vm<0>();  // and its part of the next stage has landed
@@ -484,10 +468,10 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   const int stages = max((p.chunks + 7) / 8, 2);  // at least both buffers: one of zeros for a short K
   aim(t, [&](int r) -> int64_t { return source_row(p, t.r0 + min(r, t.rows - 1)); });
   each<C::ALL>([&](auto j) { fetch_one(0, lds, j); });
-  each<C::ALL>([&](auto j) { fetch_one(1, lds + C::STAGE, j); });
+  each<C::IN3>([&](auto j) { fetch_one(1, lds + C::STAGE, j); });
   StagedTile nt;
-  advance(nt, t.e);
-  wait_vm<C::ALL>();
+  advance(nt);
+  wait_vm<C::IN3>();
   barrier_no_fence();
   each<FRAGS + (C::MX ? FRAGS : 0)>([&](auto r) { read_item(f0, sc, lds, 0, r); });
   fetch_tokens(nt);
@@ -510,7 +494,7 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   while (true) {
     for (int s = 2; s < stages; ++s) {
       pin();
-      stage(s);
+      stage(s - 1, s, [] {});
     }
     pin();
     if (stages == 2) {  // no barrier since the tokens were sent for
@@ -518,16 +502,16 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
       barrier_no_fence();
     }
     // The last two stages bring the next tile's first two.
-    limit = nt.e < 0 ? 0 : p.chunks;
-    if (nt.e >= 0)
-      aim(nt, [&](int r) -> int64_t {
-        const int m = min(r, nt.rows - 1);
-        return p.row_token ? tokens[m] : nt.r0 + m;
-      });
-    for (int s = 0; s < 2; ++s) {
-      pin();
-      stage(s);
-    }
+    stage(stages - 1, 0, [&] {
+      limit = nt.e < 0 ? 0 : p.chunks;
+      if (nt.e >= 0)
+        aim(nt, [&](int r) -> int64_t {
+          const int m = min(r, nt.rows - 1);
+          return p.row_token ? tokens[m] : nt.r0 + m;
+        });
+    });
+    pin();
+    stage(0, 1, [] {});
     pin();
     uint8_t *turn = lds + C::TURN + wave * kTurnBytes;
     const int fl = fresh_lane();
@@ -548,7 +532,7 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
     }
     if (nt.e < 0) break;
     t = nt;
-    advance(nt, t.e);
+    advance(nt);
     fetch_tokens(nt);
   }
   wait_vm<0>();  // nothing of this workgroup writes LDS after its end

@@ -52,57 +52,58 @@ struct TileAt {
 };
 
 // Row tile `index` of the grouping: experts' rows are cut into tiles of TM.
-// Every wave finds it alone: lane l sums the tiles of its E / 64 experts, a
-// wave scan gives their starts.  offsets is non-decreasing.
+// Every wave finds it alone: 64 experts at a time, one a lane, a wave scan of
+// their tiles.  offsets is non-decreasing.
 template <int TM>
 __device__ __forceinline__ TileAt find_tile(const int32_t *offsets, int E, int index) {
   const int lane = threadIdx.x & 63;
-  const int per = (E + 63) >> 6;
-  const int a = min(lane * per, E), b = min(a + per, E);
-  int32_t mine = 0;
-  int32_t lo = a < b ? offsets[a] : 0;
-  for (int e = a; e < b; ++e) {
-    const int32_t hi = offsets[e + 1];
-    mine += (hi - lo + TM - 1) / TM;
-    lo = hi;
-  }
-  int32_t sum = mine;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int32_t o = __shfl_up(sum, off);
-    if (lane >= off) sum += o;
-  }
-  TileAt t;
-  t.total = __builtin_amdgcn_readlane(sum, 63);
-  t.e = -1;
-  t.r0 = 0;
-  t.rows = 0;
-  t.before = 0;
-  if (index >= t.total) return t;
-  const uint64_t past = __ballot(sum > index);
-  const int owner = __builtin_ctzll(past);
-  int32_t at = __builtin_amdgcn_readlane(sum - mine, owner);
-  const int e0 = owner * per;
-  int32_t first = offsets[e0];
-  for (int e = e0; e < E; ++e) {  // at most `per` rounds: the owner's experts hold the tile
-    const int32_t last = offsets[e + 1];
-    const int32_t n = (last - first + TM - 1) / TM;
-    if (index < at + n) {
-      t.e = e;
-      t.before = at;
-      t.r0 = first + (index - at) * TM;
-      t.rows = min(last - t.r0, static_cast<int32_t>(TM));
-      break;
+  TileAt t{-1, 0, 0, 0, 0};
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    const int32_t lo = offsets[min(e, E)], hi = offsets[min(e + 1, E)];
+    const int32_t n = (hi - lo + TM - 1) / TM;
+    const int32_t end = t.total + static_cast<int32_t>(wave_scan<false>(static_cast<uint32_t>(n)));
+    const uint64_t here = __ballot(index >= end - n && index < end);
+    if (here) {
+      const int owner = __builtin_ctzll(here);
+      t.e = e0 + owner;
+      t.before = __builtin_amdgcn_readlane(end - n, owner);
+      t.r0 = __builtin_amdgcn_readlane(lo, owner) + (index - t.before) * TM;
+      t.rows = min(__builtin_amdgcn_readlane(hi, owner) - t.r0, static_cast<int32_t>(TM));
     }
-    at += n;
-    first = last;
+    t.total = __builtin_amdgcn_readlane(end, 63);
   }
-  t.e = __builtin_amdgcn_readfirstlane(t.e);  // the same in every lane: into scalar registers
-  t.r0 = __builtin_amdgcn_readfirstlane(t.r0);
-  t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-  t.before = __builtin_amdgcn_readfirstlane(t.before);
   return t;
 }
+
+// All row tiles.
+template <int TM>
+__device__ __forceinline__ int32_t count_tiles(const int32_t *offsets, int E) {
+  return find_tile<TM>(offsets, E, -1).total;
+}
+
+// Row tiles in increasing order, without scans: experts are walked by scalar loads.
+struct Walker {
+  typedef const __attribute__((address_space(4))) int32_t uniform_i32;
+  uniform_i32 *offsets;
+  int32_t e, before, first, last;  // expert, row tiles before it, its rows
+  __device__ __forceinline__ Walker(const int32_t *o, const TileAt &t)
+      : offsets((uniform_i32 *)reinterpret_cast<uintptr_t>(o)), e(t.e), before(t.before), first(offsets[t.e]), last(offsets[t.e + 1]) {}
+  // Row tile `index`, which exists and is no earlier than the last one asked for.
+  template <int TM>
+  __device__ __forceinline__ void to(int32_t index, int32_t &r0, int32_t &rows) {
+    int32_t n = (last - first + TM - 1) / TM;
+    while (index >= before + n) {
+      before += n;
+      ++e;
+      first = last;
+      last = offsets[e + 1];
+      n = (last - first + TM - 1) / TM;
+    }
+    r0 = first + (index - before) * TM;
+    rows = min(last - r0, static_cast<int32_t>(TM));
+  }
+};
 
 __device__ __forceinline__ int64_t source_row(const GroupedParams &p, int32_t row) {
   return p.row_token ? p.row_token[row] : row;

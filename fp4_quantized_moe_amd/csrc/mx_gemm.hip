@@ -31,7 +31,7 @@ template <int EPI>
 hipError_t run(const MxGemmLaunch &a, hipStream_t stream) {
   const GroupedParams p = params(a);
   // The staged kernel reads scales by dwords: K % 128.
-  if (a.K % 128 == 0 && a.R > 16 * a.E) {
+  if (a.K % 128 == 0 && a.R > 32 * a.E) {
     if (a.R >= 128 * a.E) return launch_staged<StagedCfg<kOpMx, 256, 256, 2, 2>, EPI>(p, a.R, stream);
     return launch_staged<StagedCfg<kOpMx, 128, 128, 2, 2>, EPI>(p, a.R, stream);
   }
