@@ -36,7 +36,8 @@ struct DirectStage {
   uint32_t sa, sa2, sb;
 };
 
-template <int OP, int EPI>
+// DWORDS: MXFP4 scale rows are dword-aligned (K % 128 == 0).
+template <int OP, int EPI, bool DWORDS>
 __global__ __launch_bounds__(64 * kSplit, 2) void k_grouped_direct(GroupedParams p, int col_groups) {
   constexpr bool PAIR = EPI == kEpiSwiglu || EPI == kEpiSwigluMx;
   constexpr int COLS = PAIR ? 32 : 64;
@@ -56,7 +57,6 @@ __global__ __launch_bounds__(64 * kSplit, 2) void k_grouped_direct(GroupedParams
   int32_t r0 = t0.r0, rows = t0.rows;
 
   const int stages = (p.chunks + 7) / 8, rounds = (stages + kSplit - 1) / kSplit;
-  const bool dwords = p.chunks % 4 == 0;  // scale rows are dword-aligned
 
   // Sources of the item that is being loaded.
   const uint8_t *xr, *xs, *wr, *wr2, *ws, *ws2;
@@ -80,51 +80,44 @@ __global__ __launch_bounds__(64 * kSplit, 2) void k_grouped_direct(GroupedParams
     }
   };
 
-  // Chunks behind K are zeros with scale 2^0; the load is of chunk 0.
+  // Stage s of the item into r (chunks at and behind `limit`: zeros).
+  int32_t limit = p.chunks;
+  const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_chunk);
   const auto load = [&](DirectStage &r, int s) {
     const int c0 = 8 * s + 4 * half;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bool in = c0 + j < p.chunks;
-      const int64_t c = in ? c0 + j : 0;
-      const uint4 b = *reinterpret_cast<const uint4 *>(xr + 16 * c);
-      r.b[j] = in ? b : zero;
+      const bool in = c0 + j < limit;
+      const int64_t c = c0 + j;
+      r.b[j] = *reinterpret_cast<const uint4 *>(in ? xr + 16 * c : zero);
       if constexpr (OP == kOpBf16T) {
         uint32_t h[8], g[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          h[i] = *reinterpret_cast<const uint16_t *>(wr + (8 * c + i) * p.w_row);
-          g[i] = *reinterpret_cast<const uint16_t *>(wr2 + (8 * c + i) * p.w_row);
+          h[i] = *reinterpret_cast<const uint16_t *>(in ? wr + (8 * c + i) * p.w_row : zero);
+          g[i] = *reinterpret_cast<const uint16_t *>(in ? wr2 + (8 * c + i) * p.w_row : zero);
         }
-        r.a[j] = in ? make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16) : zero;
-        r.a2[j] = in ? make_uint4(g[0] | g[1] << 16, g[2] | g[3] << 16, g[4] | g[5] << 16, g[6] | g[7] << 16) : zero;
+        r.a[j] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        r.a2[j] = make_uint4(g[0] | g[1] << 16, g[2] | g[3] << 16, g[4] | g[5] << 16, g[6] | g[7] << 16);
       } else {
-        const uint4 a = *reinterpret_cast<const uint4 *>(wr + 16 * c);
-        const uint4 a2 = *reinterpret_cast<const uint4 *>(wr2 + 16 * c);
-        r.a[j] = in ? a : zero;
-        r.a2[j] = in ? a2 : zero;
+        r.a[j] = *reinterpret_cast<const uint4 *>(in ? wr + 16 * c : zero);
+        r.a2[j] = *reinterpret_cast<const uint4 *>(in ? wr2 + 16 * c : zero);
       }
     }
     if constexpr (OP == kOpMx) {
-      constexpr uint32_t ones = 0x7F7F7F7Fu;
-      if (dwords) {
-        const bool in = c0 < p.chunks;
-        const int c = in ? c0 : 0;
-        const uint32_t sb = *reinterpret_cast<const uint32_t *>(xs + c), sa = *reinterpret_cast<const uint32_t *>(ws + c),
-                       sa2 = *reinterpret_cast<const uint32_t *>(ws2 + c);
-        r.sb = in ? sb : ones;
-        r.sa = in ? sa : ones;
-        r.sa2 = in ? sa2 : ones;
+      if constexpr (DWORDS) {
+        const bool in = c0 < limit;
+        r.sb = *reinterpret_cast<const uint32_t *>(in ? xs + c0 : zero);
+        r.sa = *reinterpret_cast<const uint32_t *>(in ? ws + c0 : zero);
+        r.sa2 = *reinterpret_cast<const uint32_t *>(in ? ws2 + c0 : zero);
       } else {
         r.sa = r.sb = r.sa2 = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bool in = c0 + j < p.chunks;
-          const int c = in ? c0 + j : 0;
-          r.sb |= (in ? xs[c] : 127u) << (8 * j);
-          r.sa |= (in ? ws[c] : 127u) << (8 * j);
-          r.sa2 |= (in ? ws2[c] : 127u) << (8 * j);
+          const bool in = c0 + j < limit;
+          r.sb |= static_cast<uint32_t>(*(in ? xs + c0 + j : zero)) << (8 * j);
+          r.sa |= static_cast<uint32_t>(*(in ? ws + c0 + j : zero)) << (8 * j);
+          r.sa2 |= static_cast<uint32_t>(*(in ? ws2 + c0 + j : zero)) << (8 * j);
         }
       }
     }
@@ -159,17 +152,24 @@ __global__ __launch_bounds__(64 * kSplit, 2) void k_grouped_direct(GroupedParams
     const bool row_ok = (lane & 31) < rows;
     const int32_t n0 = static_cast<int32_t>(group) * COLS;
     const bool more = at + 1 < end;
-    if (!item_done) {
-      load(next, wave + (round + 1) * kSplit);
-    } else if (more) {
-      if (++group == static_cast<uint32_t>(col_groups)) {
-        group = 0;
-        walk.to<32>(static_cast<int32_t>(++tile), r0, rows);
-        aim_rows();
+    int s = wave + (round + 1) * kSplit;
+    if (item_done) {
+      s = wave;
+      if (!more) {
+        limit = 0;
+      } else {
+        if (++group == static_cast<uint32_t>(col_groups)) {
+          group = 0;
+          walk.to<32>(static_cast<int32_t>(++tile), r0, rows);
+          aim_rows();
+        }
+        aim_columns();
       }
-      aim_columns();
-      load(next, wave);
     }
+    // No branch between these: where paths with different numbers of loads
+    // meet, the compiler can only wait for all of them.
+    load(next, s);
+    __builtin_amdgcn_sched_barrier(0);  // all of it before the products
     multiply(now);
     ++round;
     if (!item_done) return true;
@@ -218,8 +218,11 @@ hipError_t launch_direct(const GroupedParams &p, int64_t R, hipStream_t stream) 
   const int64_t items = (max_row_tiles(R, p.E, 32) * groups + 7) / 8 * 8;
   if (items > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const int64_t grid = items < 512 ? items : 512;  // two workgroups on each of the 256 CUs
-  hipLaunchKernelGGL((k_grouped_direct<OP, EPI>), dim3(static_cast<unsigned>(grid)), dim3(64 * kSplit), 0, stream, p,
-                     static_cast<int>(groups));
+  const dim3 blocks(static_cast<unsigned>(grid)), threads(64 * kSplit);
+  if (OP == kOpMx && p.chunks % 4)
+    hipLaunchKernelGGL((k_grouped_direct<OP, EPI, OP != kOpMx>), blocks, threads, 0, stream, p, static_cast<int>(groups));
+  else
+    hipLaunchKernelGGL((k_grouped_direct<OP, EPI, true>), blocks, threads, 0, stream, p, static_cast<int>(groups));
   return hipGetLastError();
 }
 

@@ -34,9 +34,6 @@
 
 namespace quads {
 
-// Zeros that the staging reads in the place of chunks and scales behind K.
-__device__ __attribute__((aligned(16))) uint32_t g_zero_chunk[4];
-
 template <class F, int... I>
 __device__ __forceinline__ void each_index(F &&f, std::integer_sequence<int, I...>) {
   (f(std::integral_constant<int, I>{}), ...);

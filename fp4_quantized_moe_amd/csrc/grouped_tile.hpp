@@ -43,6 +43,10 @@ struct GroupedParams {
   const uint16_t *gu;  // kEpiGatedBwd
 };
 
+// Zeros that are read in the place of chunks and scales behind K (a scale byte
+// 0 is 2^-127).  Choosing the address, not the data, keeps loads in flight.
+__device__ __attribute__((aligned(16))) uint32_t g_zero_chunk[4];
+
 struct TileAt {
   int e;          // expert, or -1: past the last tile
   int32_t r0;     // first routed row
