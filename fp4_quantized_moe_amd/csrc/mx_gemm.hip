@@ -3,6 +3,7 @@
 // v_mfma_scale_f32_32x32x64_f8f6f4 multiplies the codes as stored, scales each
 // 32-element block product by 2^(E_w + E_x) and accumulates in fp32.
 #include "grouped_staged.hpp"
+#include "grouped_stream.hpp"
 #include "launch.hpp"
 
 namespace quads {
@@ -35,6 +36,7 @@ hipError_t run(const MxGemmLaunch &a, hipStream_t stream) {
     if (a.R >= 128 * a.E) return launch_staged<StagedCfg<kOpMx, 256, 256, 2, 2>, EPI>(p, a.R, stream);
     return launch_staged<StagedCfg<kOpMx, 128, 128, 2, 2>, EPI>(p, a.R, stream);
   }
+  if (a.K % 128 == 0 && stream_items<EPI>(p, a.R) >= kStreamItems) return launch_stream<EPI>(p, stream);
   return launch_direct<kOpMx, EPI>(p, a.R, stream);
 }
 

@@ -158,6 +158,8 @@ SHAPES = [
     ([33, 0, 31, 1], 160, 1056), ([17] * 9, 256, 512), ([130, 5, 0, 257], 192, 384), ([300], 320, 128),
     ([512, 255, 1], 512, 768), ([700, 30], 544, 1024), ([40] * 3, 64, 8192), ([1, 2, 0, 4], 2048, 2048),
     ([16] * 70, 128, 256), ([2048], 256, 640),
+    # few rows of many experts, columns enough for every wave of the card
+    ([3, 0, 40, 1, 17, 70, 0, 2] * 3, 1472, 384), ([3, 0, 40, 1, 17, 70, 0, 2] * 3, 1440, 128), ([9, 33] * 10, 2048, 1152),
 ]
 
 
