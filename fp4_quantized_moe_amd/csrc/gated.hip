@@ -35,20 +35,14 @@ GroupedParams params(const GatedLaunch &a, bool backward) {
 hipError_t launch_gated_forward(const GatedLaunch &a, hipStream_t stream) {
   if (a.R == 0) return hipSuccess;
   const GroupedParams p = params(a, false);
-  if (a.R > 32 * a.E) {
-    if (a.R >= 128 * a.E) return launch_staged<StagedCfg<kOpBf16, 256, 256, 2, 2>, kEpiSwiglu>(p, a.R, stream);
-    return launch_staged<StagedCfg<kOpBf16, 128, 128, 2, 2>, kEpiSwiglu>(p, a.R, stream);
-  }
+  if (a.R > 32 * a.E) return launch_staged_tiles<kOpBf16, kEpiSwiglu>(p, a.R, stream);
   return launch_direct<kOpBf16, kEpiSwiglu>(p, a.R, stream);
 }
 
 hipError_t launch_gated_backward(const GatedLaunch &a, hipStream_t stream) {
   if (a.R == 0) return hipSuccess;
   const GroupedParams p = params(a, true);
-  if (a.R > 32 * a.E) {
-    if (a.R >= 128 * a.E) return launch_staged<StagedCfg<kOpBf16T, 256, 256, 2, 2>, kEpiGatedBwd>(p, a.R, stream);
-    return launch_staged<StagedCfg<kOpBf16T, 128, 128, 2, 2>, kEpiGatedBwd>(p, a.R, stream);
-  }
+  if (a.R > 32 * a.E) return launch_staged_tiles<kOpBf16T, kEpiGatedBwd>(p, a.R, stream);
   return launch_direct<kOpBf16T, kEpiGatedBwd>(p, a.R, stream);
 }
 

@@ -44,8 +44,6 @@ __device__ __forceinline__ void each(F &&f) {
   each_index(static_cast<F &&>(f), std::make_integer_sequence<int, N>{});
 }
 
-constexpr int D3 = 12, D0 = 4;
-constexpr int kTurnBytes = 4096;  // a wave's epilogue block: 32 rows of 128 bytes
 
 template <int OP_, int TM_, int TN_, int WM_, int WN_>
 struct StagedCfg {
@@ -59,13 +57,17 @@ struct StagedCfg {
   static constexpr int KROWS = 512 / TN;  // kOpBf16T: weight rows of one staging instruction
   static constexpr int SLOADS = MX ? ROWS / 32 / WAVES : 0;  // scale instructions (32 rows each)
   static constexpr int TURN = 2 * (ROWS * 128 + (MX ? ROWS * 8 : 0));  // LDS: two stages, then the epilogue's blocks,
-  static constexpr int TOKENS = TURN + WAVES * kTurnBytes;             // then the next tile's token ids
+  // Rows of the blocks that the epilogue turns around: whole lines, or half
+  // ones for the small tile, of which two workgroups then fit a CU.
+  static constexpr int RB = NI >= 4 ? 128 : 64, TURN_BYTES = 32 * RB;
+  static constexpr int TOKENS = TURN + WAVES * TURN_BYTES;             // then the next tile's token ids
   static constexpr int LDS = TOKENS + 256 * WAVES;
   static constexpr int STAGE = ROWS * 128 + (MX ? ROWS * 8 : 0);
   static constexpr int ALL = LOADS + SLOADS;
-  // Staging instructions issued in a stage's last step, in the next stage's
-  // first and in its second.
-  static constexpr int IN3 = ALL * D3 / 16, IN0 = ALL * D0 / 16, IN1 = ALL - IN3 - IN0;
+  // Staging instructions issued in a stage's last step and in the next
+  // stage's first.  Three quarters and a quarter measured best (8192 x 8192 x
+  // 16384 MXFP4: all in the last 518 us, 3 : 1 504, half and half 545).
+  static constexpr int LATE = ALL * 3 / 4;
   static_assert(!MX || (TN % (32 * WAVES) == 0 && TM % (32 * WAVES) == 0), "a scale instruction reads one operand");
   static_assert(WAVES * KROWS % 4 == 0 || !TRANS, "slots of kOpBf16T");
   static_assert(64 * WAVES >= TM, "token ids of a tile");
@@ -162,38 +164,46 @@ __device__ __forceinline__ int fresh_lane() {
 
 // A wave's accumulators a[i] (i-th 32 columns) of 32 rows: row0 is the first
 // row's index in the output, rows how many exist, n0 the wave's first column.
-template <int EPI, int NI>
-__device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16 (&a)[NI], uint8_t *turn, int lane, int64_t row0,
-                                            int rows, int32_t n0) {
+// RB: bytes of a row of the block that is turned around.
+template <int EPI, int NI, int RB>
+__device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16 (&a)[NI], uint8_t *turn, int lane,
+                                            int64_t row0, int rows, int32_t n0) {
   if (rows <= 0) return;
+  constexpr int TILES = RB / 64;  // 32-column bf16 tiles of a block
   float v[16];
   if constexpr (EPI == kEpiF32) {
     const int half = lane >> 5, fr = lane & 31;
+    constexpr int COLS = RB / 4;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<float4 *>(turn + turn_at<128>(fr, 2 * q + half)) =
-            make_float4(a[i][4 * q], a[i][4 * q + 1], a[i][4 * q + 2], a[i][4 * q + 3]);
-      const int32_t n = n0 + 32 * i;
-      turn_store<128>(turn, lane, static_cast<uint8_t *>(p.y) + 4 * (row0 * p.width + n), 4 * static_cast<int64_t>(p.width),
-                      rows, 4 * (p.width - n));
-    }
+      for (int part = 0; part < 32 / COLS; ++part) {
+#pragma unroll
+        for (int q = 0; q < COLS / 8; ++q) {
+          const int r = 4 * (q + part * (COLS / 8));
+          *reinterpret_cast<float4 *>(turn + turn_at<RB>(fr, 2 * q + half)) =
+              make_float4(a[i][r], a[i][r + 1], a[i][r + 2], a[i][r + 3]);
+        }
+        const int32_t n = n0 + 32 * i + COLS * part;
+        turn_store<RB>(turn, lane, static_cast<uint8_t *>(p.y) + 4 * (row0 * p.width + n),
+                       4 * static_cast<int64_t>(p.width), rows, 4 * (p.width - n));
+      }
   } else if constexpr (EPI == kEpiBf16) {
 #pragma unroll
-    for (int i = 0; i < NI; i += 2) {
+    for (int i = 0; i < NI; i += TILES) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < TILES; ++t) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] = a[i + t][r];
-        turn_put_bf16<128>(turn, lane, t, v);
+        turn_put_bf16<RB>(turn, lane, t, v);
       }
       const int32_t n = n0 + 32 * i;
-      turn_store<128>(turn, lane, static_cast<uint8_t *>(p.y) + 2 * (row0 * p.width + n), 2 * static_cast<int64_t>(p.width),
-                      rows, 2 * (p.width - n));
+      turn_store<RB>(turn, lane, static_cast<uint8_t *>(p.y) + 2 * (row0 * p.width + n),
+                     2 * static_cast<int64_t>(p.width), rows, 2 * (p.width - n));
     }
   } else if constexpr (EPI == kEpiSwiglu) {
-    constexpr int PAIRS = NI / 2, RB = 64 * PAIRS;
+    constexpr int PAIRS = NI / 2;
+    static_assert(PAIRS == TILES, "a block holds the wave's columns");
     const int64_t stride = 2 * static_cast<int64_t>(p.width);
     const int limit = 2 * (p.width - n0);
 #pragma unroll
@@ -212,11 +222,12 @@ __device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16
           for (int r = 0; r < 16; ++r) v[r] = a[part * PAIRS + i][r];
           turn_put_bf16<RB>(turn, lane, i, v);
         }
-        turn_store<RB>(turn, lane, static_cast<uint8_t *>(p.y2) + row0 * 2 * stride + part * stride + 2 * n0, 2 * stride, rows,
-                       limit);
+        turn_store<RB>(turn, lane, static_cast<uint8_t *>(p.y2) + row0 * 2 * stride + part * stride + 2 * n0, 2 * stride,
+                       rows, limit);
       }
     }
-  } else if constexpr (EPI == kEpiSwigluMx) {
+  } else {
+    static_assert(EPI == kEpiSwigluMx, "kEpiGatedBwd has an epilogue of its own");
     constexpr int PAIRS = NI / 2;
     const int fr = lane & 31;
 #pragma unroll
@@ -233,40 +244,50 @@ __device__ __forceinline__ void store_block(const GroupedParams &p, const f32x16
       static_cast<uint8_t *>(p.y2)[(row0 + row) * (p.width >> 5) + (n0 >> 5) + i] = s;
     }
     __builtin_amdgcn_sched_barrier(0);
-  } else {  // kEpiGatedBwd: a is dh; dg and du take the place of g and u
-    const int64_t stride = 4 * static_cast<int64_t>(p.width);  // bytes of a row [gate | up]
-#pragma unroll
-    for (int i = 0; i < NI; i += 2) {
-      const int32_t n = n0 + 32 * i;
-      const int limit = 2 * (p.width - n);
-      const int64_t at = row0 * stride + 2 * n;
-      const uint8_t *in = reinterpret_cast<const uint8_t *>(p.gu) + at;
-      uint8_t *out = static_cast<uint8_t *>(p.y) + at;
-      TurnLoad<128> lg, lu;
-      lg.load(in, lane, stride, rows, limit);
-      lu.load(in + 2 * static_cast<int64_t>(p.width), lane, stride, rows, limit);
-      float g[2][16], u[2][16];
-      lg.put(turn, lane);
-      turn_get_bf16<128>(turn, lane, 0, g[0]);
-      turn_get_bf16<128>(turn, lane, 1, g[1]);
-      lu.put(turn, lane);
-      turn_get_bf16<128>(turn, lane, 0, u[0]);
-      turn_get_bf16<128>(turn, lane, 1, u[1]);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float d = a[i + t][r];
-          gated_grad(d, g[t][r], u[t][r]);
-        }
-      turn_put_bf16<128>(turn, lane, 0, g[0]);
-      turn_put_bf16<128>(turn, lane, 1, g[1]);
-      turn_store<128>(turn, lane, out, stride, rows, limit);
-      turn_put_bf16<128>(turn, lane, 0, u[0]);
-      turn_put_bf16<128>(turn, lane, 1, u[1]);
-      turn_store<128>(turn, lane, out + 2 * static_cast<int64_t>(p.width), stride, rows, limit);
-    }
   }
+}
+
+// The backward's epilogue: a[i] is dh; du and dg take the place of u and g.
+// (Sending for the next block's gate and up while one is computed, from a
+// second set of registers or from this one, measured slower: 515 - 535
+// against 505 us for the layer.)
+template <int RB>
+struct GatedBlock {
+  TurnLoad<RB> g, u;
+  __device__ __forceinline__ void load(const GroupedParams &p, int lane, int64_t row0, int rows, int32_t n) {
+    const int64_t stride = 4 * static_cast<int64_t>(p.width);  // bytes of a row [gate | up]
+    const uint8_t *in = reinterpret_cast<const uint8_t *>(p.gu) + row0 * stride + 2 * n;
+    g.load(in, lane, stride, rows, 2 * (p.width - n));
+    u.load(in + 2 * static_cast<int64_t>(p.width), lane, stride, rows, 2 * (p.width - n));
+  }
+};
+
+template <int RB>
+__device__ __forceinline__ void store_gated_grad(const GroupedParams &p, const f32x16 (&d)[RB / 64], uint8_t *turn,
+                                                 int lane, int64_t row0, int rows, int32_t n) {
+  GatedBlock<RB> in;
+  in.load(p, lane, row0, rows, n);
+  constexpr int TILES = RB / 64;
+  const int64_t stride = 4 * static_cast<int64_t>(p.width);
+  uint8_t *out = static_cast<uint8_t *>(p.y) + row0 * stride + 2 * n;
+  const int limit = 2 * (p.width - n);
+  float g[TILES][16], u[TILES][16];
+  in.g.put(turn, lane);
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) turn_get_bf16<RB>(turn, lane, t, g[t]);
+  in.u.put(turn, lane);
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) turn_get_bf16<RB>(turn, lane, t, u[t]);
+#pragma unroll
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) gated_grad(d[t][r], g[t][r], u[t][r]);
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) turn_put_bf16<RB>(turn, lane, t, g[t]);
+  turn_store<RB>(turn, lane, out, stride, rows, limit);
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) turn_put_bf16<RB>(turn, lane, t, u[t]);
+  turn_store<RB>(turn, lane, out + 2 * static_cast<int64_t>(p.width), stride, rows, limit);
 }
 
 // One workgroup's tiles.  Tiles are numbered columns fastest, each XCD owns a
@@ -422,8 +443,7 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   const auto step = [&](auto sel, const Frag &f, Frag &g, Scales &gsc, const uint8_t *gbase, int gs, int ds,
                         uint8_t *dbase) {
     constexpr int S = decltype(sel)::value;
-    constexpr int DN = S == 3 ? C::IN3 : S == 0 ? C::IN0 : S == 1 ? C::IN1 : 0;
-    constexpr int DF = S == 3 ? 0 : S == 0 ? C::IN3 : C::IN3 + C::IN0;
+    constexpr int DF = S == 3 ? 0 : C::LATE, DN = S == 3 ? C::LATE : S == 0 ? C::ALL - C::LATE : 0;
     constexpr int READS = FRAGS + (C::MX && S == 3 ? FRAGS : 0);
     constexpr int RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
     each<SLOTS>([&](auto slot) {
@@ -443,14 +463,14 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  // One stage.  The rest of stage `now`, which the last step before began to
-  // bring, goes on in its first steps, and stage `ds` begins in its last;
-  // `between` may aim at another tile.
+  // One stage.  The rest of stage `now`, which the step before began to bring,
+  // follows in its first step, and stage `ds` begins in its last; `between` may
+  // aim at another tile.
   uint8_t *cur = lds;
   const auto stage = [&](int now, int ds, auto between) {
     uint8_t *nxt = lds + (cur == lds ? C::STAGE : 0);
     step(std::integral_constant<int, 0>{}, f0, f1, sc, cur, 1, now, nxt);
-    step(std::integral_constant<int, 1>{}, f1, f0, sc, cur, 2, now, nxt);
+    step(std::integral_constant<int, 1>{}, f1, f0, sc, cur, 2, 0, cur);
     between();
     step(std::integral_constant<int, 2>{}, f0, f1, sc, cur, 3, 0, cur);
     wait_lgkm0();  // step 3's fragments are in registers: this wave is done with the stage's LDS
@@ -465,10 +485,10 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   const int stages = max((p.chunks + 7) / 8, 2);  // at least both buffers: one of zeros for a short K
   aim(t, [&](int r) -> int64_t { return source_row(p, t.r0 + min(r, t.rows - 1)); });
   each<C::ALL>([&](auto j) { fetch_one(0, lds, j); });
-  each<C::IN3>([&](auto j) { fetch_one(1, lds + C::STAGE, j); });
+  each<C::LATE>([&](auto j) { fetch_one(1, lds + C::STAGE, j); });
   StagedTile nt;
   advance(nt);
-  wait_vm<C::IN3>();
+  wait_vm<C::LATE>();
   barrier_no_fence();
   each<FRAGS + (C::MX ? FRAGS : 0)>([&](auto r) { read_item(f0, sc, lds, 0, r); });
   fetch_tokens(nt);
@@ -510,22 +530,41 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
     pin();
     stage(0, 1, [] {});
     pin();
-    uint8_t *turn = lds + C::TURN + wave * kTurnBytes;
+    uint8_t *turn = lds + C::TURN + wave * C::TURN_BYTES;
     const int fl = fresh_lane();
+    const int32_t wn0 = t.n0 + wn * (C::TN / C::WN) / (PAIR ? 2 : 1);
+    const int64_t wrow = static_cast<int64_t>(t.r0) + wm * (C::TM / C::WM);
+    const int wrows = t.rows - wm * (C::TM / C::WM);
+    if constexpr (EPI == kEpiGatedBwd) {
+      constexpr int TILES = C::RB / 64, ACROSS = C::NI / TILES, BLOCKS = C::MI * ACROSS;
+      each<BLOCKS>([&](auto bc) {
+        constexpr int b = decltype(bc)::value, k = b / ACROSS, i = b % ACROSS * TILES;
+        f32x16 d[TILES];
 #pragma unroll
-    for (int k = 0; k < C::MI; ++k) {
-      f32x16 col[C::NI];
+        for (int q = 0; q < TILES; ++q) {
+          asm volatile("" : "+a"(acc[i + q][k]));  // not read before its turn
+          d[q] = acc[i + q][k];
+        }
+        if (wrows > 32 * k)
+          store_gated_grad<C::RB>(p, d, turn, fl, wrow + 32 * k, wrows - 32 * k, wn0 + 32 * i);
 #pragma unroll
-      for (int i = 0; i < C::NI; ++i) {
-        asm volatile("" : "+a"(acc[i][k]));  // not read before its turn
-        col[i] = acc[i][k];
+        for (int q = 0; q < TILES; ++q) acc[i + q][k] = f32x16{};
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    } else {
+#pragma unroll
+      for (int k = 0; k < C::MI; ++k) {
+        f32x16 col[C::NI];
+#pragma unroll
+        for (int i = 0; i < C::NI; ++i) {
+          asm volatile("" : "+a"(acc[i][k]));  // not read before its turn
+          col[i] = acc[i][k];
+        }
+        store_block<EPI, C::NI, C::RB>(p, col, turn, fl, wrow + 32 * k, wrows - 32 * k, wn0);
+#pragma unroll
+        for (int i = 0; i < C::NI; ++i) acc[i][k] = f32x16{};
+        __builtin_amdgcn_sched_barrier(0);
       }
-      const int m = wm * (C::TM / C::WM) + 32 * k;
-      store_block<EPI, C::NI>(p, col, turn, fl, static_cast<int64_t>(t.r0) + m, t.rows - m,
-                              t.n0 + wn * (C::TN / C::WN) / (PAIR ? 2 : 1));
-#pragma unroll
-      for (int i = 0; i < C::NI; ++i) acc[i][k] = f32x16{};
-      __builtin_amdgcn_sched_barrier(0);
     }
     if (nt.e < 0) break;
     t = nt;
@@ -554,6 +593,20 @@ hipError_t launch_staged(const GroupedParams &p, int64_t R, hipStream_t stream) 
   hipLaunchKernelGGL((k_grouped_staged<C, EPI>), dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), 0, stream, p,
                      static_cast<int>(cols));
   return hipGetLastError();
+}
+
+// The large and the small tile.  256 x 256 reads each operand half as often
+// and its waves read LDS least per product (8192 x 8192 x 8192 MXFP4: 308 us
+// against 434 us with 128 x 128), but wants rows to fill it and tiles to fill
+// the card: from 128 rows an expert on, and three quarters of the CUs with a
+// tile (4096 x 1536 x 2048, 96 large tiles: 25.5 against 19.6 us).
+template <int OP, int EPI>
+hipError_t launch_staged_tiles(const GroupedParams &p, int64_t R, hipStream_t stream) {
+  constexpr int COLS = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? 128 : 256;
+  const int64_t tiles = (R + 255) / 256 * ((p.width + COLS - 1) / COLS);
+  if (R >= 128 * static_cast<int64_t>(p.E) && tiles >= 192)
+    return launch_staged<StagedCfg<OP, 256, 256, 2, 2>, EPI>(p, R, stream);
+  return launch_staged<StagedCfg<OP, 128, 128, 2, 2>, EPI>(p, R, stream);
 }
 
 }  // namespace quads

@@ -32,10 +32,7 @@ template <int EPI>
 hipError_t run(const MxGemmLaunch &a, hipStream_t stream) {
   const GroupedParams p = params(a);
   // The staged kernel reads scales by dwords: K % 128.
-  if (a.K % 128 == 0 && a.R > 32 * a.E) {
-    if (a.R >= 128 * a.E) return launch_staged<StagedCfg<kOpMx, 256, 256, 2, 2>, EPI>(p, a.R, stream);
-    return launch_staged<StagedCfg<kOpMx, 128, 128, 2, 2>, EPI>(p, a.R, stream);
-  }
+  if (a.K % 128 == 0 && a.R > 32 * a.E) return launch_staged_tiles<kOpMx, EPI>(p, a.R, stream);
   if (a.K % 128 == 0 && stream_items<EPI>(p, a.R) >= kStreamItems) return launch_stream<EPI>(p, stream);
   return launch_direct<kOpMx, EPI>(p, a.R, stream);
 }
