@@ -49,6 +49,9 @@ class _MxGemmArgs(ctypes.Structure):
     ]
 
 
+_MX_GEMM_SIZE = ctypes.sizeof(_MxGemmArgs)
+
+
 class _GemmArgs(ctypes.Structure):
     _fields_ = [
         ("struct_size", _c_u32), ("flags", _c_u32), ("operand_mode", _c_i32), ("epilogue", _c_i32), ("y_dtype", _c_i32),
@@ -658,12 +661,13 @@ def _on_device(x: torch.Tensor, fn, what: str, *args):
 
 
 def _require(what: str, t: torch.Tensor, name: str, dtype, like: torch.Tensor | None = None):
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (like is None or t.get_device() == like.get_device()):
+        return
     if not t.is_cuda or not t.is_contiguous():
         raise QuadsError(f"{what}: {name} must be contiguous and on the GPU")
     if t.dtype != dtype:
         raise QuadsError(f"{what}: {name} must be {dtype}, not {t.dtype}")
-    if like is not None and t.device != like.device:
-        raise QuadsError(f"{what}: {name} is on {t.device}, not {like.device}")
+    raise QuadsError(f"{what}: {name} is on {t.device}, not {like.device}")
 
 
 def _batch_rows_cols(what: str, shape):
@@ -804,35 +808,30 @@ def moe_mxfp4_gemm(x: MXFP4Tensor, w: MXFP4Tensor, expert_offsets: torch.Tensor,
     dev = x.codes.device
     R = _grouping(what, x.codes, x.rows, expert_offsets, row_token, w.batch)
     width = w.rows // 2 if epilogue == EPI_SWIGLU else w.rows
-    a = _MxGemmArgs()
-    a.struct_size = ctypes.sizeof(_MxGemmArgs)
-    a.epilogue = epilogue
-    a.num_experts = w.batch
-    a.num_rows, a.act_rows, a.N, a.K = R, x.rows, w.rows, x.cols
-    a.x_codes, a.x_scales = x.codes.data_ptr(), x.scales.data_ptr()
-    a.w_codes, a.w_scales = w.codes.data_ptr(), w.scales.data_ptr()
-    a.row_token = None if row_token is None else row_token.data_ptr()
-    a.expert_offsets = expert_offsets.data_ptr()
+    y_scales = None
     if y_dtype == MXFP4:
-        a.y_dtype = MXFP4
+        code = MXFP4
         if y is None:
             y = empty_mxfp4(1, R, width - width % 32, dev)
         else:
             _require_mx(what, y, "y", x.codes)
             if (y.batch, y.rows, y.cols) != (1, R, width):
                 raise QuadsError(f"{what}: y must be [{R}, {width}]")
-        a.y, a.y_scales = y.codes.data_ptr(), y.scales.data_ptr()
+        y_data, y_scales = y.codes.data_ptr(), y.scales.data_ptr()
     else:
         if y_dtype not in (torch.float32, torch.bfloat16):
             raise QuadsError(f"{what}: y_dtype must be float32, bfloat16 or MXFP4, not {y_dtype}")
-        a.y_dtype = BF16 if y_dtype == torch.bfloat16 else F32
+        code = BF16 if y_dtype == torch.bfloat16 else F32
         if y is None:
             y = torch.empty(R, width, dtype=y_dtype, device=dev)
         else:
             _require(what, y, "y", y_dtype, x.codes)
             if tuple(y.shape) != (R, width):
                 raise QuadsError(f"{what}: y must be [{R}, {width}]")
-        a.y = y.data_ptr()
+        y_data = y.data_ptr()
+    a = _MxGemmArgs(_MX_GEMM_SIZE, 0, epilogue, code, w.batch, 0, R, x.rows, w.rows, x.cols, x.codes.data_ptr(),
+                    x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+                    None if row_token is None else row_token.data_ptr(), expert_offsets.data_ptr(), y_data, y_scales)
     _on_device(x.codes, load().quads_moe_mxfp4_gemm, what, ctypes.byref(a))
     return y
 
