@@ -45,7 +45,7 @@ __device__ __forceinline__ void each(F &&f) {
 }
 
 
-template <int OP_, int TM_, int TN_, int WM_, int WN_>
+template <int OP_, int TM_, int TN_, int WM_, int WN_, bool ODD_ = false>
 struct StagedCfg {
   static constexpr int OP = OP_, TM = TM_, TN = TN_, WM = WM_, WN = WN_;
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
@@ -54,15 +54,18 @@ struct StagedCfg {
   static constexpr int LOADS = ROWS / 8 / WAVES;       // staging instructions of a wave and stage
   static constexpr int WLOADS = TN / 8 / WAVES;        // the weights' part of them
   static constexpr bool MX = OP == kOpMx, TRANS = OP == kOpBf16T;
+  // MXFP4 scale rows that are not dword-aligned (K % 128 != 0): the DMA does
+  // not take them, and each lane loads its fragments' scales to registers.
+  static constexpr bool ODD = ODD_, SLDS = MX && !ODD;
   static constexpr int KROWS = 512 / TN;  // kOpBf16T: weight rows of one staging instruction
-  static constexpr int SLOADS = MX ? ROWS / 32 / WAVES : 0;  // scale instructions (32 rows each)
-  static constexpr int TURN = 2 * (ROWS * 128 + (MX ? ROWS * 8 : 0));  // LDS: two stages, then the epilogue's blocks,
+  static constexpr int SLOADS = SLDS ? ROWS / 32 / WAVES : 0;  // scale instructions (32 rows each)
+  static constexpr int TURN = 2 * (ROWS * 128 + (SLDS ? ROWS * 8 : 0));  // LDS: two stages, then the epilogue's blocks,
   // Rows of the blocks that the epilogue turns around: whole lines, or half
   // ones for the small tile, of which two workgroups then fit a CU.
   static constexpr int RB = NI >= 4 ? 128 : 64, TURN_BYTES = 32 * RB;
   static constexpr int TOKENS = TURN + WAVES * TURN_BYTES;             // then the next tile's token ids
   static constexpr int LDS = TOKENS + 256 * WAVES;
-  static constexpr int STAGE = ROWS * 128 + (MX ? ROWS * 8 : 0);
+  static constexpr int STAGE = ROWS * 128 + (SLDS ? ROWS * 8 : 0);
   static constexpr int ALL = LOADS + SLOADS;
   // Staging instructions issued in a stage's last step and in the next
   // stage's first.  Three quarters and a quarter measured best (8192 x 8192 x
@@ -330,6 +333,8 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   // kOpBf16T: weight row of the stage and column chunk that this lane stages.
   // Instructions are 4 rows or a multiple apart, so the slot does not depend on j.
   const int wk = wave * C::KROWS + lane / (64 / C::KROWS);
+  // ODD: the scale rows of this lane's fragment rows.
+  const uint8_t *arows[C::ODD ? C::NI : 1], *brows[C::ODD ? C::MI : 1];
   int32_t limit = p.chunks;  // chunks of the staged tile (0: there is none, and zeros are staged)
   const auto aim = [&](const StagedTile &u, auto token) {
     const int lane = fresh_lane(), lr = lane >> 3, chunk = (lane & 7) ^ ((4 * wave + (lr >> 1)) & 7);
@@ -355,6 +360,15 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
         from[j] = we + weight_row((j * C::WAVES + wave) * 8 + lr) * p.w_row + 16 * chunk;
       else
         from[j] = p.x + token(((j - C::WLOADS) * C::WAVES + wave) * 8 + lr) * p.x_row + 16 * chunk;
+    }
+    if constexpr (C::ODD) {
+      const int fr = lane & 31;
+#pragma unroll
+      for (int i = 0; i < C::NI; ++i)
+        arows[i] = p.w_scales + (static_cast<int64_t>(u.e) * p.N + weight_row(wn * (C::TN / C::WN) + 32 * i + fr)) * p.chunks;
+#pragma unroll
+      for (int i = 0; i < C::MI; ++i)
+        brows[i] = p.x_scales + token(wm * (C::TM / C::WM) + 32 * i + fr) * p.chunks;
     }
 #pragma unroll
     for (int j = 0; j < C::SLOADS; ++j) {
@@ -435,6 +449,31 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
 
   f32x16 acc[C::NI][C::MI];
   Scales sc;
+  // ODD: the scales of a stage as loaded (a dword at any byte; near the end of
+  // a row its last four bytes), the shift that brings the stage's first byte
+  // down, and whether there is one.  Bytes behind K become 0 (2^-127).
+  struct Raw {
+    Scales v;
+    int shift;
+    bool any;
+  };
+  Raw raw;
+  const auto load_scales = [&](int s) {
+    const int at = 8 * s + 4 * half, valid = min(limit - at, 4);
+    const int off = valid >= 4 ? at : valid > 0 ? limit - 4 : 0;
+    raw.any = valid > 0;
+    raw.shift = 8 * (4 - max(valid, 1));
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) __builtin_memcpy(&raw.v.a[i], arows[C::ODD ? i : 0] + off, 4);
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i) __builtin_memcpy(&raw.v.b[i], brows[C::ODD ? i : 0] + off, 4);
+  };
+  const auto take_scales = [&](Scales &to) {
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) to.a[i] = raw.any ? raw.v.a[i] >> raw.shift : 0u;
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i) to.b[i] = raw.any ? raw.v.b[i] >> raw.shift : 0u;
+  };
   Frag f0, f1;
   // One step: its products of `f`, with the reads of `g` (step gs of the stage
   // at gbase) and, in a stage's last step, the next stage's scales and the
@@ -444,7 +483,7 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
                         uint8_t *dbase) {
     constexpr int S = decltype(sel)::value;
     constexpr int DF = S == 3 ? 0 : C::LATE, DN = S == 3 ? C::LATE : S == 0 ? C::ALL - C::LATE : 0;
-    constexpr int READS = FRAGS + (C::MX && S == 3 ? FRAGS : 0);
+    constexpr int READS = FRAGS + (C::SLDS && S == 3 ? FRAGS : 0);
     constexpr int RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
     each<SLOTS>([&](auto slot) {
       constexpr int n = decltype(slot)::value, i = n / C::MI, k = n % C::MI;
@@ -477,6 +516,10 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
     wait_vm<0>();  // and its part of the next stage has landed
     barrier_no_fence();
     Scales next;
+    if constexpr (C::ODD) {  // the next stage's have landed with its operands
+      take_scales(next);
+      load_scales(ds);
+    }
     step(std::integral_constant<int, 3>{}, f1, f0, next, nxt, 0, ds, cur);
     if constexpr (C::MX) sc = next;
     cur = nxt;
@@ -484,13 +527,18 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
 
   const int stages = max((p.chunks + 7) / 8, 2);  // at least both buffers: one of zeros for a short K
   aim(t, [&](int r) -> int64_t { return source_row(p, t.r0 + min(r, t.rows - 1)); });
+  if constexpr (C::ODD) {
+    load_scales(0);
+    take_scales(sc);
+    load_scales(1);
+  }
   each<C::ALL>([&](auto j) { fetch_one(0, lds, j); });
   each<C::LATE>([&](auto j) { fetch_one(1, lds + C::STAGE, j); });
   StagedTile nt;
   advance(nt);
   wait_vm<C::LATE>();
   barrier_no_fence();
-  each<FRAGS + (C::MX ? FRAGS : 0)>([&](auto r) { read_item(f0, sc, lds, 0, r); });
+  each<FRAGS + (C::SLDS ? FRAGS : 0)>([&](auto r) { read_item(f0, sc, lds, 0, r); });
   fetch_tokens(nt);
 
 #pragma unroll
@@ -600,13 +648,13 @@ hipError_t launch_staged(const GroupedParams &p, int64_t R, hipStream_t stream) 
 // against 434 us with 128 x 128), but wants rows to fill it and tiles to fill
 // the card: from 128 rows an expert on, and three quarters of the CUs with a
 // tile (4096 x 1536 x 2048, 96 large tiles: 25.5 against 19.6 us).
-template <int OP, int EPI>
+template <int OP, int EPI, bool ODD = false>
 hipError_t launch_staged_tiles(const GroupedParams &p, int64_t R, hipStream_t stream) {
   constexpr int COLS = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? 128 : 256;
   const int64_t tiles = (R + 255) / 256 * ((p.width + COLS - 1) / COLS);
   if (R >= 128 * static_cast<int64_t>(p.E) && tiles >= 192)
-    return launch_staged<StagedCfg<OP, 256, 256, 2, 2>, EPI>(p, R, stream);
-  return launch_staged<StagedCfg<OP, 128, 128, 2, 2>, EPI>(p, R, stream);
+    return launch_staged<StagedCfg<OP, 256, 256, 2, 2, ODD>, EPI>(p, R, stream);
+  return launch_staged<StagedCfg<OP, 128, 128, 2, 2, ODD>, EPI>(p, R, stream);
 }
 
 }  // namespace quads

@@ -31,8 +31,12 @@ GroupedParams params(const MxGemmLaunch &a) {
 template <int EPI>
 hipError_t run(const MxGemmLaunch &a, hipStream_t stream) {
   const GroupedParams p = params(a);
-  // The staged kernel reads scales by dwords: K % 128.
-  if (a.K % 128 == 0 && a.R > 32 * a.E) return launch_staged_tiles<kOpMx, EPI>(p, a.R, stream);
+  // From 32 rows an expert on a weight row meets more than one 32-row tile:
+  // staged through LDS.  Scale rows are whole dwords with K % 128 == 0.
+  if (a.R > 32 * a.E) {
+    if (a.K % 128 == 0) return launch_staged_tiles<kOpMx, EPI>(p, a.R, stream);
+    if (a.K > 128) return launch_staged_tiles<kOpMx, EPI, true>(p, a.R, stream);
+  }
   if (a.K % 128 == 0 && stream_items<EPI>(p, a.R) >= kStreamItems) return launch_stream<EPI>(p, stream);
   return launch_direct<kOpMx, EPI>(p, a.R, stream);
 }

@@ -49,6 +49,8 @@ def check(y, x, w, ends, token, K):
 CASES = [
     ("skewed", 8, 30000, 1536, 256), ("even", 64, 64 * 520, 768, 512), ("last", 3, 20000, 2080, 768),
     ("skewed", 16, 40000, 1024, 2048), ("skewed", 300, 30000, 544, 384), ("even", 128, 128 * 70, 576, 640),
+    # scale rows that no dword fits: 5, 9, 27 and 33 blocks a row
+    ("skewed", 8, 30000, 1536, 160), ("last", 3, 20000, 2080, 288), ("even", 64, 64 * 520, 768, 864), ("even", 40, 40 * 70, 448, 1056),
 ]
 
 

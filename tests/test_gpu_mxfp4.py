@@ -159,6 +159,7 @@ SHAPES = [
     ([512, 255, 1], 512, 768), ([700, 30], 544, 1024), ([40] * 3, 64, 8192), ([1, 2, 0, 4], 2048, 2048),
     ([16] * 70, 128, 256), ([2048], 256, 640),
     # few rows of many experts, columns enough for every wave of the card
+    ([300], 320, 160), ([40, 129, 70], 96, 288), ([200, 0, 33], 128, 704), ([130], 64, 1888),
     ([3, 0, 40, 1, 17, 70, 0, 2] * 3, 1472, 384), ([3, 0, 40, 1, 17, 70, 0, 2] * 3, 1440, 128), ([9, 33] * 10, 2048, 1152),
 ]
 
@@ -231,7 +232,7 @@ def test_rows_behind_the_last_expert_stay():
     assert bool((q.codes[33:] == 0xAB).all()) and bool((q.scales[33:] == 0xCD).all())
 
 
-@pytest.mark.parametrize("K", [96, 256])
+@pytest.mark.parametrize("K", [96, 160, 256, 288, 416, 448])
 def test_nan_reaches_its_rows_alone(K):
     """A NaN block of one activation row makes that row NaN; one of a weight row that column."""
     d = make(9, [40], 128, K, gather=False)
