@@ -34,9 +34,10 @@ constexpr int kSplit = 4;  // waves of a workgroup
 struct DirectStage {
   uint4 a[4], a2[4], b[4];
   uint32_t sa, sa2, sb;
+  int shift;  // brings the stage's first scale byte down (a row's last dword may begin before it)
 };
 
-// DWORDS: MXFP4 scale rows are dword-aligned (K % 128 == 0).
+// DWORDS: an MXFP4 scale row has at least a dword (K >= 128), read at any byte.
 template <int OP, int EPI, bool DWORDS>
 __global__ __launch_bounds__(64 * kSplit, 2) void k_grouped_direct(GroupedParams p, int col_groups) {
   constexpr bool PAIR = EPI == kEpiSwiglu || EPI == kEpiSwigluMx;
@@ -106,12 +107,15 @@ __global__ __launch_bounds__(64 * kSplit, 2) void k_grouped_direct(GroupedParams
     }
     if constexpr (OP == kOpMx) {
       if constexpr (DWORDS) {
-        const bool in = c0 < limit;
-        r.sb = *reinterpret_cast<const uint32_t *>(in ? xs + c0 : zero);
-        r.sa = *reinterpret_cast<const uint32_t *>(in ? ws + c0 : zero);
-        r.sa2 = *reinterpret_cast<const uint32_t *>(in ? ws2 + c0 : zero);
+        const int valid = min(limit - c0, 4);  // scale bytes of this half; behind K: 0 (2^-127)
+        const int c = valid >= 4 ? c0 : limit - 4;
+        r.shift = 8 * (4 - max(valid, 1));
+        __builtin_memcpy(&r.sb, valid > 0 ? xs + c : zero, 4);
+        __builtin_memcpy(&r.sa, valid > 0 ? ws + c : zero, 4);
+        __builtin_memcpy(&r.sa2, valid > 0 ? ws2 + c : zero, 4);
       } else {
         r.sa = r.sb = r.sa2 = 0;
+        r.shift = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const bool in = c0 + j < limit;
@@ -125,14 +129,15 @@ __global__ __launch_bounds__(64 * kSplit, 2) void k_grouped_direct(GroupedParams
   f32x16 acc = {}, acc2 = {};
   const auto multiply = [&](const DirectStage &r) {
     if constexpr (OP == kOpMx) {
-      acc = mfma_mx<0>(r.a[0], r.b[0], acc, r.sa, r.sb);
-      acc2 = mfma_mx<0>(r.a2[0], r.b[0], acc2, r.sa2, r.sb);
-      acc = mfma_mx<1>(r.a[1], r.b[1], acc, r.sa, r.sb);
-      acc2 = mfma_mx<1>(r.a2[1], r.b[1], acc2, r.sa2, r.sb);
-      acc = mfma_mx<2>(r.a[2], r.b[2], acc, r.sa, r.sb);
-      acc2 = mfma_mx<2>(r.a2[2], r.b[2], acc2, r.sa2, r.sb);
-      acc = mfma_mx<3>(r.a[3], r.b[3], acc, r.sa, r.sb);
-      acc2 = mfma_mx<3>(r.a2[3], r.b[3], acc2, r.sa2, r.sb);
+      const uint32_t sa = r.sa >> r.shift, sa2 = r.sa2 >> r.shift, sb = r.sb >> r.shift;
+      acc = mfma_mx<0>(r.a[0], r.b[0], acc, sa, sb);
+      acc2 = mfma_mx<0>(r.a2[0], r.b[0], acc2, sa2, sb);
+      acc = mfma_mx<1>(r.a[1], r.b[1], acc, sa, sb);
+      acc2 = mfma_mx<1>(r.a2[1], r.b[1], acc2, sa2, sb);
+      acc = mfma_mx<2>(r.a[2], r.b[2], acc, sa, sb);
+      acc2 = mfma_mx<2>(r.a2[2], r.b[2], acc2, sa2, sb);
+      acc = mfma_mx<3>(r.a[3], r.b[3], acc, sa, sb);
+      acc2 = mfma_mx<3>(r.a2[3], r.b[3], acc2, sa2, sb);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -219,7 +224,7 @@ hipError_t launch_direct(const GroupedParams &p, int64_t R, hipStream_t stream) 
   if (items > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const int64_t grid = items < 512 ? items : 512;  // two workgroups on each of the 256 CUs
   const dim3 blocks(static_cast<unsigned>(grid)), threads(64 * kSplit);
-  if (OP == kOpMx && p.chunks % 4)
+  if (OP == kOpMx && p.chunks < 4)
     hipLaunchKernelGGL((k_grouped_direct<OP, EPI, OP != kOpMx>), blocks, threads, 0, stream, p, static_cast<int>(groups));
   else
     hipLaunchKernelGGL((k_grouped_direct<OP, EPI, true>), blocks, threads, 0, stream, p, static_cast<int>(groups));
