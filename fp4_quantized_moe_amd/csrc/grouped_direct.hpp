@@ -21,12 +21,6 @@
 
 namespace quads {
 
-enum GroupedOperands {
-  kOpMx = 0,    // MXFP4 rows, weights [E, N, K]
-  kOpBf16 = 1,  // bf16 rows, weights [E, N, K]
-  kOpBf16T = 2  // bf16 rows, weights [E, K, N] (contraction along the weights' rows)
-};
-
 constexpr int kSplit = 4;  // waves of a workgroup
 
 // A lane's operands of one stage: four 16-byte chunks of each row, and their
@@ -70,15 +64,10 @@ __global__ __launch_bounds__(64 * kSplit, 2) void k_grouped_direct(GroupedParams
     const int32_t n = static_cast<int32_t>(group) * COLS + (lane & 31);
     const int64_t a = min(n, p.width - 1), b = PAIR ? a + p.width : min(n + 32, p.width - 1);
     const uint8_t *we = p.w + walk.e * p.w_expert;
-    if constexpr (OP == kOpBf16T) {
-      wr = we + 2 * a;
-      wr2 = we + 2 * b;
-    } else {
-      wr = we + a * p.w_row;
-      wr2 = we + b * p.w_row;
-      ws = p.w_scales + (static_cast<int64_t>(walk.e) * p.N + a) * p.chunks;
-      ws2 = p.w_scales + (static_cast<int64_t>(walk.e) * p.N + b) * p.chunks;
-    }
+    wr = we + a * p.w_row;
+    wr2 = we + b * p.w_row;
+    ws = p.w_scales + (static_cast<int64_t>(walk.e) * p.N + a) * p.chunks;
+    ws2 = p.w_scales + (static_cast<int64_t>(walk.e) * p.N + b) * p.chunks;
   };
 
   // Stage s of the item into r (chunks at and behind `limit`: zeros).
@@ -91,19 +80,8 @@ __global__ __launch_bounds__(64 * kSplit, 2) void k_grouped_direct(GroupedParams
       const bool in = c0 + j < limit;
       const int64_t c = c0 + j;
       r.b[j] = *reinterpret_cast<const uint4 *>(in ? xr + 16 * c : zero);
-      if constexpr (OP == kOpBf16T) {
-        uint32_t h[8], g[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[i] = *reinterpret_cast<const uint16_t *>(in ? wr + (8 * c + i) * p.w_row : zero);
-          g[i] = *reinterpret_cast<const uint16_t *>(in ? wr2 + (8 * c + i) * p.w_row : zero);
-        }
-        r.a[j] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-        r.a2[j] = make_uint4(g[0] | g[1] << 16, g[2] | g[3] << 16, g[4] | g[5] << 16, g[6] | g[7] << 16);
-      } else {
-        r.a[j] = *reinterpret_cast<const uint4 *>(in ? wr + 16 * c : zero);
-        r.a2[j] = *reinterpret_cast<const uint4 *>(in ? wr2 + 16 * c : zero);
-      }
+      r.a[j] = *reinterpret_cast<const uint4 *>(in ? wr + 16 * c : zero);
+      r.a2[j] = *reinterpret_cast<const uint4 *>(in ? wr2 + 16 * c : zero);
     }
     if constexpr (OP == kOpMx) {
       if constexpr (DWORDS) {

@@ -43,6 +43,12 @@ struct GroupedParams {
   const uint16_t *gu;  // kEpiGatedBwd
 };
 
+enum GroupedOperands {
+  kOpMx = 0,    // MXFP4 rows, weights [E, N, K]
+  kOpBf16 = 1,  // bf16 rows, weights [E, N, K]
+  kOpBf16T = 2  // bf16 rows, weights [E, K, N] (contraction along the weights' rows)
+};
+
 // Zeros that are read in the place of chunks and scales behind K (a scale byte
 // 0 is 2^-127).  Choosing the address, not the data, keeps loads in flight.
 __device__ __attribute__((aligned(16))) uint32_t g_zero_chunk[4];
@@ -220,19 +226,6 @@ __device__ __forceinline__ void store_tile(const GroupedParams &p, const f32x16 
           *reinterpret_cast<uint2 *>(pre + p.width) =
               make_uint2(pack_bf16(b[4 * q], b[4 * q + 1]), pack_bf16(b[4 * q + 2], b[4 * q + 3]));
         }
-      } else {
-        const int64_t at = row * 2 * p.width + n;
-        const uint2 gw = *reinterpret_cast<const uint2 *>(p.gu + at);
-        const uint2 uw = *reinterpret_cast<const uint2 *>(p.gu + at + p.width);
-        float g[4] = {__uint_as_float(gw.x << 16), __uint_as_float(gw.x & 0xFFFF0000u),
-                      __uint_as_float(gw.y << 16), __uint_as_float(gw.y & 0xFFFF0000u)};
-        float u[4] = {__uint_as_float(uw.x << 16), __uint_as_float(uw.x & 0xFFFF0000u),
-                      __uint_as_float(uw.y << 16), __uint_as_float(uw.y & 0xFFFF0000u)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) gated_grad(a[4 * q + i], g[i], u[i]);
-        uint16_t *o = static_cast<uint16_t *>(p.y) + at;
-        *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]));
-        *reinterpret_cast<uint2 *>(o + p.width) = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
       }
     }
   }

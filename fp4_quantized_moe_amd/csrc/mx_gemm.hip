@@ -31,11 +31,19 @@ GroupedParams params(const MxGemmLaunch &a) {
 template <int EPI>
 hipError_t run(const MxGemmLaunch &a, hipStream_t stream) {
   const GroupedParams p = params(a);
-  // From 32 rows an expert on a weight row meets more than one 32-row tile:
-  // staged through LDS.  Scale rows are whole dwords with K % 128 == 0.
-  if (a.R > 32 * a.E) {
+  // The streaming kernels read an expert's weights once for every 32 rows.
+  // One reading is what the call costs anyway (decode); two or three still
+  // pay while they are short beside the 12 us that a staged tile takes from
+  // its first load to its last store.  Measured, streamed against staged:
+  // 17 MB twice 12.4 and 15.2 us, 34 MB twice 12.9 and 13.2, 17 MB four times
+  // 16.5 and 12.8, 268 MB twice 95 and 65.  Rows that do not begin on a line
+  // (K % 128 != 0) stream worse: 8 MB five times 21 and 13.
+  const int64_t readings = (a.R + 32 * static_cast<int64_t>(a.E) - 1) / (32 * static_cast<int64_t>(a.E));
+  const int64_t bytes = static_cast<int64_t>(a.E) * a.N * (a.K / 2) * readings;
+  if (readings > 1 && bytes > (int64_t(a.K % 128 ? 16 : 48) << 20) && a.K >= 128) {
+    // Scale rows are whole dwords with K % 128 == 0.
     if (a.K % 128 == 0) return launch_staged_tiles<kOpMx, EPI>(p, a.R, stream);
-    if (a.K > 128) return launch_staged_tiles<kOpMx, EPI, true>(p, a.R, stream);
+    return launch_staged_tiles<kOpMx, EPI, true>(p, a.R, stream);
   }
   if (a.K % 128 == 0 && stream_items<EPI>(p, a.R) >= kStreamItems) return launch_stream<EPI>(p, stream);
   return launch_direct<kOpMx, EPI>(p, a.R, stream);

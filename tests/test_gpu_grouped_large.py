@@ -176,3 +176,51 @@ def test_two_streams_at_once():
                 got[k] = Q.moe_mxfp4_ffn(xs[k], wg, wd, offs, token)
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("K", [448, 512, 1088])
+def test_nan_and_rows_behind_the_last_expert_staged(K):
+    """At sizes that go through the staged kernel: a NaN block stays in its row or column, rows behind the last
+    expert are left as they were."""
+    R, N, behind = 40000, 256, 77
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    x = Q.quantize_mxfp4(torch.randn(R + behind, K, generator=gen, device="cuda"))
+    w = Q.quantize_mxfp4(torch.randn(1, N, K, generator=gen, device="cuda"))
+    offs = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    clean = Q.moe_mxfp4_gemm(x, w, offs)
+    bad_rows, bad_col = [0, 255, 256, 39999], 200
+    for r in bad_rows:
+        x.scales[r, K // 32 - 1] = 255
+    w.scales.view(N, K // 32)[bad_col, 0] = 255
+    y = torch.full((R + behind, N), 3.0, device="cuda")
+    Q.moe_mxfp4_gemm(x, w, offs, y=y)
+    nan = torch.zeros(R + behind, N, dtype=torch.bool, device="cuda")
+    nan[bad_rows] = True
+    nan[:R, bad_col] = True
+    assert torch.equal(torch.isnan(y), nan)
+    assert bool((y[R:] == 3.0).all())
+    assert torch.equal(y[:R][~nan[:R]], clean[:R][~nan[:R]])
+    q = Q.empty_mxfp4(1, R + behind, N // 2, "cuda")
+    q.codes.fill_(0x5A)
+    q.scales.fill_(0x77)
+    Q.moe_mxfp4_gemm(x, w, offs, epilogue=Q.EPI_SWIGLU, y_dtype=Q.MXFP4, y=q)
+    assert bool((q.codes[R:] == 0x5A).all()) and bool((q.scales[R:] == 0x77).all())
+    hit = torch.zeros(R, N // 64, dtype=torch.bool, device="cuda")
+    hit[bad_rows] = True
+    hit[:, (bad_col - N // 2) // 32] = True  # the up column's block of h
+    assert torch.equal(q.scales[:R] == 255, hit)
+
+
+def test_gated_rows_behind_the_last_expert_staged():
+    R, H, I, behind = 20000, 128, 144, 50
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(R + behind, H, generator=gen, device="cuda").to(torch.bfloat16)
+    w = torch.randn(2, 2 * I, H, generator=gen, device="cuda").to(torch.bfloat16)
+    offs = torch.tensor([0, 137, R], dtype=torch.int32, device="cuda")
+    h, gu = Q.moe_gated_forward(x, w, offs)
+    h2, gu2 = Q.moe_gated_forward(x[:R].contiguous(), w, offs)
+    assert torch.equal(h[:R], h2) and torch.equal(gu[:R], gu2)
+    gu[R:] = 1.0
+    dgu = torch.full_like(gu, 5.0)
+    Q.moe_gated_backward(x, torch.randn(2, H, I, generator=gen, device="cuda").to(torch.bfloat16), gu, offs, dgu=dgu)
+    assert bool((dgu[R:] == 5.0).all()) and not bool((dgu[:R] == 5.0).any(1).all())
