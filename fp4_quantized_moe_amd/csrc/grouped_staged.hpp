@@ -5,9 +5,10 @@
 // A stage is 128 bytes of K (256 MXFP4 or 64 bf16 elements) of TN weight and
 // TM routed rows; two stages in LDS.  128 bytes are one cache line, so every
 // staging instruction reads whole lines (8 rows of 8 chunks).  Row r keeps its
-// chunk c in slot c ^ (r % 8): the 8 rows a fragment read touches together
-// then lie in 8 different 16-byte bank groups, and the permutation is applied
-// to the source address of the DMA, within the line.
+// chunk c in slot c ^ (r / 2 % 8): 16 consecutive rows of a fragment read then
+// take each of the 16-byte groups of the 64 banks (two rows of 128 bytes)
+// once, and the permutation is applied to the source address of the DMA,
+// within the line.
 //
 // With kOpBf16T the weights' part of a stage is 64 rows k of TN columns, and
 // fragments are gathered by the transposing LDS read: a group of 16 lanes
@@ -44,7 +45,6 @@ __device__ __forceinline__ void each(F &&f) {
   each_index(static_cast<F &&>(f), std::make_integer_sequence<int, N>{});
 }
 
-
 template <int OP_, int TM_, int TN_, int WM_, int WN_, bool ODD_ = false>
 struct StagedCfg {
   static constexpr int OP = OP_, TM = TM_, TN = TN_, WM = WM_, WN = WN_;
@@ -59,13 +59,13 @@ struct StagedCfg {
   static constexpr bool ODD = ODD_, SLDS = MX && !ODD;
   static constexpr int KROWS = 512 / TN;  // kOpBf16T: weight rows of one staging instruction
   static constexpr int SLOADS = SLDS ? ROWS / 32 / WAVES : 0;  // scale instructions (32 rows each)
-  static constexpr int TURN = 2 * (ROWS * 128 + (SLDS ? ROWS * 8 : 0));  // LDS: two stages, then the epilogue's blocks,
+  static constexpr int STAGE = ROWS * 128 + (SLDS ? ROWS * 8 : 0);
+  static constexpr int TURN = 2 * STAGE;  // LDS: two stages, then the epilogue's blocks,
   // Rows of the blocks that the epilogue turns around: whole lines, or half
   // ones for the small tile, of which two workgroups then fit a CU.
   static constexpr int RB = NI >= 4 ? 128 : 64, TURN_BYTES = 32 * RB;
   static constexpr int TOKENS = TURN + WAVES * TURN_BYTES;             // then the next tile's token ids
   static constexpr int LDS = TOKENS + 256 * WAVES;
-  static constexpr int STAGE = ROWS * 128 + (SLDS ? ROWS * 8 : 0);
   static constexpr int ALL = LOADS + SLOADS;
   // Staging instructions issued in a stage's last step and in the next
   // stage's first.  Three quarters and a quarter measured best (8192 x 8192 x
@@ -326,6 +326,16 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
     u.n0 = static_cast<int32_t>(at % col_tiles) * COLS;
   };
 
+  // Rows of a tile that a wave takes: with at most half of the large tile's
+  // rows (an expert's last ones) the waves halve those, and do half the
+  // products (512 rows an expert on average: 677 -> 647 us for the gated
+  // forward).  There only: in the others the second form of the loops makes
+  // the compiler spill (the backward 478 -> 531 us, MXFP4 547 -> 555).
+  constexpr bool HALVES = PAIR && C::MI >= 4 && !C::MX;
+  const auto wave_rows = [](const StagedTile &u) {
+    return HALVES && u.rows <= C::TM / 2 ? C::TM / C::WM / 2 : C::TM / C::WM;
+  };
+
   // This lane's staging sources; each moves on by one stage when it is used.
   const uint8_t *from[C::LOADS], *sfrom[C::SLOADS + 1];
   const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_chunk);
@@ -405,7 +415,9 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
 
   // Fragment addresses: row (lane % 32) of a 32-row group, chunk 4 half + s.
   const int fr = lane & 31;
-  const int arow = wn * (C::TN / C::WN) + fr, brow = C::TN + wm * (C::TM / C::WM) + fr;
+  const int arow = wn * (C::TN / C::WN) + fr;
+  const auto first_brow = [&](const StagedTile &u) { return C::TN + wm * wave_rows(u) + fr; };
+  int brow = first_brow(t);  // of the fragments that are read
   // kOpBf16T: lane 16 g + 4 j + b of a transposing read addresses row j and
   // columns 16 (g % 2) + 4 b .. + 3 of the fragment's 32, in half g / 2.
   int tcol[C::NI];
@@ -421,7 +433,7 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   struct Scales {
     uint32_t a[C::NI], b[C::MI];
   };
-  constexpr int FRAGS = C::NI + C::MI, SLOTS = C::NI * C::MI;
+  constexpr int FRAGS = C::NI + C::MI;
   // Item r of a step's fragment reads, in the order the products need them:
   // a[0], all of b, then the other a; behind them a stage's scales.
   const auto read_item = [&](Frag &f, Scales &sf, const uint8_t *base, int s, auto rc) {
@@ -479,21 +491,24 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   // at gbase) and, in a stage's last step, the next stage's scales and the
   // staging of stage ds between them, in exactly this order.  Left to itself
   // the compiler puts the reads last, where the next step waits for them.
-  const auto step = [&](auto sel, const Frag &f, Frag &g, Scales &gsc, const uint8_t *gbase, int gs, int ds,
+  // MA: row groups of 32 that the tile has for each wave.
+  const auto step = [&](auto ma, auto sel, const Frag &f, Frag &g, Scales &gsc, const uint8_t *gbase, int gs, int ds,
                         uint8_t *dbase) {
-    constexpr int S = decltype(sel)::value;
+    constexpr int S = decltype(sel)::value, MA = decltype(ma)::value, SLOTS = C::NI * MA;
+    constexpr int MR = S == 3 ? C::MI : MA;  // the last step's reads may be for another tile
     constexpr int DF = S == 3 ? 0 : C::LATE, DN = S == 3 ? C::LATE : S == 0 ? C::ALL - C::LATE : 0;
-    constexpr int READS = FRAGS + (C::SLDS && S == 3 ? FRAGS : 0);
+    constexpr int READS = C::NI + MR + (C::SLDS && S == 3 ? FRAGS : 0);
     constexpr int RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
     each<SLOTS>([&](auto slot) {
-      constexpr int n = decltype(slot)::value, i = n / C::MI, k = n % C::MI;
+      constexpr int n = decltype(slot)::value, i = n / MA, k = n % MA;
       if constexpr (C::MX)
         acc[i][k] = mfma_mx<S>(f.a[i], f.b[k], acc[i][k], sc.a[i], sc.b[k]);
       else
         acc[i][k] = mfma_bf16(f.a[i], f.b[k], acc[i][k]);
       each<RPS>([&](auto q) {
         constexpr int r = n * RPS + decltype(q)::value;
-        if constexpr (r < READS) read_item(g, gsc, gbase, gs, std::integral_constant<int, r>{});
+        if constexpr (r < READS)
+          read_item(g, gsc, gbase, gs, std::integral_constant<int, (r <= MR ? r : r + C::MI - MR)>{});
       });
       each<DPS>([&](auto q) {
         constexpr int d = n * DPS + decltype(q)::value;
@@ -506,12 +521,12 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   // follows in its first step, and stage `ds` begins in its last; `between` may
   // aim at another tile.
   uint8_t *cur = lds;
-  const auto stage = [&](int now, int ds, auto between) {
+  const auto stage = [&](auto ma, int now, int ds, auto between, int next_brow) {
     uint8_t *nxt = lds + (cur == lds ? C::STAGE : 0);
-    step(std::integral_constant<int, 0>{}, f0, f1, sc, cur, 1, now, nxt);
-    step(std::integral_constant<int, 1>{}, f1, f0, sc, cur, 2, 0, cur);
+    step(ma, std::integral_constant<int, 0>{}, f0, f1, sc, cur, 1, now, nxt);
+    step(ma, std::integral_constant<int, 1>{}, f1, f0, sc, cur, 2, 0, cur);
     between();
-    step(std::integral_constant<int, 2>{}, f0, f1, sc, cur, 3, 0, cur);
+    step(ma, std::integral_constant<int, 2>{}, f0, f1, sc, cur, 3, 0, cur);
     wait_lgkm0();  // step 3's fragments are in registers: this wave is done with the stage's LDS
     wait_vm<0>();  // and its part of the next stage has landed
     barrier_no_fence();
@@ -520,7 +535,8 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
       take_scales(next);
       load_scales(ds);
     }
-    step(std::integral_constant<int, 3>{}, f1, f0, next, nxt, 0, ds, cur);
+    brow = next_brow;
+    step(ma, std::integral_constant<int, 3>{}, f1, f0, next, nxt, 0, ds, cur);
     if constexpr (C::MX) sc = next;
     cur = nxt;
   };
@@ -545,8 +561,6 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   for (int i = 0; i < C::NI; ++i)
 #pragma unroll
     for (int k = 0; k < C::MI; ++k) acc[i][k] = f32x16{};
-  // A stage is one block of code without branches: with one inside, the
-  // compiler sinks the products past all the reads.
   // Names every accumulator as an accumulation register where the loops meet
   // (no instruction): the compiler otherwise carries them in ordinary
   // registers and copies all of them twice a stage.
@@ -556,10 +570,12 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
 #pragma unroll
       for (int k = 0; k < C::MI; ++k) asm volatile("" : "+a"(acc[i][k]));
   };
-  while (true) {
+  // All stages of a tile.  A stage is one block of code without branches: with
+  // one inside, the compiler sinks the products past all the reads.
+  const auto contract = [&](auto ma) {
     for (int s = 2; s < stages; ++s) {
       pin();
-      stage(s - 1, s, [] {});
+      stage(ma, s - 1, s, [] {}, brow);
     }
     pin();
     if (stages == 2) {  // no barrier since the tokens were sent for
@@ -567,22 +583,32 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
       barrier_no_fence();
     }
     // The last two stages bring the next tile's first two.
-    stage(stages - 1, 0, [&] {
+    stage(ma, stages - 1, 0, [&] {
       limit = nt.e < 0 ? 0 : p.chunks;
       if (nt.e >= 0)
         aim(nt, [&](int r) -> int64_t {
           const int m = min(r, nt.rows - 1);
           return p.row_token ? tokens[m] : nt.r0 + m;
         });
-    });
+    }, brow);
     pin();
-    stage(0, 1, [] {});
+    stage(ma, 0, 1, [] {}, first_brow(nt));
     pin();
+  };
+  while (true) {
+    if constexpr (HALVES) {
+      if (t.rows <= C::TM / 2)
+        contract(std::integral_constant<int, C::MI / 2>{});
+      else
+        contract(std::integral_constant<int, C::MI>{});
+    } else {
+      contract(std::integral_constant<int, C::MI>{});
+    }
     uint8_t *turn = lds + C::TURN + wave * C::TURN_BYTES;
     const int fl = fresh_lane();
     const int32_t wn0 = t.n0 + wn * (C::TN / C::WN) / (PAIR ? 2 : 1);
-    const int64_t wrow = static_cast<int64_t>(t.r0) + wm * (C::TM / C::WM);
-    const int wrows = t.rows - wm * (C::TM / C::WM);
+    const int64_t wrow = static_cast<int64_t>(t.r0) + wm * wave_rows(t);
+    const int wrows = min(t.rows - wm * wave_rows(t), wave_rows(t));
     if constexpr (EPI == kEpiGatedBwd) {
       constexpr int TILES = C::RB / 64, ACROSS = C::NI / TILES, BLOCKS = C::MI * ACROSS;
       each<BLOCKS>([&](auto bc) {
