@@ -224,3 +224,26 @@ def test_gated_rows_behind_the_last_expert_staged():
     dgu = torch.full_like(gu, 5.0)
     Q.moe_gated_backward(x, torch.randn(2, H, I, generator=gen, device="cuda").to(torch.bfloat16), gu, offs, dgu=dgu)
     assert bool((dgu[R:] == 5.0).all()) and not bool((dgu[:R] == 5.0).any(1).all())
+
+
+def test_quantize_past_32_bits_of_lanes():
+    """2^34 elements are 2^31 lanes of 8: a launch's most.  Slices around the
+    seam and at both ends against the same slices quantized alone."""
+    n = 2 ** 34 + 4096
+    x = torch.zeros(n // 32, 32, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    seam = 2 ** 34 // 32
+    parts = [slice(0, 64), slice(2 ** 31 // 32 - 32, 2 ** 31 // 32 + 32), slice(seam - 64, seam + 64), slice(n // 32 - 40, n // 32)]
+    for p in parts:
+        x[p] = torch.randn(x[p].shape, generator=gen, device="cuda").bfloat16()
+    q = Q.quantize_mxfp4(x)
+    back = Q.dequantize_mxfp4(q)
+    for p in parts:
+        alone = Q.quantize_mxfp4(x[p].contiguous())
+        assert torch.equal(q.codes[p], alone.codes) and torch.equal(q.scales[p], alone.scales), p
+        assert torch.equal(back[p], Q.dequantize_mxfp4(alone)), p
+    assert int(q.scales.count_nonzero()) <= sum(p.stop - p.start for p in parts)
+    del back
+    out, _ = Q.weight_qdq_mxfp4(x)
+    for p in parts:
+        assert torch.equal(out[p], Q.weight_qdq_mxfp4(x[p].contiguous())[0]), p
