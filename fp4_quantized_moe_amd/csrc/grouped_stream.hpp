@@ -11,6 +11,13 @@
 // three stages and issues the DMA of the next but two as soon as a stage's
 // fragments are in registers, also across items: no barriers, and about
 // 100 KB of weights in flight on every CU.
+//
+// ONCE: the weights are read past the caches, for calls that read them once.
+// With those of several layers in turn, as in a model, the MXFP4 block of 256
+// tokens took 94 instead of 101 us (4.65 TB/s; its projections 59.6 and 36.4
+// instead of 63.4 and 38.2); a lone layer that finds a part of its weights in
+// the last-level cache loses by it (285 MB: 51 -> 54 us).  With two row tiles
+// an expert the second would find them there: 12.6 -> 13.9 us.
 #pragma once
 
 #include "dma.hpp"
@@ -23,7 +30,7 @@ constexpr int kStreamRows = 96;                          // 64 weight rows, 32 r
 constexpr int kStreamStage = kStreamRows * (128 + 8);    // bytes: chunks, then scales
 constexpr int kStreamLoads = kStreamRows / 8 + kStreamRows / 32;  // DMA instructions of a stage
 
-template <int EPI>
+template <int EPI, bool ONCE>
 __global__ __launch_bounds__(64 * kStreamWaves, 1) void k_grouped_stream(GroupedParams p, int col_groups) {
   constexpr bool PAIR = EPI == kEpiSwiglu || EPI == kEpiSwigluMx;
   constexpr int COLS = PAIR ? 32 : 64;
@@ -75,6 +82,12 @@ __global__ __launch_bounds__(64 * kStreamWaves, 1) void k_grouped_stream(Grouped
     second = other * p.w_row;
     second_scale = static_cast<int64_t>(other) * p.chunks;
   };
+  const auto bring = [](const uint8_t *src, uint8_t *to) {
+    if constexpr (ONCE)
+      dma_once(src, to);
+    else
+      dma(src, to, 16);
+  };
   const auto fetch = [&](int s, uint8_t *base) {
     const int64_t off = 128 * static_cast<int64_t>(s);
     const bool in0 = 8 * s + chunk0 < p.chunks, in1 = 8 * s + (chunk0 ^ 4) < p.chunks;
@@ -83,9 +96,9 @@ __global__ __launch_bounds__(64 * kStreamWaves, 1) void k_grouped_stream(Grouped
     for (int j = 0; j < 8; ++j) {
       const uint8_t *src = wsrc + (j >= 4 ? second : 0) + 8 * (j & 3) * p.w_row + off;
       if (j & 1)  // the swizzle of rows 16 k + 8 ..
-        dma(in1 ? src + ((chunk0 ^ 4) - chunk0) * 16 : zero, base + 1024 * j, 16);
+        bring(in1 ? src + ((chunk0 ^ 4) - chunk0) * 16 : zero, base + 1024 * j);
       else
-        dma(in0 ? src : zero, base + 1024 * j, 16);
+        bring(in0 ? src : zero, base + 1024 * j);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) dma((j & 1 ? in1 : in0) ? xsrc[j] + off : zero, base + 1024 * (8 + j), 16);
@@ -181,10 +194,14 @@ int64_t stream_items(const GroupedParams &p, int64_t R) {
 }
 
 template <int EPI>
-hipError_t launch_stream(const GroupedParams &p, hipStream_t stream) {
+hipError_t launch_stream(const GroupedParams &p, int64_t R, hipStream_t stream) {
   constexpr int COLS = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? 32 : 64;
-  hipLaunchKernelGGL((k_grouped_stream<EPI>), dim3(256), dim3(64 * kStreamWaves), 0, stream, p,
-                     (p.width + COLS - 1) / COLS);
+  const int groups = (p.width + COLS - 1) / COLS;
+  const dim3 grid(256), threads(64 * kStreamWaves);
+  if (R <= 32 * static_cast<int64_t>(p.E))
+    hipLaunchKernelGGL((k_grouped_stream<EPI, true>), grid, threads, 0, stream, p, groups);
+  else
+    hipLaunchKernelGGL((k_grouped_stream<EPI, false>), grid, threads, 0, stream, p, groups);
   return hipGetLastError();
 }
 

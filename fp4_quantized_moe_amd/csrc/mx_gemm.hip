@@ -45,7 +45,7 @@ hipError_t run(const MxGemmLaunch &a, hipStream_t stream) {
     if (a.K % 128 == 0) return launch_staged_tiles<kOpMx, EPI>(p, a.R, stream);
     return launch_staged_tiles<kOpMx, EPI, true>(p, a.R, stream);
   }
-  if (a.K % 128 == 0 && stream_items<EPI>(p, a.R) >= kStreamItems) return launch_stream<EPI>(p, stream);
+  if (a.K % 128 == 0 && stream_items<EPI>(p, a.R) >= kStreamItems) return launch_stream<EPI>(p, a.R, stream);
   return launch_direct<kOpMx, EPI>(p, a.R, stream);
 }
 
