@@ -11,6 +11,7 @@
 
 #include "../../include/quads.h"
 #include "launch.hpp"
+#include "mx_launch.hpp"
 
 namespace {
 

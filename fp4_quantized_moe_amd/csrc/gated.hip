@@ -6,7 +6,7 @@
 // projection would cost twice the backward's own product).  dh exists in the
 // accumulators only: the backward's epilogue reads g and u and writes d g, d u.
 #include "grouped_staged.hpp"
-#include "launch.hpp"
+#include "mx_launch.hpp"
 
 namespace quads {
 namespace {

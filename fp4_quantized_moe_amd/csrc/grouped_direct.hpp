@@ -16,7 +16,7 @@
 // one, across items and their barrier too: what keeps HBM busy.
 #pragma once
 
-#include "dma.hpp"
+#include "grouped_dma.hpp"
 #include "grouped_tile.hpp"
 
 namespace quads {

@@ -30,7 +30,7 @@
 #include <type_traits>
 #include <utility>
 
-#include "dma.hpp"
+#include "grouped_dma.hpp"
 #include "grouped_direct.hpp"
 
 namespace quads {
@@ -400,13 +400,13 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
     constexpr int j = decltype(jc)::value;
     if constexpr (j >= C::LOADS) {
       constexpr int k = j - C::LOADS;
-      dma(8 * s + 4 * (lane & 1) < limit ? sfrom[k] : zero, base + C::ROWS * 128 + (k * C::WAVES + wave) * 256, 4);
+      dma_wave(8 * s + 4 * (lane & 1) < limit ? sfrom[k] : zero, base + C::ROWS * 128 + (k * C::WAVES + wave) * 256, 4);
       sfrom[k] += 8;
     } else if constexpr (C::TRANS && j < C::WLOADS) {
-      dma(64 * s + wk + j * C::WAVES * C::KROWS < 8 * limit ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
+      dma_wave(64 * s + wk + j * C::WAVES * C::KROWS < 8 * limit ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
       from[j] += 64 * p.w_row;
     } else {
-      dma(8 * s + chunk < limit ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
+      dma_wave(8 * s + chunk < limit ? from[j] : zero, base + (j * C::WAVES + wave) * 1024, 16);
       from[j] += 128;
     }
   };
@@ -414,7 +414,7 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
   int32_t *tokens = reinterpret_cast<int32_t *>(lds + C::TOKENS);
   const auto fetch_tokens = [&](const StagedTile &u) {
     if (p.row_token == nullptr || u.e < 0) return;
-    dma(p.row_token + u.r0 + min(64 * wave + lane, u.rows - 1), tokens + 64 * wave, 4);
+    dma_wave(p.row_token + u.r0 + min(64 * wave + lane, u.rows - 1), tokens + 64 * wave, 4);
   };
 
   // Fragment addresses: row (lane % 32) of a 32-row group, chunk 4 half + s.

@@ -20,7 +20,7 @@
 // an expert the second would find them there: 12.6 -> 13.9 us.
 #pragma once
 
-#include "dma.hpp"
+#include "grouped_dma.hpp"
 #include "grouped_tile.hpp"
 
 namespace quads {
@@ -84,9 +84,9 @@ __global__ __launch_bounds__(64 * kStreamWaves, 1) void k_grouped_stream(Grouped
   };
   const auto bring = [](const uint8_t *src, uint8_t *to) {
     if constexpr (ONCE)
-      dma_once(src, to);
+      dma_wave_once(src, to);
     else
-      dma(src, to, 16);
+      dma_wave(src, to, 16);
   };
   const auto fetch = [&](int s, uint8_t *base) {
     const int64_t off = 128 * static_cast<int64_t>(s);
@@ -101,11 +101,11 @@ __global__ __launch_bounds__(64 * kStreamWaves, 1) void k_grouped_stream(Grouped
         bring(in0 ? src : zero, base + 1024 * j);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dma((j & 1 ? in1 : in0) ? xsrc[j] + off : zero, base + 1024 * (8 + j), 16);
+    for (int j = 0; j < 4; ++j) dma_wave((j & 1 ? in1 : in0) ? xsrc[j] + off : zero, base + 1024 * (8 + j), 16);
     uint8_t *sc = base + kStreamRows * 128;
-    dma(sin ? wscale + 8 * s : zero, sc, 4);
-    dma(sin ? wscale + second_scale + 8 * s : zero, sc + 256, 4);
-    dma(sin ? xscale + 8 * s : zero, sc + 512, 4);
+    dma_wave(sin ? wscale + 8 * s : zero, sc, 4);
+    dma_wave(sin ? wscale + second_scale + 8 * s : zero, sc + 256, 4);
+    dma_wave(sin ? xscale + 8 * s : zero, sc + 512, 4);
   };
 
   const int stages = (p.chunks + 7) / 8;

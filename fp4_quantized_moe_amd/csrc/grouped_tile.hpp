@@ -19,7 +19,7 @@
 #include <stdint.h>
 
 #include "fp4_mfma.hpp"
-#include "launch.hpp"
+#include "mx_launch.hpp"
 #include "mx_device.hpp"
 #include "quads_device.hpp"
 

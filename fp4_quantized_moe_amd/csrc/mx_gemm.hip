@@ -4,7 +4,7 @@
 // 32-element block product by 2^(E_w + E_x) and accumulates in fp32.
 #include "grouped_staged.hpp"
 #include "grouped_stream.hpp"
-#include "launch.hpp"
+#include "mx_launch.hpp"
 
 namespace quads {
 namespace {

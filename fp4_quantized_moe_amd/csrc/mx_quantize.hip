@@ -8,7 +8,7 @@
 // read 2 (4) and write 0.53 bytes an element, QDQ reads and writes 2.
 #include <algorithm>
 
-#include "launch.hpp"
+#include "mx_launch.hpp"
 #include "mx_device.hpp"
 
 namespace quads {
