@@ -674,15 +674,25 @@ hipError_t launch_staged(const GroupedParams &p, int64_t R, hipStream_t stream) 
 }
 
 // The large and the small tile.  256 x 256 reads each operand half as often
-// and its waves read LDS least per product (8192 x 8192 x 8192 MXFP4: 308 us
-// against 434 us with 128 x 128), but wants rows to fill it and tiles to fill
-// the card: from 128 rows an expert on, and three quarters of the CUs with a
-// tile (4096 x 1536 x 2048, 96 large tiles: 25.5 against 19.6 us).
+// and its waves read LDS least per product (8192 x 8192 x 8192 MXFP4: 282 us
+// against 422 us with 128 x 128), but wants rows to fill it, from 128 an
+// expert on, and fills the card in coarse rounds of 256 tiles.  Small tiles
+// run two a CU, one's stores under the other's products, in rounds of 512
+// that take 0.5 to 0.6 of a large one's with short contractions and in the
+// backward, 0.6 to 0.75 from 16 stages on.  An expert adds half a row tile.
+// Large against small, with the rounds: 4096 x 1536 x 2048 21.7 and 16 us (1,
+// 1); 32768 x 800 x 992 in 16 groups 47 and 37 (3, 4); 131072 x 1536 x 2048 in
+// 64 groups 310 and 362 (13, 25); backward of 32032 x 1408 x 1152 in 16 groups
+// 237 and 205 (4, 6), of 65536 x 1456 x 2048 in 32 637 and 691 (7, 13).
 template <int OP, int EPI, bool ODD = false>
 hipError_t launch_staged_tiles(const GroupedParams &p, int64_t R, hipStream_t stream) {
-  constexpr int COLS = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? 128 : 256;
-  const int64_t tiles = (R + 255) / 256 * ((p.width + COLS - 1) / COLS);
-  if (R >= 128 * static_cast<int64_t>(p.E) && tiles >= 192)
+  constexpr int PAIRED = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? 2 : 1;
+  const auto rounds = [&](int64_t tile, int64_t places) {
+    const int64_t rows = (R + tile * p.E / 2 + tile - 1) / tile, cols = (PAIRED * static_cast<int64_t>(p.width) + tile - 1) / tile;
+    return (rows * cols + places - 1) / places;
+  };
+  const int64_t percent = p.chunks >= 16 * 8 && EPI != kEpiGatedBwd ? 65 : 57;
+  if (R >= 128 * static_cast<int64_t>(p.E) && 100 * rounds(256, 256) <= percent * rounds(128, 512))
     return launch_staged<StagedCfg<OP, 256, 256, 2, 2, ODD>, EPI>(p, R, stream);
   return launch_staged<StagedCfg<OP, 128, 128, 2, 2, ODD>, EPI>(p, R, stream);
 }

@@ -85,7 +85,9 @@ def test_mxfp4(kind, E, R, N, K):
 
 @pytest.mark.parametrize("kind, E, R, H, I", [
     ("even", 32, 32 * 520, 512, 512), ("skewed", 8, 30000, 64, 272), ("last", 5, 10000, 192, 1040),
-    ("skewed", 200, 20000, 128, 128), ("even", 64, 64 * 60, 320, 192)])
+    ("skewed", 200, 20000, 128, 128), ("even", 64, 64 * 60, 320, 192),
+    # 256-row tiles in the forward too, of 1, 3, 17 and 2 stages, with last tiles above and below 128 rows
+    ("skewed", 16, 4900, 64, 880), ("even", 16, 16 * 310, 192, 896), ("skewed", 16, 4900, 1088, 864), ("last", 3, 6000, 128, 1040)])
 def test_gated(kind, E, R, H, I):
     ends, offs, token = grouping(kind, E, R, 4000)
     gen = torch.Generator(device="cuda").manual_seed(H)
