@@ -76,7 +76,8 @@ EXPORTS = [
     "quads_moe_route_workspace_bytes", "quads_moe_route", "quads_moe_combine",
     "quads_moe_wgrad_workspace_bytes", "quads_moe_wgrad_bf16", "quads_transpose_bf16",
     "quads_quantize_mxfp4", "quads_dequantize_mxfp4", "quads_weight_qdq_mxfp4",
-    "quads_moe_mxfp4_gemm", "quads_moe_mxfp4_ffn_workspace_bytes", "quads_moe_mxfp4_ffn",
+    "quads_moe_mxfp4_gemm", "quads_moe_mxfp4_gemm_kernel",
+    "quads_moe_mxfp4_ffn_workspace_bytes", "quads_moe_mxfp4_ffn",
     "quads_moe_gated_forward_bf16", "quads_moe_gated_backward_bf16",
 ]
 
@@ -143,6 +144,8 @@ def load(path: str = LIB_PATH):
     L.quads_weight_qdq_mxfp4.argtypes = [_vp, _c_i64, _c_i64, _c_i64, _vp, ctypes.POINTER(_MXFP4), _c_u32, _vp]
     L.quads_moe_mxfp4_gemm.restype = ctypes.c_int
     L.quads_moe_mxfp4_gemm.argtypes = [ctypes.POINTER(_MxGemmArgs), _vp]
+    L.quads_moe_mxfp4_gemm_kernel.restype = _c_i32
+    L.quads_moe_mxfp4_gemm_kernel.argtypes = [ctypes.POINTER(_MxGemmArgs)]
     L.quads_moe_mxfp4_ffn_workspace_bytes.restype = ctypes.c_size_t
     L.quads_moe_mxfp4_ffn_workspace_bytes.argtypes = [_c_i64, _c_i64, _c_i64, _c_i64]
     L.quads_moe_mxfp4_ffn.restype = ctypes.c_int
@@ -834,6 +837,21 @@ def moe_mxfp4_gemm(x: MXFP4Tensor, w: MXFP4Tensor, expert_offsets: torch.Tensor,
                     None if row_token is None else row_token.data_ptr(), expert_offsets.data_ptr(), y_data, y_scales)
     _on_device(x.codes, load().quads_moe_mxfp4_gemm, what, ctypes.byref(a))
     return y
+
+
+_MX_KERNELS = ("none", "direct", "stream", "staged_small", "staged_large")
+
+
+def mxfp4_gemm_kernel(num_rows: int, num_experts: int, N: int, K: int, epilogue: int = EPI_NONE,
+                      y_dtype=torch.float32) -> str:
+    """quads_moe_mxfp4_gemm_kernel: which kernel moe_mxfp4_gemm takes for these sizes."""
+    code = MXFP4 if y_dtype == MXFP4 else BF16 if y_dtype == torch.bfloat16 else F32
+    any_array = 16  # an aligned address that is not touched
+    a = _MxGemmArgs(_MX_GEMM_SIZE, 0, epilogue, code, num_experts, 0, num_rows, num_rows, N, K, *[any_array] * 8)
+    kernel = load().quads_moe_mxfp4_gemm_kernel(ctypes.byref(a))
+    if kernel < 0:
+        _check(kernel, "mxfp4_gemm_kernel")
+    return _MX_KERNELS[kernel]
 
 
 def moe_mxfp4_ffn(x: torch.Tensor, w_gate_up: MXFP4Tensor, w_down: MXFP4Tensor, expert_offsets: torch.Tensor,

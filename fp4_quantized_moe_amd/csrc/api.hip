@@ -564,7 +564,8 @@ static quads_status_t grouped_shape(const char *what, int32_t E, int64_t R, int6
   return QUADS_OK;
 }
 
-quads_status_t quads_moe_mxfp4_gemm(const quads_moe_mxfp4_args *a, void *stream) {
+static quads_status_t mx_gemm_fill(const quads_moe_mxfp4_args *a, quads::MxGemmLaunch &g) {
+  g = quads::MxGemmLaunch{};
   if (!a) return fail(QUADS_ERR_ARG, "mxfp4_gemm: null args");
   if (a->struct_size != sizeof(quads_moe_mxfp4_args))
     return fail(QUADS_ERR_ARG, "mxfp4_gemm: struct_size %u != %zu", a->struct_size, sizeof(quads_moe_mxfp4_args));
@@ -583,10 +584,8 @@ quads_status_t quads_moe_mxfp4_gemm(const quads_moe_mxfp4_args *a, void *stream)
   if (!a->expert_offsets || !a->w_codes || !a->w_scales) return fail(QUADS_ERR_ARG, "mxfp4_gemm: null pointer");
   if (misaligned({a->x_codes, a->x_scales, a->w_codes, a->w_scales, a->y, a->y_scales}))
     return fail(QUADS_ERR_ARG, "mxfp4_gemm: arrays must be 16-byte aligned");
-  if (a->num_rows == 0) return ok();
-  if (!a->x_codes || !a->x_scales || !a->y || (a->y_dtype == QUADS_MXFP4 && !a->y_scales))
+  if (a->num_rows > 0 && (!a->x_codes || !a->x_scales || !a->y || (a->y_dtype == QUADS_MXFP4 && !a->y_scales)))
     return fail(QUADS_ERR_ARG, "mxfp4_gemm: null pointer");
-  quads::MxGemmLaunch g{};
   g.epi = !swiglu ? (a->y_dtype == QUADS_F32 ? quads::kEpiF32 : quads::kEpiBf16)
                   : (a->y_dtype == QUADS_BF16 ? quads::kEpiSwiglu : quads::kEpiSwigluMx);
   g.E = a->num_experts;
@@ -601,7 +600,20 @@ quads_status_t quads_moe_mxfp4_gemm(const quads_moe_mxfp4_args *a, void *stream)
   g.expert_offsets = a->expert_offsets;
   g.y = a->y;
   g.y_scales = a->y_dtype == QUADS_MXFP4 ? a->y_scales : nullptr;
+  return ok();
+}
+
+quads_status_t quads_moe_mxfp4_gemm(const quads_moe_mxfp4_args *a, void *stream) {
+  quads::MxGemmLaunch g;
+  const quads_status_t st = mx_gemm_fill(a, g);
+  if (st != QUADS_OK || g.R == 0) return st;
   return device_status(quads::launch_mx_gemm(g, static_cast<hipStream_t>(stream)), "mxfp4_gemm");
+}
+
+int32_t quads_moe_mxfp4_gemm_kernel(const quads_moe_mxfp4_args *a) {
+  quads::MxGemmLaunch g;
+  const quads_status_t st = mx_gemm_fill(a, g);
+  return st != QUADS_OK ? st : quads::mx_gemm_kernel(g);
 }
 
 static int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }

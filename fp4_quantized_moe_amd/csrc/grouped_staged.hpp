@@ -684,15 +684,20 @@ hipError_t launch_staged(const GroupedParams &p, int64_t R, hipStream_t stream) 
 // 1); 32768 x 800 x 992 in 16 groups 47 and 37 (3, 4); 131072 x 1536 x 2048 in
 // 64 groups 310 and 362 (13, 25); backward of 32032 x 1408 x 1152 in 16 groups
 // 237 and 205 (4, 6), of 65536 x 1456 x 2048 in 32 637 and 691 (7, 13).
-template <int OP, int EPI, bool ODD = false>
-hipError_t launch_staged_tiles(const GroupedParams &p, int64_t R, hipStream_t stream) {
+template <int EPI>
+bool staged_large(const GroupedParams &p, int64_t R) {
   constexpr int PAIRED = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? 2 : 1;
   const auto rounds = [&](int64_t tile, int64_t places) {
     const int64_t rows = (R + tile * p.E / 2 + tile - 1) / tile, cols = (PAIRED * static_cast<int64_t>(p.width) + tile - 1) / tile;
     return (rows * cols + places - 1) / places;
   };
   const int64_t percent = p.chunks >= 16 * 8 && EPI != kEpiGatedBwd ? 65 : 57;
-  if (R >= 128 * static_cast<int64_t>(p.E) && 100 * rounds(256, 256) <= percent * rounds(128, 512))
+  return R >= 128 * static_cast<int64_t>(p.E) && 100 * rounds(256, 256) <= percent * rounds(128, 512);
+}
+
+template <int OP, int EPI, bool ODD = false>
+hipError_t launch_staged_tiles(const GroupedParams &p, int64_t R, hipStream_t stream) {
+  if (staged_large<EPI>(p, R))
     return launch_staged<StagedCfg<OP, 256, 256, 2, 2, ODD>, EPI>(p, R, stream);
   return launch_staged<StagedCfg<OP, 128, 128, 2, 2, ODD>, EPI>(p, R, stream);
 }

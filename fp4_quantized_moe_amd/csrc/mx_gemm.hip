@@ -29,8 +29,8 @@ GroupedParams params(const MxGemmLaunch &a) {
 }
 
 template <int EPI>
-hipError_t run(const MxGemmLaunch &a, hipStream_t stream) {
-  const GroupedParams p = params(a);
+MxKernel choose(const MxGemmLaunch &a, const GroupedParams &p) {
+  if (a.R == 0) return kMxNone;
   // The streaming kernels read an expert's weights once for every 32 rows.
   // One reading is what the call costs anyway (decode); two or three still
   // pay while they are short beside the 12 us that a staged tile takes from
@@ -40,24 +40,42 @@ hipError_t run(const MxGemmLaunch &a, hipStream_t stream) {
   // (K % 128 != 0) stream worse: 8 MB five times 21 and 13.
   const int64_t readings = (a.R + 32 * static_cast<int64_t>(a.E) - 1) / (32 * static_cast<int64_t>(a.E));
   const int64_t bytes = static_cast<int64_t>(a.E) * a.N * (a.K / 2) * readings;
-  if (readings > 1 && bytes > (int64_t(a.K % 128 ? 16 : 48) << 20) && a.K >= 128) {
-    // Scale rows are whole dwords with K % 128 == 0.
-    if (a.K % 128 == 0) return launch_staged_tiles<kOpMx, EPI>(p, a.R, stream);
-    return launch_staged_tiles<kOpMx, EPI, true>(p, a.R, stream);
+  if (readings > 1 && bytes > (int64_t(a.K % 128 ? 16 : 48) << 20) && a.K >= 128)
+    return staged_large<EPI>(p, a.R) ? kMxStagedLarge : kMxStagedSmall;
+  return a.K % 128 == 0 && stream_items<EPI>(p, a.R) >= kStreamItems ? kMxStream : kMxDirect;
+}
+
+template <int EPI>
+hipError_t run(const MxGemmLaunch &a, hipStream_t stream) {
+  const GroupedParams p = params(a);
+  switch (choose<EPI>(a, p)) {
+    case kMxNone: return hipSuccess;
+    case kMxDirect: return launch_direct<kOpMx, EPI>(p, a.R, stream);
+    case kMxStream: return launch_stream<EPI>(p, a.R, stream);
+    default: break;
   }
-  if (a.K % 128 == 0 && stream_items<EPI>(p, a.R) >= kStreamItems) return launch_stream<EPI>(p, a.R, stream);
-  return launch_direct<kOpMx, EPI>(p, a.R, stream);
+  // Scale rows are whole dwords with K % 128 == 0.
+  if (a.K % 128 == 0) return launch_staged_tiles<kOpMx, EPI>(p, a.R, stream);
+  return launch_staged_tiles<kOpMx, EPI, true>(p, a.R, stream);
 }
 
 }  // namespace
 
 hipError_t launch_mx_gemm(const MxGemmLaunch &a, hipStream_t stream) {
-  if (a.R == 0) return hipSuccess;
   switch (a.epi) {
     case kEpiF32: return run<kEpiF32>(a, stream);
     case kEpiBf16: return run<kEpiBf16>(a, stream);
     case kEpiSwiglu: return run<kEpiSwiglu>(a, stream);
     default: return run<kEpiSwigluMx>(a, stream);
+  }
+}
+
+MxKernel mx_gemm_kernel(const MxGemmLaunch &a) {
+  switch (a.epi) {
+    case kEpiF32: return choose<kEpiF32>(a, params(a));
+    case kEpiBf16: return choose<kEpiBf16>(a, params(a));
+    case kEpiSwiglu: return choose<kEpiSwiglu>(a, params(a));
+    default: return choose<kEpiSwigluMx>(a, params(a));
   }
 }
 

@@ -40,6 +40,10 @@ struct MxGemmLaunch {
 };
 hipError_t launch_mx_gemm(const MxGemmLaunch &a, hipStream_t stream);
 
+// The kernel that launch_mx_gemm takes: the values of QUADS_MX_KERNEL_*.
+enum MxKernel { kMxNone = 0, kMxDirect = 1, kMxStream = 2, kMxStagedSmall = 3, kMxStagedLarge = 4 };
+MxKernel mx_gemm_kernel(const MxGemmLaunch &a);
+
 // ---- gated.hip ---------------------------------------------------------------
 struct GatedLaunch {
   int E;

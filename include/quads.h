@@ -503,6 +503,18 @@ typedef struct {
 
 quads_status_t quads_moe_mxfp4_gemm(const quads_moe_mxfp4_args *a, void *stream);
 
+/* Which kernel quads_moe_mxfp4_gemm takes for these arguments (a negative
+ * status if it refuses them).  Host only: nothing is enqueued, the arrays are
+ * not touched.  The choice follows the sizes and types alone, so a row's sums
+ * are added in the same order in all calls of one kernel; between kernels the
+ * last bits of fp32 may differ. */
+#define QUADS_MX_KERNEL_NONE 0         /* no rows: nothing is launched */
+#define QUADS_MX_KERNEL_DIRECT 1       /* operands to registers, four waves split K */
+#define QUADS_MX_KERNEL_STREAM 2       /* each wave streams weight rows through LDS */
+#define QUADS_MX_KERNEL_STAGED_SMALL 3 /* 128 x 128 tiles staged through LDS */
+#define QUADS_MX_KERNEL_STAGED_LARGE 4 /* 256 x 256 tiles */
+int32_t quads_moe_mxfp4_gemm_kernel(const quads_moe_mxfp4_args *a);
+
 size_t quads_moe_mxfp4_ffn_workspace_bytes(int64_t act_rows, int64_t num_rows, int64_t hidden, int64_t inter);
 quads_status_t quads_moe_mxfp4_ffn(const void *x_bf16, const quads_mxfp4_t *w_gate_up, const quads_mxfp4_t *w_down,
                                    const int32_t *row_token, const int32_t *expert_offsets, int32_t num_experts,
