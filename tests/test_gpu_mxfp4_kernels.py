@@ -1,6 +1,7 @@
 """Each kernel of the grouped MXFP4 product at sizes that the library says it
 takes there (quads_moe_mxfp4_gemm_kernel, asserted for every case on the CPU):
-the streaming kernel with several items a wave.
+the streaming kernel with several items a wave, and every kernel past 32-bit
+offsets, on two streams at once and in a replayed graph.
 
 References are float64 products on the GPU of the operands' values (whose codec
 test_gpu_mxfp4.py pins).  Tolerances, with u = 2^-24: K products exact in fp32
@@ -43,6 +44,14 @@ STREAM = {
 EPILOGUES = {"f32": (Q.EPI_NONE, torch.float32), "bf16": (Q.EPI_NONE, torch.bfloat16),
              "swiglu bf16": (Q.EPI_SWIGLU, torch.bfloat16), "swiglu mxfp4": (Q.EPI_SWIGLU, Q.MXFP4)}
 
+# num_rows, experts, N, K of far operands by the kernel that takes them
+FAR_ROWS = {"direct": (40, 2, 256, 2048), "stream": (200, 8, 4096, 2048), "staged_small": (200, 2, 8192, 2048),
+            "staged_large": (700, 2, 16384, 2048)}
+FAR_ROWS_ODD = {"direct": (40, 2, 256, 2080), "staged_small": (200, 2, 8192, 2080), "staged_large": (700, 2, 16384, 2080)}
+FAR_WEIGHTS = {"stream": (40, 130, 32768, 2048), "staged_small": (5200, 130, 32768, 2048),
+               "staged_large": (5200, 18, 131072, 4096)}
+BLOCKS = {"stream": (2000, 64, 1024, 1024), "staged_small": (4000, 32, 2048, 1024), "staged_large": (6000, 16, 2048, 2048)}
+
 
 def test_cases_reach_their_kernels():
     for name, (counts, N, K) in STREAM.items():
@@ -53,6 +62,12 @@ def test_cases_reach_their_kernels():
                 assert Q.mxfp4_gemm_kernel(R, E, N, K, epilogue, dtype) == "stream", (name, epi)
         assert sum(-(-c // 32) for c in counts) * -(-N // 64) > 1024, name  # more items than waves
         assert max(counts) > 32
+    for table in (FAR_ROWS, FAR_ROWS_ODD, FAR_WEIGHTS):
+        for kernel, sizes in table.items():
+            assert Q.mxfp4_gemm_kernel(*sizes) == kernel, sizes
+    for kernel, (R, E, H, I) in BLOCKS.items():
+        assert Q.mxfp4_gemm_kernel(R, E, 2 * I, H, Q.EPI_SWIGLU, Q.MXFP4) == kernel
+        assert Q.mxfp4_gemm_kernel(R, E, H, I, Q.EPI_NONE, torch.float32) == kernel
 
 
 def test_kernel_query():
@@ -166,3 +181,109 @@ def test_stream_nan_and_rows_behind(name):
     hit[bad_rows] = True
     hit[ends[last]:, (bad_col - N // 2) // 32] = True
     assert torch.equal(q.scales[:R] == 255, hit)
+
+
+def far_rows(R, E, N, K):
+    """R rows at the end of a table whose codes pass 2^32 bytes, against 64-bit products."""
+    rows = 2 ** 32 // (K // 2) + R + 5
+    part, w = operands(R + K, R, E, N, K)
+    x = Q.empty_mxfp4(1, rows, K, "cuda")
+    x.codes.zero_()
+    x.scales.fill_(127)
+    x.codes[-R:], x.scales[-R:] = part.codes, part.scales
+    assert (rows - R) * (K // 2) >= 2 ** 32
+    # the last row first: the far end of the ids too
+    token = torch.arange(rows - 1, rows - R - 1, -1, dtype=torch.int32, device="cuda")
+    ends, offs = offsets([R // E] * (E - 1) + [R - R // E * (E - 1)])
+    want, tol = product(values(part), values(w).view(E, N, K), ends, (token - (rows - R)))
+    y = Q.moe_mxfp4_gemm(x, w, offs, token)
+    assert bool(((y.double() - want).abs() <= tol).all())
+
+
+@gpu
+@pytest.mark.parametrize("kernel", FAR_ROWS)
+def test_rows_past_32_bits(kernel):
+    far_rows(*FAR_ROWS[kernel])
+
+
+@gpu
+@pytest.mark.parametrize("kernel", FAR_ROWS_ODD)
+def test_rows_past_32_bits_odd_scales(kernel):
+    far_rows(*FAR_ROWS_ODD[kernel])
+
+
+@gpu
+@pytest.mark.parametrize("kernel", FAR_WEIGHTS)
+def test_weights_past_32_bits(kernel):
+    """Weights whose codes pass 2^32 bytes; rows for the last two experts alone."""
+    R, E, N, K = FAR_WEIGHTS[kernel]
+    x, tail = operands(R, R, 2, N, K)
+    w = Q.empty_mxfp4(E, N, K, "cuda")
+    w.codes.zero_()
+    w.scales.fill_(127)
+    w.codes[-2:], w.scales[-2:] = tail.codes, tail.scales
+    assert (E - 2) * N * (K // 2) >= 2 ** 32
+    ends, offs = offsets([0] * (E - 2) + [R // 3, R - R // 3])
+    y = Q.moe_mxfp4_gemm(x, w, offs)
+    xv, wv = values(x), values(tail).view(2, N, K)
+    for e, (a, b) in enumerate(zip(ends[-3:-1], ends[-2:])):
+        for i in range(a, b, 1024):
+            j = min(b, i + 1024)
+            want, tol = product(xv[i:j], wv[e:e + 1], [0, j - i], torch.arange(j - i, device="cuda"))
+            assert bool(((y[i:j].double() - want).abs() <= tol).all()), (e, i)
+
+
+def block(kernel):
+    R, E, H, I = BLOCKS[kernel]
+    gen = seeded(R)
+    counts = [R // E] * E
+    counts[1] += counts[0] - 1
+    counts[0] = 1
+    counts[-1] += R - sum(counts)
+    ends, offs = offsets(counts)
+    wg = Q.quantize_mxfp4(torch.randn(E, 2 * I, H, generator=gen, device="cuda") * 0.05)
+    wd = Q.quantize_mxfp4(torch.randn(E, H, I, generator=gen, device="cuda") * 0.05)
+    token = torch.randint(0, R // 2, (R,), generator=gen, device="cuda").to(torch.int32)
+    xs = [torch.randn(R // 2, H, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    return xs, wg, wd, ends, offs, token
+
+
+@gpu
+@pytest.mark.parametrize("kernel", BLOCKS)
+def test_two_streams_and_replays(kernel):
+    """Two blocks in flight on two streams, and one captured and replayed between eager calls, each with its own
+    output and workspace; one of them against 64-bit products."""
+    xs, wg, wd, ends, offs, token = block(kernel)
+    R, E, H, I = BLOCKS[kernel]
+    want = [Q.moe_mxfp4_ffn(x, wg, wd, offs, token) for x in xs]
+    xq = Q.quantize_mxfp4(xs[0])
+    gu, tol = product(values(xq), values(wg).view(E, 2 * I, H), ends, token)
+    pre = Q.moe_mxfp4_gemm(xq, wg, offs, token)
+    assert bool(((pre.double() - gu).abs() <= tol).all())
+    g, u = pre.double().chunk(2, 1)
+    hv = g * torch.sigmoid(g) * u
+    h = Q.moe_mxfp4_gemm(xq, wg, offs, token, epilogue=Q.EPI_SWIGLU, y_dtype=Q.MXFP4)
+    check_block(h, hv, (7 + 1.23 * g.abs()) * U * hv.abs() + 2.0 ** -125)
+    y, tol = product(values(h), values(wd).view(E, H, I), ends, torch.arange(R, device="cuda"))
+    assert bool(((want[0].double() - y).abs() <= tol).all())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(4):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k] = Q.moe_mxfp4_ffn(xs[k], wg, wd, offs, token)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    x, out = xs[0].clone(), torch.empty_like(want[0])
+    ws = torch.empty(Q.mxfp4_ffn_workspace_bytes(R // 2, R, H, I), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Q.moe_mxfp4_ffn(x, wg, wd, offs, token, y=out, ws=ws)
+    for k in (0, 1, 1, 0):
+        x.copy_(xs[k])
+        out.zero_()
+        graph.replay()
+        assert torch.equal(Q.moe_mxfp4_ffn(xs[1 - k], wg, wd, offs, token), want[1 - k])
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[k])
