@@ -76,7 +76,10 @@ def grouped(x, w, offsets, row_token=None, magnitude=False):
 
 
 def sigmoid(z):
-    return 0.5 * (1 + np.tanh(0.5 * np.asarray(z, np.float64)))
+    """1 / (1 + e^-z), as e^z / (1 + e^z) below 0: no cancellation, no overflow."""
+    z = np.asarray(z, np.float64)
+    e = np.exp(-np.abs(z))
+    return np.where(z < 0, e, 1.0) / (1 + e)
 
 
 def silu(z):
