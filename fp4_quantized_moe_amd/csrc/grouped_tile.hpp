@@ -174,6 +174,10 @@ __device__ __forceinline__ void store_mx_block(const float (&h)[16], int lane, b
   }
 }
 
+// 1 / (1 + e^-z) as in silu: off by (5 + 1.23 |z|) 2^-24 of it, of which 1.23 |z|
+// is the argument of exp2 (its product and constant), and 0 below z = -87.3,
+// where the reciprocal is subnormal.  The outputs are rounded to bf16 (2^-8) or
+// MXFP4 next.
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * 1.44269504088896341f));
 }
