@@ -551,13 +551,15 @@ quads_status_t quads_weight_qdq_mxfp4(const void *w_bf16, int64_t batch, int64_t
   return device_status(quads::launch_mx_quantize(a, static_cast<hipStream_t>(stream)), "weight_qdq_mxfp4");
 }
 
-// Grouping and size checks shared by the MXFP4 and gated products.
+// Grouping and size checks shared by the MXFP4 and gated products.  `width`:
+// what the limit of 2^24 on N holds for, N itself or its half, one matrix of a
+// gate/up pair.
 static quads_status_t grouped_shape(const char *what, int32_t E, int64_t R, int64_t A, const int32_t *row_token,
-                                    int64_t N, int64_t K) {
+                                    int64_t N, int64_t K, int64_t width) {
   if (E < 1 || E > 1024) return fail(QUADS_ERR_SHAPE, "%s: num_experts outside [1,1024]", what);
   if (R < 0 || A < 0 || R > (int64_t(1) << 31) - 1024 || A > (int64_t(1) << 31) - 1)
     return fail(QUADS_ERR_SHAPE, "%s: row counts out of range", what);
-  if (N >= (int64_t(1) << 24) || K >= (int64_t(1) << 24) || !mul_ok(R, N, kMaxElems) || !mul_ok(E * N, K, kMaxElems))
+  if (width >= (int64_t(1) << 24) || K >= (int64_t(1) << 24) || !mul_ok(R, N, kMaxElems) || !mul_ok(E * N, K, kMaxElems))
     return fail(QUADS_ERR_SHAPE, "%s: size overflow", what);
   if (row_token == nullptr && A < R) return fail(QUADS_ERR_SHAPE, "%s: identity rows need act_rows >= num_rows", what);
   if (R > 0 && A == 0) return fail(QUADS_ERR_SHAPE, "%s: routed rows of no activation rows", what);
@@ -579,7 +581,7 @@ static quads_status_t mx_gemm_fill(const quads_moe_mxfp4_args *a, quads::MxGemmL
   if (a->K <= 0 || a->K % 32) return fail(QUADS_ERR_SHAPE, "mxfp4_gemm: K must be a positive multiple of 32");
   if (a->N <= 0 || a->N % (swiglu ? 64 : 32))
     return fail(QUADS_ERR_SHAPE, "mxfp4_gemm: N must be a positive multiple of %d", swiglu ? 64 : 32);
-  const quads_status_t st = grouped_shape("mxfp4_gemm", a->num_experts, a->num_rows, a->act_rows, a->row_token, a->N, a->K);
+  const quads_status_t st = grouped_shape("mxfp4_gemm", a->num_experts, a->num_rows, a->act_rows, a->row_token, a->N, a->K, a->N);
   if (st != QUADS_OK) return st;
   if (!a->expert_offsets || !a->w_codes || !a->w_scales) return fail(QUADS_ERR_ARG, "mxfp4_gemm: null pointer");
   if (misaligned({a->x_codes, a->x_scales, a->w_codes, a->w_scales, a->y, a->y_scales}))
@@ -633,8 +635,9 @@ quads_status_t quads_moe_mxfp4_ffn(const void *x_bf16, const quads_mxfp4_t *w_ga
   if (y_dtype != QUADS_F32 && y_dtype != QUADS_BF16) return fail(QUADS_ERR_ARG, "mxfp4_ffn: bad y_dtype %d", y_dtype);
   if (hidden <= 0 || hidden % 32 || inter <= 0 || inter % 32)
     return fail(QUADS_ERR_SHAPE, "mxfp4_ffn: hidden and inter must be positive multiples of 32");
-  quads_status_t st = grouped_shape("mxfp4_ffn", num_experts, num_rows, act_rows, row_token, 2 * inter, hidden);
-  if (st == QUADS_OK) st = grouped_shape("mxfp4_ffn", num_experts, num_rows, num_rows, row_token, hidden, inter);
+  quads_status_t st = grouped_shape("mxfp4_ffn", num_experts, num_rows, act_rows, row_token, 2 * inter, hidden, 2 * inter);
+  if (st == QUADS_OK)
+    st = grouped_shape("mxfp4_ffn", num_experts, num_rows, num_rows, row_token, hidden, inter, hidden);
   if (st == QUADS_OK && !mul_ok(act_rows, hidden, kMaxElems)) st = fail(QUADS_ERR_SHAPE, "mxfp4_ffn: size overflow");
   if (st != QUADS_OK) return st;
   if (!w_gate_up || !w_down || !w_gate_up->codes || !w_gate_up->scales || !w_down->codes || !w_down->scales ||
@@ -702,7 +705,8 @@ quads_status_t quads_moe_gated_forward_bf16(const void *x_bf16, const void *w_ga
                                             int64_t act_rows, int64_t hidden, int64_t inter, void *h_bf16,
                                             void *gu_bf16, void *stream) {
   quads_status_t st = gated_shape("gated_forward", hidden, inter);
-  if (st == QUADS_OK) st = grouped_shape("gated_forward", num_experts, num_rows, act_rows, row_token, 2 * inter, hidden);
+  if (st == QUADS_OK)
+    st = grouped_shape("gated_forward", num_experts, num_rows, act_rows, row_token, 2 * inter, hidden, inter);
   if (st != QUADS_OK) return st;
   if (!expert_offsets || !w_gate_up_bf16) return fail(QUADS_ERR_ARG, "gated_forward: null pointer");
   if (misaligned({x_bf16, w_gate_up_bf16, h_bf16, gu_bf16}))
@@ -727,7 +731,8 @@ quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_
                                              const int32_t *expert_offsets, int32_t num_experts, int64_t num_rows,
                                              int64_t hidden, int64_t inter, void *dgu_bf16, void *stream) {
   quads_status_t st = gated_shape("gated_backward", hidden, inter);
-  if (st == QUADS_OK) st = grouped_shape("gated_backward", num_experts, num_rows, num_rows, nullptr, 2 * inter, hidden);
+  if (st == QUADS_OK)
+    st = grouped_shape("gated_backward", num_experts, num_rows, num_rows, nullptr, 2 * inter, hidden, inter);
   if (st != QUADS_OK) return st;
   if (!expert_offsets || !w_down_bf16) return fail(QUADS_ERR_ARG, "gated_backward: null pointer");
   if (misaligned({dy_bf16, w_down_bf16, gu_bf16, dgu_bf16}))

@@ -478,7 +478,8 @@ quads_status_t quads_weight_qdq_mxfp4(const void *w_bf16, int64_t batch, int64_t
  * and requantization over w_gate_up [E, 2 inter, hidden], then the down
  * product over w_down [E, hidden, inter] into y [num_rows, hidden] (F32 or
  * BF16), one routed row each (quads_moe_combine sums F32 rows to tokens).
- * The same bits as the three calls.  hidden % 32 == 0, inter % 32 == 0.
+ * The same bits as the three calls.  hidden % 32 == 0, inter % 32 == 0; hidden
+ * and 2 inter are N and K of those calls, below 2^24.
  * ws: quads_moe_mxfp4_ffn_workspace_bytes(act_rows, num_rows, hidden, inter)
  * bytes (both quantized activations); calls in flight at the same time need
  * a workspace each.
