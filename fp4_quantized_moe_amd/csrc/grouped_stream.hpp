@@ -12,13 +12,19 @@
 // fragments are in registers, also across items: no barriers, and about
 // 100 KB of weights in flight on every CU.
 //
-// ONCE: the weights are read past the caches, for calls that read them once.
-// With those of several layers in turn, as in a model, the MXFP4 block of 256
-// tokens took 94 instead of 101 us (4.65 TB/s; its projections 59.6 and 36.4
-// instead of 63.4 and 38.2); a lone layer that finds a part of its weights in
-// the last-level cache loses by it (285 MB: 51 -> 54 us).  With two row tiles
-// an expert the second would find them there: 12.6 -> 13.9 us.
+// An expert with one row tile has its weights read past the caches, since nobody
+// comes back to them; with more tiles the later ones find them there.  With the
+// weights of four layers in turn, as in a model, 128 experts of 2048 -> 2 x 1024
+// and back, the two products took (past the caches for experts of one tile / for
+// all experts / for none): 256 tokens x 8 evenly routed 89.5 / 89.2 / 97.4 us,
+// by Zipf(1.1) 107.4 / 112.4 / 109.9; 512 tokens evenly 130.5 / 143.1 / 131.3,
+// by Zipf 133.5 / 158.4 / 134.3.  A lone layer, warm: 89.2 / 89.3 / 96.4,
+// 106.3 / 112.5 / 107.8, 124.7 / 143.2 / 127.7 and 129.0 / 158.1 / 131.4.
+// Where the last-level cache would hold all of a lone layer's used experts, they
+// lose a little (51 of them: 43.7 / 42.8 / 41.6).
 #pragma once
+
+#include <type_traits>
 
 #include "grouped_dma.hpp"
 #include "grouped_tile.hpp"
@@ -30,7 +36,7 @@ constexpr int kStreamRows = 96;                          // 64 weight rows, 32 r
 constexpr int kStreamStage = kStreamRows * (128 + 8);    // bytes: chunks, then scales
 constexpr int kStreamLoads = kStreamRows / 8 + kStreamRows / 32;  // DMA instructions of a stage
 
-template <int EPI, bool ONCE>
+template <int EPI>
 __global__ __launch_bounds__(64 * kStreamWaves, 1) void k_grouped_stream(GroupedParams p, int col_groups) {
   constexpr bool PAIR = EPI == kEpiSwiglu || EPI == kEpiSwigluMx;
   constexpr int COLS = PAIR ? 32 : 64;
@@ -82,24 +88,28 @@ __global__ __launch_bounds__(64 * kStreamWaves, 1) void k_grouped_stream(Grouped
     second = other * p.w_row;
     second_scale = static_cast<int64_t>(other) * p.chunks;
   };
-  const auto bring = [](const uint8_t *src, uint8_t *to) {
-    if constexpr (ONCE)
-      dma_wave_once(src, to);
-    else
-      dma_wave(src, to, 16);
-  };
   const auto fetch = [&](int s, uint8_t *base) {
     const int64_t off = 128 * static_cast<int64_t>(s);
     const bool in0 = 8 * s + chunk0 < p.chunks, in1 = 8 * s + (chunk0 ^ 4) < p.chunks;
     const bool sin = 8 * s + 4 * (lane & 1) < p.chunks;
+    const auto weights = [&](auto once) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint8_t *src = wsrc + (j >= 4 ? second : 0) + 8 * (j & 3) * p.w_row + off;
-      if (j & 1)  // the swizzle of rows 16 k + 8 ..
-        bring(in1 ? src + ((chunk0 ^ 4) - chunk0) * 16 : zero, base + 1024 * j);
-      else
-        bring(in0 ? src : zero, base + 1024 * j);
-    }
+      for (int j = 0; j < 8; ++j) {
+        const uint8_t *src = wsrc + (j >= 4 ? second : 0) + 8 * (j & 3) * p.w_row + off;
+        if (j & 1)  // the swizzle of rows 16 k + 8 ..
+          src = in1 ? src + ((chunk0 ^ 4) - chunk0) * 16 : zero;
+        else
+          src = in0 ? src : zero;
+        if constexpr (decltype(once)::value)
+          dma_wave_once(src, base + 1024 * j);
+        else
+          dma_wave(src, base + 1024 * j, 16);
+      }
+    };
+    if (walk.last - walk.first <= 32)  // the expert's only row tile
+      weights(std::true_type{});
+    else
+      weights(std::false_type{});
 #pragma unroll
     for (int j = 0; j < 4; ++j) dma_wave((j & 1 ? in1 : in0) ? xsrc[j] + off : zero, base + 1024 * (8 + j), 16);
     uint8_t *sc = base + kStreamRows * 128;
@@ -198,10 +208,7 @@ hipError_t launch_stream(const GroupedParams &p, int64_t R, hipStream_t stream) 
   constexpr int COLS = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? 32 : 64;
   const int groups = (p.width + COLS - 1) / COLS;
   const dim3 grid(256), threads(64 * kStreamWaves);
-  if (R <= 32 * static_cast<int64_t>(p.E))
-    hipLaunchKernelGGL((k_grouped_stream<EPI, true>), grid, threads, 0, stream, p, groups);
-  else
-    hipLaunchKernelGGL((k_grouped_stream<EPI, false>), grid, threads, 0, stream, p, groups);
+  hipLaunchKernelGGL((k_grouped_stream<EPI>), grid, threads, 0, stream, p, groups);
   return hipGetLastError();
 }
 

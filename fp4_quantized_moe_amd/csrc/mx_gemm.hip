@@ -38,6 +38,8 @@ MxKernel choose(const MxGemmLaunch &a, const GroupedParams &p) {
   // 17 MB twice 12.4 and 15.2 us, 34 MB twice 12.9 and 13.2, 17 MB four times
   // 16.5 and 12.8, 268 MB twice 95 and 65.  Rows that do not begin on a line
   // (K % 128 != 0) stream worse: 8 MB five times 21 and 13.
+  // The readings are an average: the host does not know the experts' rows, and
+  // a skewed routing reads a loud expert's weights more often.
   const int64_t readings = (a.R + 32 * static_cast<int64_t>(a.E) - 1) / (32 * static_cast<int64_t>(a.E));
   const int64_t bytes = static_cast<int64_t>(a.E) * a.N * (a.K / 2) * readings;
   if (readings > 1 && bytes > (int64_t(a.K % 128 ? 16 : 48) << 20) && a.K >= 128)
