@@ -897,7 +897,9 @@ def mxfp4_ffn_workspace_bytes(act_rows: int, num_rows: int, hidden: int, inter: 
 def moe_gated_forward(x: torch.Tensor, w_gate_up: torch.Tensor, expert_offsets: torch.Tensor,
                       row_token: torch.Tensor | None = None, keep: bool = True):
     """quads_moe_gated_forward_bf16: x bf16 [act_rows, H], w_gate_up bf16
-    [E, 2 I, H] -> (h bf16 [R, I], gate | up bf16 [R, 2 I], or None with keep=False)."""
+    [E, 2 I, H] -> (h bf16 [R, I], gate | up bf16 [R, 2 I], or None with keep=False:
+    the same h, for a trainer that computes gate | up again; inference takes
+    moe_w4a4_gemm with bf16 operands and EPI_SWIGLU)."""
     what = "moe_gated_forward"
     _require(what, x, "x", torch.bfloat16)
     _require(what, w_gate_up, "w_gate_up", torch.bfloat16, x)

@@ -332,7 +332,7 @@ __device__ __forceinline__ void staged_tiles(const GroupedParams &p, uint8_t *ld
 
   // Rows of a tile that a wave takes: with at most half of the large tile's
   // rows (an expert's last ones) the waves halve those, and do half the
-  // products (512 rows an expert on average: 677 -> 647 us for the gated
+  // products (512 rows an expert on average: 689 -> 660 us for the gated
   // forward).  There only: in the others the second form of the loops makes
   // the compiler spill (the backward 478 -> 531 us, MXFP4 547 -> 555).
   constexpr bool HALVES = PAIR && C::MI >= 4 && !C::MX;
@@ -680,10 +680,10 @@ hipError_t launch_staged(const GroupedParams &p, int64_t R, hipStream_t stream) 
 // run two a CU, one's stores under the other's products, in rounds of 512
 // that take 0.5 to 0.6 of a large one's with short contractions and in the
 // backward, 0.6 to 0.75 from 16 stages on.  An expert adds half a row tile.
-// Large against small, with the rounds: 4096 x 1536 x 2048 21.7 and 16 us (1,
-// 1); 32768 x 800 x 992 in 16 groups 47 and 37 (3, 4); 131072 x 1536 x 2048 in
-// 64 groups 310 and 362 (13, 25); backward of 32032 x 1408 x 1152 in 16 groups
-// 237 and 205 (4, 6), of 65536 x 1456 x 2048 in 32 637 and 691 (7, 13).
+// Large against small, with the rounds: 4096 x 1536 x 2048 22.0 and 16.1 us (1,
+// 1); 32768 x 800 x 992 in 16 groups 48 and 36 (3, 4); 131072 x 1536 x 2048 in
+// 64 groups 265 and 306 (13, 25); backward of 32032 x 1408 x 1152 in 16 groups
+// 234 and 187 (4, 6), of 65536 x 1456 x 2048 in 32 632 and 684 (7, 13).
 template <int EPI>
 bool staged_large(const GroupedParams &p, int64_t R) {
   constexpr int PAIRED = EPI == kEpiSwiglu || EPI == kEpiSwigluMx ? 2 : 1;

@@ -530,7 +530,10 @@ quads_status_t quads_moe_mxfp4_ffn(const void *x_bf16, const quads_mxfp4_t *w_ga
  * quads_moe_gated_forward_bf16: for routed row i of expert e
  *   [g | u] = W_gate_up[e] x[t(i)]  (fp32 accumulation),  h = silu(g) u,
  * h [num_rows, inter] bf16 rounded once from fp32; gu [num_rows, 2 inter]
- * bf16 receives g and u for the backward (NULL: not kept).
+ * bf16 receives g and u for the backward (NULL: not kept; h has the same bits.
+ * That is quads_moe_w4a4_gemm's QUADS_OPERANDS_BF16 with QUADS_EPI_SWIGLU up to
+ * the order of the sums; for inference take that call, for a trainer that
+ * computes g and u again this one).
  *
  * quads_moe_gated_backward_bf16: from dy [num_rows, hidden] bf16, the gradient
  * of y[i] = W_down[e] h[i] (W_down [E, hidden, inter]),
