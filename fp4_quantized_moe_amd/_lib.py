@@ -845,9 +845,11 @@ _MX_KERNELS = ("none", "direct", "stream", "staged_small", "staged_large")
 def mxfp4_gemm_kernel(num_rows: int, num_experts: int, N: int, K: int, epilogue: int = EPI_NONE,
                       y_dtype=torch.float32) -> str:
     """quads_moe_mxfp4_gemm_kernel: which kernel moe_mxfp4_gemm takes for these sizes."""
-    code = MXFP4 if y_dtype == MXFP4 else BF16 if y_dtype == torch.bfloat16 else F32
+    codes = {torch.float32: F32, torch.bfloat16: BF16, MXFP4: MXFP4}
+    if y_dtype not in codes:
+        raise QuadsError(f"mxfp4_gemm_kernel: y_dtype must be float32, bfloat16 or MXFP4, not {y_dtype}")
     any_array = 16  # an aligned address that is not touched
-    a = _MxGemmArgs(_MX_GEMM_SIZE, 0, epilogue, code, num_experts, 0, num_rows, num_rows, N, K, *[any_array] * 8)
+    a = _MxGemmArgs(_MX_GEMM_SIZE, 0, epilogue, codes[y_dtype], num_experts, 0, num_rows, num_rows, N, K, *[any_array] * 8)
     kernel = load().quads_moe_mxfp4_gemm_kernel(ctypes.byref(a))
     if kernel < 0:
         _check(kernel, "mxfp4_gemm_kernel")

@@ -76,6 +76,9 @@ def test_kernel_query():
         Q.mxfp4_gemm_kernel(4, 4, 64, 48)
     with pytest.raises(Q.QuadsError, match="y_dtype"):
         Q.mxfp4_gemm_kernel(4, 4, 64, 64, Q.EPI_SWIGLU, torch.float32)
+    with pytest.raises(Q.QuadsError, match="y_dtype"):
+        Q.mxfp4_gemm_kernel(4, 4, 64, 64, y_dtype=torch.float16)
+    assert Q.load().quads_moe_mxfp4_gemm_kernel(None) == -1
 
 
 def offsets(counts):
