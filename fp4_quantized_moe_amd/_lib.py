@@ -10,20 +10,21 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libquads.so")
 
-F32, BF16, MXFP4 = 0, 1, 2
+F32, BF16, MXFP4, MXFP8 = 0, 1, 2, 3
 GSCALE_GIVEN, WANT_SCORES = 1, 2
 OPERANDS_W4A4, OPERANDS_BF16, OPERANDS_BF16_QDQ, OPERANDS_BF16_W4 = 0, 1, 2, 3
 SCALES_ONLY, MX_SCALE_EVEN = 4, 8
 EPI_NONE, EPI_SWIGLU = 0, 1
 RAC_FORM_AUTO, RAC_FORM_EXACT, RAC_FORM_MERGED = 0, 1, 2
 
-_c_i64, _c_i32, _c_u32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_void_p
+_c_i64, _c_i32, _c_u32, _c_f32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_float, ctypes.c_void_p
 
 
 class QuadsError(RuntimeError):
@@ -50,6 +51,18 @@ class _MxGemmArgs(ctypes.Structure):
 
 
 _MX_GEMM_SIZE = ctypes.sizeof(_MxGemmArgs)
+
+
+class _RmsNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", _c_u32), ("flags", _c_u32), ("x_dtype", _c_i32), ("residual_dtype", _c_i32),
+        ("weight_dtype", _c_i32), ("q_format", _c_i32), ("rows", _c_i64), ("cols", _c_i64),
+        ("x", _vp), ("residual", _vp), ("weight", _vp), ("sum", _vp), ("y_bf16", _vp), ("q_codes", _vp),
+        ("q_scales", _vp), ("rstd", _vp), ("eps", _c_f32), ("reserved", _c_i32),
+    ]
+
+
+_RMS_NORM_SIZE = ctypes.sizeof(_RmsNormArgs)
 
 
 class _GemmArgs(ctypes.Structure):
@@ -79,6 +92,9 @@ EXPORTS = [
     "quads_moe_mxfp4_gemm", "quads_moe_mxfp4_gemm_kernel",
     "quads_moe_mxfp4_ffn_workspace_bytes", "quads_moe_mxfp4_ffn",
     "quads_moe_gated_forward_bf16", "quads_moe_gated_backward_bf16",
+    "quads_rms_norm", "quads_rms_norm_backward_workspace_bytes", "quads_rms_norm_backward", "quads_dequantize_mxfp8",
+    "quads_moe_balance_loss_workspace_bytes", "quads_moe_balance_loss", "quads_moe_route_backward",
+    "quads_moe_combine_backward",
 ]
 
 _lib = None
@@ -155,6 +171,25 @@ def load(path: str = LIB_PATH):
     L.quads_moe_gated_forward_bf16.argtypes = [_vp, _vp, _vp, _vp, _c_i32, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp]
     L.quads_moe_gated_backward_bf16.restype = ctypes.c_int
     L.quads_moe_gated_backward_bf16.argtypes = [_vp, _vp, _vp, _vp, _c_i32, _c_i64, _c_i64, _c_i64, _vp, _vp]
+    L.quads_rms_norm.restype = ctypes.c_int
+    L.quads_rms_norm.argtypes = [ctypes.POINTER(_RmsNormArgs), _vp]
+    L.quads_rms_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.quads_rms_norm_backward_workspace_bytes.argtypes = [_c_i64, _c_i64]
+    L.quads_rms_norm_backward.restype = ctypes.c_int
+    L.quads_rms_norm_backward.argtypes = [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _c_i64,
+                                          _c_i64, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    L.quads_dequantize_mxfp8.restype = ctypes.c_int
+    L.quads_dequantize_mxfp8.argtypes = [_MXFP4, _vp, ctypes.c_int, _vp]
+    L.quads_moe_balance_loss_workspace_bytes.restype = ctypes.c_size_t
+    L.quads_moe_balance_loss_workspace_bytes.argtypes = [_c_i64, _c_i32]
+    L.quads_moe_balance_loss.restype = ctypes.c_int
+    L.quads_moe_balance_loss.argtypes = [_vp, _vp, _vp, _c_i64, _c_i32, _c_i32, _c_f32, _vp, _vp, _vp, _vp,
+                                         ctypes.c_size_t, _vp]
+    L.quads_moe_route_backward.restype = ctypes.c_int
+    L.quads_moe_route_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i32, _c_i32, _vp, _vp]
+    L.quads_moe_combine_backward.restype = ctypes.c_int
+    L.quads_moe_combine_backward.argtypes = [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _c_i64, _c_i32, _c_i64, _vp,
+                                             _vp, _vp]
     _lib = L
     return L
 
@@ -939,3 +974,229 @@ def moe_gated_backward(dy: torch.Tensor, w_down: torch.Tensor, gu: torch.Tensor,
     _on_device(dy, load().quads_moe_gated_backward_bf16, what, dy.data_ptr(), w_down.data_ptr(), gu.data_ptr(),
                expert_offsets.data_ptr(), E, R, H, I, dgu.data_ptr())
     return dgu
+
+
+# ---- around the experts: the norm, the router's and the combine's gradients -------
+#
+# Streams and devices as in the section above.
+
+@dataclass
+class MXFP8Tensor:
+    """E4M3 codes [batch, rows, cols] u8 and E8M0 scales [batch, rows, cols/32] u8
+    (batch axis omitted when batch == 1)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    batch: int
+    rows: int
+    cols: int
+
+    def c_struct(self):
+        return _MXFP4(self.codes.data_ptr(), self.scales.data_ptr(), self.batch, self.rows, self.cols)
+
+
+def mxfp8_tensor(codes: torch.Tensor, scales: torch.Tensor) -> MXFP8Tensor:
+    """An MXFP8Tensor over existing codes [.., rows, cols] and scales [.., rows, cols/32]."""
+    what = "mxfp8_tensor"
+    _require(what, codes, "codes", torch.uint8)
+    _require(what, scales, "scales", torch.uint8, codes)
+    batch, rows, cols = _batch_rows_cols(what, codes.shape)
+    if cols % 32 or codes.shape[:-1] != scales.shape[:-1] or scales.shape[-1] * 32 != cols:
+        raise QuadsError(f"{what}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not match")
+    return MXFP8Tensor(codes, scales, batch, rows, cols)
+
+
+def dequantize_mxfp8(q: MXFP8Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """quads_dequantize_mxfp8: the bf16 or fp32 values q stands for."""
+    what = "dequantize_mxfp8"
+    _require(what, q.codes, "q.codes", torch.uint8)
+    _require(what, q.scales, "q.scales", torch.uint8, q.codes)
+    n = q.batch * q.rows * q.cols
+    if q.codes.numel() != n or q.scales.numel() * 32 != n:
+        raise QuadsError(f"{what}: q's arrays do not hold [{q.batch}, {q.rows}, {q.cols}]")
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise QuadsError(f"{what}: dtype must be bfloat16 or float32, not {dtype}")
+    if out is None:
+        out = torch.empty(q.codes.shape, dtype=dtype, device=q.codes.device)
+    else:
+        _require(what, out, "out", dtype, q.codes)
+        if out.shape != q.codes.shape:
+            raise QuadsError(f"{what}: out must be {tuple(q.codes.shape)}")
+    _on_device(out, load().quads_dequantize_mxfp8, what, q.c_struct(), out.data_ptr(), _dtype_code(out))
+    return out
+
+
+def _require_float(what: str, t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
+    """Checks a bf16 or fp32 tensor; -> its dtype code."""
+    if t.dtype == torch.float32:
+        _require(what, t, name, torch.float32, like)
+        return F32
+    _require(what, t, name, torch.bfloat16, like)
+    return BF16
+
+
+class RmsNorm(NamedTuple):
+    y: torch.Tensor | None              # bf16 [rows, cols]
+    q: MXFP4Tensor | MXFP8Tensor | None
+    sum: torch.Tensor                   # the stream that was normalised (x itself without a residual)
+    rstd: torch.Tensor | None           # float32 [rows]
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+             quantize: int | None = None, bf16: bool | None = None, rule: str = "floor", keep: bool = False,
+             out_sum: torch.Tensor | None = None) -> RmsNorm:
+    """quads_rms_norm: x [rows, cols] and residual, weight [cols], each bf16 or
+    fp32.  quantize: MXFP4 or MXFP8 for a quantized output; bf16: whether y is
+    written in bf16 (default: if nothing else is); keep: rstd for
+    rms_norm_backward; out_sum may be residual, to add in place."""
+    what = "rms_norm"
+    x_code = _require_float(what, x, "x")
+    w_code = _require_float(what, weight, "weight", x)
+    if x.dim() != 2 or tuple(weight.shape) != (x.shape[1],):
+        raise QuadsError(f"{what}: x {tuple(x.shape)} needs weight [cols], not {tuple(weight.shape)}")
+    rows, cols = x.shape
+    r_code = F32
+    if residual is not None:
+        r_code = _require_float(what, residual, "residual", x)
+        if residual.shape != x.shape:
+            raise QuadsError(f"{what}: residual must have x's shape")
+        if out_sum is None:
+            out_sum = torch.empty_like(residual)
+        else:
+            _require(what, out_sum, "out_sum", residual.dtype, x)
+            if out_sum.shape != x.shape:
+                raise QuadsError(f"{what}: out_sum must have x's shape")
+    elif out_sum is not None:
+        raise QuadsError(f"{what}: out_sum without a residual")
+    if quantize not in (None, MXFP4, MXFP8):
+        raise QuadsError(f"{what}: quantize must be None, MXFP4 or MXFP8, not {quantize}")
+    flags = _rule_flags(rule)
+    if flags and quantize != MXFP4:
+        raise QuadsError(f"{what}: rule {rule!r} is for MXFP4")
+    if quantize is not None and cols % 32:
+        raise QuadsError(f"{what}: a quantized output needs cols ({cols}) to be a multiple of 32")
+    q = None
+    if quantize == MXFP4:
+        q = empty_mxfp4(1, rows, cols, x.device)
+    elif quantize == MXFP8:
+        q = MXFP8Tensor(torch.empty(rows, cols, dtype=torch.uint8, device=x.device),
+                        torch.empty(rows, cols // 32, dtype=torch.uint8, device=x.device), 1, rows, cols)
+    if bf16 is None:
+        bf16 = q is None
+    y = torch.empty(rows, cols, dtype=torch.bfloat16, device=x.device) if bf16 else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if keep else None
+    a = _RmsNormArgs(_RMS_NORM_SIZE, flags, x_code, r_code, w_code, -1 if quantize is None else quantize, rows, cols,
+                     x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(),
+                     None if residual is None else out_sum.data_ptr(), None if y is None else y.data_ptr(),
+                     None if q is None else q.codes.data_ptr(), None if q is None else q.scales.data_ptr(),
+                     None if rstd is None else rstd.data_ptr(), eps, 0)
+    _on_device(x, load().quads_rms_norm, what, ctypes.byref(a))
+    return RmsNorm(y, q, x if residual is None else out_sum, rstd)
+
+
+def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                      dsum: torch.Tensor | None = None, want_dweight: bool = True):
+    """quads_rms_norm_backward: dy bf16/fp32 [rows, cols], s and rstd as rms_norm
+    gave them (sum, rstd), dsum the gradient that reaches s past the norm -> (dx
+    of s's type: the gradient of x and of the residual; dweight fp32 [cols] or None)."""
+    what = "rms_norm_backward"
+    dy_code = _require_float(what, dy, "dy")
+    s_code = _require_float(what, s, "s", dy)
+    w_code = _require_float(what, weight, "weight", dy)
+    _require(what, rstd, "rstd", torch.float32, dy)
+    if dy.dim() != 2 or s.shape != dy.shape or tuple(weight.shape) != (dy.shape[1],) or tuple(rstd.shape) != (dy.shape[0],):
+        raise QuadsError(f"{what}: dy {tuple(dy.shape)}, s {tuple(s.shape)}, weight {tuple(weight.shape)} and rstd "
+                         f"{tuple(rstd.shape)} do not match")
+    if dsum is not None:
+        _require(what, dsum, "dsum", s.dtype, dy)
+        if dsum.shape != dy.shape:
+            raise QuadsError(f"{what}: dsum must have s's shape")
+    rows, cols = dy.shape
+    L = load()
+    dx = torch.empty_like(s)
+    dweight = ws = None
+    if want_dweight:
+        dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
+        ws = _workspace(L.quads_rms_norm_backward_workspace_bytes(rows, cols), dy.device)
+    _on_device(dy, L.quads_rms_norm_backward, what, dy.data_ptr(), dy_code, s.data_ptr(), s_code, weight.data_ptr(), w_code,
+               rstd.data_ptr(), None if dsum is None else dsum.data_ptr(), rows, cols, dx.data_ptr(),
+               None if dweight is None else dweight.data_ptr(), None if ws is None else ws.data_ptr(),
+               0 if ws is None else ws.numel())
+    return dx, dweight
+
+
+def _require_routing(what: str, logits: torch.Tensor, ids: torch.Tensor, mask: torch.Tensor | None):
+    _require(what, logits, "logits", torch.float32)
+    _require(what, ids, "ids", torch.int32, logits)
+    if logits.dim() != 2 or ids.dim() != 2 or ids.shape[0] != logits.shape[0]:
+        raise QuadsError(f"{what}: logits {tuple(logits.shape)} and ids {tuple(ids.shape)} must be [T, E] and [T, top]")
+    if mask is not None:
+        _require(what, mask, "mask", torch.bool if mask.dtype == torch.bool else torch.uint8, logits)
+        if tuple(mask.shape) != (logits.shape[0],):
+            raise QuadsError(f"{what}: mask must be [T]")
+
+
+class BalanceLoss(NamedTuple):
+    loss: torch.Tensor    # float32 [1]
+    counts: torch.Tensor  # int32 [E]
+    slope: torch.Tensor   # float32 [E]: d loss / d probability, for moe_route_backward
+
+
+def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float, mask: torch.Tensor | None = None) -> BalanceLoss:
+    """quads_moe_balance_loss: logits float32 [T, E], ids int32 [T, top] (moe_route's),
+    mask bool/uint8 [T], 0 for padding."""
+    what = "moe_balance_loss"
+    _require_routing(what, logits, ids, mask)
+    (T, E), top, dev = logits.shape, ids.shape[1], logits.device
+    L = load()
+    out = BalanceLoss(torch.empty(1, dtype=torch.float32, device=dev), torch.empty(E, dtype=torch.int32, device=dev),
+                      torch.empty(E, dtype=torch.float32, device=dev))
+    ws = _workspace(L.quads_moe_balance_loss_workspace_bytes(T, E), dev)
+    _on_device(logits, L.quads_moe_balance_loss, what, logits.data_ptr(), ids.data_ptr(),
+               None if mask is None else mask.data_ptr(), T, E, top, coef, out.loss.data_ptr(), out.counts.data_ptr(),
+               out.slope.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dw: torch.Tensor | None = None,
+                       slope: torch.Tensor | None = None, dloss: torch.Tensor | None = None,
+                       mask: torch.Tensor | None = None) -> torch.Tensor:
+    """quads_moe_route_backward: gradient of logits [T, E] from that of the combine
+    weights (dw float32 [T, top]) and of the balance loss (slope of
+    moe_balance_loss, times dloss float32 [1])."""
+    what = "moe_route_backward"
+    _require_routing(what, logits, ids, mask)
+    (T, E), top = logits.shape, ids.shape[1]
+    for t, name, shape in ((dw, "dw", (T, top)), (slope, "slope", (E,)), (dloss, "dloss", (1,))):
+        if t is not None:
+            _require(what, t, name, torch.float32, logits)
+            if tuple(t.shape) != shape:
+                raise QuadsError(f"{what}: {name} must be {list(shape)}, not {list(t.shape)}")
+    if dloss is not None and slope is None:
+        raise QuadsError(f"{what}: dloss without slope")
+    dlogits = torch.empty_like(logits)
+    _on_device(logits, load().quads_moe_route_backward, what, logits.data_ptr(), ids.data_ptr(),
+               *(None if t is None else t.data_ptr() for t in (mask, dw, slope, dloss)), T, E, top, dlogits.data_ptr())
+    return dlogits
+
+
+def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, inverse: torch.Tensor, topk_w: torch.Tensor):
+    """quads_moe_combine_backward: dout bf16/fp32 [T, N], y bf16/fp32 [T*top, N]
+    (None: no gradient of the weights) -> (dy bf16 [T*top, N], dw float32 [T, top] or None)."""
+    what = "moe_combine_backward"
+    d_code = _require_float(what, dout, "dout")
+    _require(what, inverse, "inverse", torch.int32, dout)
+    _require(what, topk_w, "topk_w", torch.float32, dout)
+    if dout.dim() != 2 or inverse.dim() != 2 or inverse.shape[0] != dout.shape[0] or topk_w.shape != inverse.shape:
+        raise QuadsError(f"{what}: dout {tuple(dout.shape)}, inverse {tuple(inverse.shape)} and topk_w "
+                         f"{tuple(topk_w.shape)} must be [T, N] and [T, top]")
+    (T, N), top = dout.shape, inverse.shape[1]
+    y_code, dw = F32, None
+    if y is not None:
+        y_code = _require_float(what, y, "y", dout)
+        if tuple(y.shape) != (T * top, N):
+            raise QuadsError(f"{what}: y must be [{T * top}, {N}], not {list(y.shape)}")
+        dw = torch.empty(T, top, dtype=torch.float32, device=dout.device)
+    dy = torch.empty(T * top, N, dtype=torch.bfloat16, device=dout.device)
+    _on_device(dout, load().quads_moe_combine_backward, what, dout.data_ptr(), d_code, None if y is None else y.data_ptr(),
+               y_code, inverse.data_ptr(), topk_w.data_ptr(), T, top, N, dy.data_ptr(), None if dw is None else dw.data_ptr())
+    return dy, dw

@@ -11,6 +11,7 @@
 
 #include "../../include/quads.h"
 #include "launch.hpp"
+#include "layer_launch.hpp"
 #include "mx_launch.hpp"
 
 namespace {
@@ -750,6 +751,179 @@ quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_
   a.out = static_cast<uint16_t *>(dgu_bf16);
   a.gu = static_cast<const uint16_t *>(gu_bf16);
   return device_status(quads::launch_gated_backward(a, static_cast<hipStream_t>(stream)), "gated_backward");
+}
+
+// ---- around the experts ----------------------------------------------------------
+
+static bool float_type(int32_t t) { return t == QUADS_F32 || t == QUADS_BF16; }
+
+static quads_status_t norm_shape(const char *what, int64_t rows, int64_t cols) {
+  if (cols <= 0 || cols % 16 || cols > quads::kNormCols)
+    return fail(QUADS_ERR_SHAPE, "%s: cols must be a positive multiple of 16, at most %d", what, quads::kNormCols);
+  if (rows < 0 || rows > 0x7FFFFFFF) return fail(QUADS_ERR_SHAPE, "%s: row count out of range", what);
+  return QUADS_OK;
+}
+
+quads_status_t quads_rms_norm(const quads_rms_norm_args *a, void *stream) {
+  if (!a) return fail(QUADS_ERR_ARG, "rms_norm: null args");
+  if (a->struct_size != sizeof(quads_rms_norm_args))
+    return fail(QUADS_ERR_ARG, "rms_norm: struct_size %u != %zu", a->struct_size, sizeof(quads_rms_norm_args));
+  if (a->q_format != QUADS_NONE && a->q_format != QUADS_MXFP4 && a->q_format != QUADS_MXFP8)
+    return fail(QUADS_ERR_ARG, "rms_norm: bad q_format %d", a->q_format);
+  if (a->reserved || (a->flags & ~QUADS_MX_SCALE_EVEN) || (a->flags && a->q_format != QUADS_MXFP4))
+    return fail(QUADS_ERR_ARG, "rms_norm: unknown flags");
+  if (!float_type(a->x_dtype) || !float_type(a->weight_dtype) || (a->residual && !float_type(a->residual_dtype)))
+    return fail(QUADS_ERR_ARG, "rms_norm: bad dtype");
+  const quads_status_t st = norm_shape("rms_norm", a->rows, a->cols);
+  if (st != QUADS_OK) return st;
+  const bool quantized = a->q_format != QUADS_NONE;
+  if (quantized && a->cols % 32) return fail(QUADS_ERR_SHAPE, "rms_norm: a quantized output needs cols % 32 == 0");
+  if (!(a->eps >= 0.0f)) return fail(QUADS_ERR_ARG, "rms_norm: eps must not be negative");
+  if (misaligned({a->x, a->residual, a->weight, a->sum, a->y_bf16, a->q_codes, a->q_scales, a->rstd}))
+    return fail(QUADS_ERR_ARG, "rms_norm: arrays must be 16-byte aligned");
+  if (a->sum && !a->residual) return fail(QUADS_ERR_ARG, "rms_norm: sum without a residual");
+  if (!quantized && (a->q_codes || a->q_scales)) return fail(QUADS_ERR_ARG, "rms_norm: quantized arrays without a q_format");
+  if (a->rows == 0) return ok();
+  if (!a->x || !a->weight || (a->residual && !a->sum) || (quantized && (!a->q_codes || !a->q_scales)))
+    return fail(QUADS_ERR_ARG, "rms_norm: null pointer");
+  quads::NormLaunch g{};
+  g.rows = a->rows;
+  g.cols = static_cast<int32_t>(a->cols);
+  g.x_f32 = a->x_dtype == QUADS_F32;
+  g.residual_f32 = a->residual_dtype == QUADS_F32;
+  g.weight_f32 = a->weight_dtype == QUADS_F32;
+  g.quant = a->q_format == QUADS_MXFP4 ? quads::kNormQuantMx4 : quantized ? quads::kNormQuantMx8 : quads::kNormQuantNone;
+  g.even = (a->flags & QUADS_MX_SCALE_EVEN) != 0;
+  g.eps = a->eps;
+  g.x = a->x;
+  g.residual = a->residual;
+  g.weight = a->weight;
+  g.sum = a->sum;
+  g.y = static_cast<uint16_t *>(a->y_bf16);
+  g.codes = a->q_codes;
+  g.scales = a->q_scales;
+  g.rstd = a->rstd;
+  return device_status(quads::launch_rms_norm(g, static_cast<hipStream_t>(stream)), "rms_norm");
+}
+
+quads_status_t quads_dequantize_mxfp8(quads_mxfp8_t q, void *out, quads_dtype_t dt, void *stream) {
+  if (dt != QUADS_F32 && dt != QUADS_BF16) return fail(QUADS_ERR_ARG, "dequantize_mxfp8: bad dtype %d", dt);
+  if (q.batch <= 0 || q.rows < 0) return fail(QUADS_ERR_SHAPE, "dequantize_mxfp8: bad shape");
+  if (q.cols <= 0 || q.cols % 32)
+    return fail(QUADS_ERR_SHAPE, "dequantize_mxfp8: cols must be a positive multiple of 32");
+  if (!mul_ok(q.batch, q.rows, kMaxElems) || !mul_ok(q.batch * q.rows, q.cols, kMaxElems))
+    return fail(QUADS_ERR_SHAPE, "dequantize_mxfp8: size overflow");
+  if (misaligned({q.codes, q.scales, out})) return fail(QUADS_ERR_ARG, "dequantize_mxfp8: arrays must be 16-byte aligned");
+  if (q.rows == 0) return ok();
+  if (!q.codes || !q.scales || !out) return fail(QUADS_ERR_ARG, "dequantize_mxfp8: null pointer");
+  return device_status(quads::launch_mx8_dequantize(q.codes, q.scales, q.batch * q.rows * q.cols, out, dt == QUADS_BF16,
+                                                    static_cast<hipStream_t>(stream)),
+                       "dequantize_mxfp8");
+}
+
+size_t quads_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || rows > 0x7FFFFFFF || cols <= 0 || cols % 16 || cols > quads::kNormCols) return 0;
+  return quads::norm_grad_ws_bytes(rows, static_cast<int32_t>(cols));
+}
+
+quads_status_t quads_rms_norm_backward(const void *dy, quads_dtype_t dy_dtype, const void *s, quads_dtype_t s_dtype,
+                                       const void *weight, quads_dtype_t weight_dtype, const float *rstd,
+                                       const void *dsum, int64_t rows, int64_t cols, void *dx, float *dweight, void *ws,
+                                       size_t ws_bytes, void *stream) {
+  if (!float_type(dy_dtype) || !float_type(s_dtype) || !float_type(weight_dtype))
+    return fail(QUADS_ERR_ARG, "rms_norm_backward: bad dtype");
+  const quads_status_t st = norm_shape("rms_norm_backward", rows, cols);
+  if (st != QUADS_OK) return st;
+  if (misaligned({dy, s, weight, rstd, dsum, dx, dweight, ws}))
+    return fail(QUADS_ERR_ARG, "rms_norm_backward: arrays must be 16-byte aligned");
+  if (rows == 0 && !dweight) return ok();
+  if (rows > 0 && (!dy || !s || !weight || !rstd || !dx)) return fail(QUADS_ERR_ARG, "rms_norm_backward: null pointer");
+  const size_t need = dweight ? quads::norm_grad_ws_bytes(rows, static_cast<int32_t>(cols)) : 0;
+  if (need > 0 && (ws == nullptr || ws_bytes < need))
+    return fail(QUADS_ERR_WORKSPACE, "rms_norm_backward: workspace too small (need %zu)", need);
+  quads::NormGradLaunch g{};
+  g.rows = rows;
+  g.cols = static_cast<int32_t>(cols);
+  g.dy_f32 = dy_dtype == QUADS_F32;
+  g.s_f32 = s_dtype == QUADS_F32;
+  g.weight_f32 = weight_dtype == QUADS_F32;
+  g.dy = dy;
+  g.s = s;
+  g.weight = weight;
+  g.dsum = dsum;
+  g.rstd = rstd;
+  g.dx = dx;
+  g.dweight = dweight;
+  g.ws = static_cast<float *>(ws);
+  return device_status(quads::launch_rms_norm_grad(g, static_cast<hipStream_t>(stream)), "rms_norm_backward");
+}
+
+static quads_status_t route_shape(const char *what, int64_t T, int32_t E, int32_t top) {
+  if (E < 1 || E > 1024) return fail(QUADS_ERR_SHAPE, "%s: E must be in [1, 1024]", what);
+  if (top < 1 || top > 16 || top > E) return fail(QUADS_ERR_SHAPE, "%s: top must be in [1, min(E, 16)]", what);
+  if (T < 0 || !mul_ok(T, top, 0x7FFFFFFF)) return fail(QUADS_ERR_SHAPE, "%s: token count out of range", what);
+  return QUADS_OK;
+}
+
+size_t quads_moe_balance_loss_workspace_bytes(int64_t T, int32_t E) {
+  if (T < 0 || E < 1 || E > 1024) return 0;
+  return quads::balance_ws_bytes(T, E);
+}
+
+quads_status_t quads_moe_balance_loss(const float *logits, const int32_t *ids, const uint8_t *mask, int64_t T, int32_t E,
+                                      int32_t top, float coef, float *loss, int32_t *counts, float *slope, void *ws,
+                                      size_t ws_bytes, void *stream) {
+  const quads_status_t st = route_shape("balance_loss", T, E, top);
+  if (st != QUADS_OK) return st;
+  if (misaligned({logits, ids, mask, loss, counts, slope, ws}))
+    return fail(QUADS_ERR_ARG, "balance_loss: arrays must be 16-byte aligned");
+  if (!loss || !counts || !slope || (T > 0 && (!logits || !ids))) return fail(QUADS_ERR_ARG, "balance_loss: null pointer");
+  const size_t need = quads::balance_ws_bytes(T, E);
+  if (need > 0 && (ws == nullptr || ws_bytes < need))
+    return fail(QUADS_ERR_WORKSPACE, "balance_loss: workspace too small (need %zu)", need);
+  const quads::BalanceLaunch a{logits, ids, mask, T, E, top, coef, loss, counts, slope, ws};
+  return device_status(quads::launch_balance(a, static_cast<hipStream_t>(stream)), "balance_loss");
+}
+
+quads_status_t quads_moe_route_backward(const float *logits, const int32_t *ids, const uint8_t *mask, const float *dw,
+                                        const float *slope, const float *dloss, int64_t T, int32_t E, int32_t top,
+                                        float *dlogits, void *stream) {
+  const quads_status_t st = route_shape("route_backward", T, E, top);
+  if (st != QUADS_OK) return st;
+  if (misaligned({logits, ids, mask, dw, slope, dloss, dlogits}))
+    return fail(QUADS_ERR_ARG, "route_backward: arrays must be 16-byte aligned");
+  if (T == 0) return ok();
+  if (!logits || !dlogits || (dw && !ids)) return fail(QUADS_ERR_ARG, "route_backward: null pointer");
+  const quads::RouteGradLaunch a{logits, ids, mask, dw, slope, dloss, T, E, top, dlogits};
+  return device_status(quads::launch_route_grad(a, static_cast<hipStream_t>(stream)), "route_backward");
+}
+
+quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_dtype, const void *y, quads_dtype_t y_dtype,
+                                          const int32_t *inverse, const float *topk_w, int64_t T, int32_t top, int64_t N,
+                                          void *dy_bf16, float *dw, void *stream) {
+  if (!float_type(dout_dtype) || !float_type(y_dtype)) return fail(QUADS_ERR_ARG, "combine_backward: bad dtype");
+  if (top < 1 || top > 16) return fail(QUADS_ERR_SHAPE, "combine_backward: top must be in [1, 16]");
+  if (T < 0 || !mul_ok(T, top, 0x7FFFFFFF)) return fail(QUADS_ERR_SHAPE, "combine_backward: token count out of range");
+  if (N <= 0 || N % 16) return fail(QUADS_ERR_SHAPE, "combine_backward: N must be a positive multiple of 16");
+  if (!mul_ok(T * top, N, kMaxElems)) return fail(QUADS_ERR_SHAPE, "combine_backward: size overflow");
+  if (misaligned({dout, y, inverse, topk_w, dy_bf16, dw}))
+    return fail(QUADS_ERR_ARG, "combine_backward: arrays must be 16-byte aligned");
+  if (T == 0) return ok();
+  if (!dout || !inverse || !topk_w || !dy_bf16 || (dw && !y)) return fail(QUADS_ERR_ARG, "combine_backward: null pointer");
+  quads::CombineGradLaunch a{};
+  a.dout = dout;
+  a.y = y;
+  a.dout_bf16 = dout_dtype == QUADS_BF16;
+  a.y_bf16 = y_dtype == QUADS_BF16;
+  a.inverse = inverse;
+  a.w = topk_w;
+  a.T = T;
+  a.rows = T * top;
+  a.top = top;
+  a.N = N;
+  a.dy = static_cast<uint16_t *>(dy_bf16);
+  a.dw = dw;
+  return device_status(quads::launch_combine_grad(a, static_cast<hipStream_t>(stream)), "combine_backward");
 }
 
 }  // extern "C"

@@ -1,4 +1,4 @@
-// Device-side MXFP4 codec for the gfx950 kernels.
+// Device-side MXFP4 and MXFP8 codecs for the gfx950 kernels.
 //
 // MXFP4 (OCP Microscaling): blocks of 32 elements along the last axis share
 // one E8M0 scale, a power of two 2^E stored as the byte E + 127; the elements
@@ -12,6 +12,13 @@
 // block with a NaN or an infinity gets byte 255 (E8M0's NaN) and codes 0, so
 // every value it stands for is NaN.  Multiplying by 2^-E is exact except
 // where the product is far below the first rounding threshold (0.25).
+//
+// MXFP8 has the same blocks with E4M3 elements (largest exponent 8, largest
+// value 448 = 1.75 * 2^8):
+//   E    = floor(log2 a) - 8, at least -127
+//   code = E4M3 nearest to x * 2^-E, ties to even, saturating at 448
+// so magnitudes in (448, 512) * 2^E saturate (off by at most 1/8).  Zero,
+// subnormal and non-finite blocks as above.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -61,6 +68,49 @@ __device__ __forceinline__ void mx_unpack8(uint32_t c, float (&v)[8]) {
   const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
   const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
   const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+  v[0] = a[0];
+  v[1] = a[1];
+  v[2] = b[0];
+  v[3] = b[1];
+  v[4] = d[0];
+  v[5] = d[1];
+  v[6] = e[0];
+  v[7] = e[1];
+}
+
+// Maximum over the aligned quad of lanes (quad_perm [1,0,3,2] and [2,3,0,1]).
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xF, 0xF, true)));
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xF, 0xF, true)));
+}
+
+// E8M0 byte of an MXFP8 block from the bits of its largest magnitude.
+__device__ __forceinline__ uint32_t mx8_scale_byte(uint32_t abs_bits) {
+  const uint32_t e = abs_bits >> 23;
+  return abs_bits >= 0x7F800000u ? kMxNan : e < 8u ? 0u : e - 8u;
+}
+
+// v[0..7] (already multiplied by 2^-E) -> 8 E4M3 codes, element i in byte i.
+// The conversion rounds to nearest even; what it makes of larger magnitudes
+// does not matter behind the clamp.
+__device__ __forceinline__ uint2 mx8_pack8(const float (&v)[8]) {
+  float c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = __builtin_amdgcn_fmed3f(v[i], -448.0f, 448.0f);
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], hi, true);
+  return make_uint2(static_cast<uint32_t>(lo), static_cast<uint32_t>(hi));
+}
+
+// 8 codes -> 8 values (exact; a NaN code stays NaN).
+__device__ __forceinline__ void mx8_unpack8(uint2 c, float (&v)[8]) {
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.x), false);
+  const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.x), true);
+  const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.y), false);
+  const f32x2 e = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c.y), true);
   v[0] = a[0];
   v[1] = a[1];
   v[2] = b[0];

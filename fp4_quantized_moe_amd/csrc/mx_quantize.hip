@@ -16,12 +16,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Maximum over the aligned quad of lanes (quad_perm [1,0,3,2] and [2,3,0,1]).
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xF, 0xF, true)));
-  return max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xF, 0xF, true)));
-}
-
 __device__ __forceinline__ void store_bf16x8(uint16_t *p, const float (&v)[8]) {
   *reinterpret_cast<uint4 *>(p) =
       make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));

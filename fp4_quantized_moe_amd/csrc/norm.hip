@@ -1,0 +1,435 @@
+// Root-mean-square norm with the residual's addition, and its gradient.
+//
+//   s = x + residual (rounded to the stream's type and kept),
+//   r = (mean(s^2) + eps)^(-1/2),  y = s r w,
+// y leaves as bf16, as MXFP4 or MXFP8 (each rounded once from the fp32 y), or
+// as bf16 and one of them.  Gradient, with n = s r, d = dy w:
+//   dx = r (d - n mean(d n)) + dsum,  dw = sum over rows of dy n.
+//
+// Bound: HBM.  A row stays in registers between its sum and its outputs, so
+// every element is read and written once.  A lane holds units of 8 consecutive
+// elements (16 bytes of bf16); the four lanes of an aligned quad hold a block
+// of 32, whose largest magnitude crosses the quad by two DPP permutations.
+#include <algorithm>
+
+#include "layer_launch.hpp"
+#include "mx_device.hpp"
+#include "quads_device.hpp"
+
+namespace quads {
+namespace {
+
+// Sum over the wave in a fixed order, in all lanes.
+__device__ __forceinline__ float wave_sum(float v) {
+  const auto step = [&](auto ctrl, auto mask) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, decltype(mask)::value, 0xf, false));
+  };
+  step(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xf>{});
+  step(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xf>{});
+  step(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xf>{});
+  step(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xf>{});
+  step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});
+  step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sum over the TPR lanes of a row: a wave, or the four waves of a workgroup
+// (`parts`: their meeting place; a barrier).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *parts) {
+  v = wave_sum(v);
+  if constexpr (TPR == 64) return v;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (lane == 0) parts[wave] = v;
+  __syncthreads();
+  const float4 p = *reinterpret_cast<const float4 *>(parts + (wave & ~3));
+  return ((p.x + p.y) + p.z) + p.w;
+}
+
+// A unit of 8 values as loaded: bf16 fills `lo` alone.
+struct Raw {
+  uint4 lo, hi;
+};
+
+__device__ __forceinline__ Raw load_unit(const void *p, int64_t unit, bool f32) {
+  Raw r;
+  if (f32) {
+    const uint4 *q = static_cast<const uint4 *>(p) + 2 * unit;
+    r.lo = q[0];
+    r.hi = q[1];
+  } else {
+    r.lo = static_cast<const uint4 *>(p)[unit];
+    r.hi = r.lo;
+  }
+  return r;
+}
+
+__device__ __forceinline__ void unpack(const Raw &r, bool f32, float (&v)[8]) {
+  const uint32_t lo[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w}, hi[4] = {r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (f32) {
+      v[i] = __uint_as_float(lo[i]);
+      v[4 + i] = __uint_as_float(hi[i]);
+    } else {
+      v[2 * i] = __uint_as_float(lo[i] << 16);
+      v[2 * i + 1] = __uint_as_float(lo[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint4 pack_unit(const float (&v)[8]) {
+  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
+__device__ __forceinline__ void store_unit(void *p, int64_t unit, bool f32, const float (&v)[8]) {
+  if (f32) {
+    float4 *q = static_cast<float4 *>(p) + 2 * unit;
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    static_cast<uint4 *>(p)[unit] = pack_unit(v);
+  }
+}
+
+struct NormParams {
+  int64_t rows;
+  int32_t units;  // of 8 columns
+  float cols, eps;
+  uint32_t add;  // MXFP4's scale rule
+  bool x_f32, residual_f32, weight_f32;
+  const void *x, *residual, *weight;
+  void *sum;
+  uint16_t *y;
+  uint8_t *codes, *scales;
+  float *rstd;
+};
+
+// TPR lanes a row, V units a lane.
+template <int QUANT, int TPR, int V>
+__global__ __launch_bounds__(256) void k_rms_norm(NormParams p) {
+  __shared__ __attribute__((aligned(16))) float parts[4];
+  const int t = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t row = TPR == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (TPR == 64 && row >= p.rows) return;  // whole waves, and no barrier with TPR == 64
+  const int64_t first = row * p.units;
+
+  Raw x[V], res[V], w[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = load_unit(p.x, first + min(t + v * TPR, p.units - 1), p.x_f32);
+  if (p.residual) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) res[v] = load_unit(p.residual, first + min(t + v * TPR, p.units - 1), p.residual_f32);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) w[v] = load_unit(p.weight, min(t + v * TPR, p.units - 1), p.weight_f32);
+
+  float s[V][8], ss = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int unit = t + v * TPR;
+    unpack(x[v], p.x_f32, s[v]);
+    if (p.residual) {
+      float r[8];
+      unpack(res[v], p.residual_f32, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[v][i] = s[v][i] + r[i];
+      if (!p.residual_f32) {  // what is normalised is the stream as it is kept
+        const uint4 k = pack_unit(s[v]);
+        if (unit < p.units) static_cast<uint4 *>(p.sum)[first + unit] = k;
+        unpack(Raw{k, k}, false, s[v]);
+      } else if (unit < p.units) {
+        store_unit(p.sum, first + unit, true, s[v]);
+      }
+    }
+    if (unit < p.units) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(s[v][i], s[v][i], ss);
+    }
+  }
+  const float r = 1.0f / sqrtf(row_sum<TPR>(ss, parts) / p.cols + p.eps);
+  if (p.rstd && t == 0) p.rstd[row] = r;
+
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int unit = t + v * TPR;
+    float y[8], g[8];
+    unpack(w[v], p.weight_f32, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = s[v][i] * r * g[i];
+    if (p.y && unit < p.units) static_cast<uint4 *>(static_cast<void *>(p.y))[first + unit] = pack_unit(y);
+    if constexpr (QUANT != kNormQuantNone) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+      a = quad_max(a);  // quads lie inside the row or behind it: cols % 32 == 0
+      const uint32_t b = QUANT == kNormQuantMx4 ? mx_scale_byte(a, p.add) : mx8_scale_byte(a);
+      const float inv = mx_inv_scale(b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= inv;
+      if (unit < p.units) {
+        if constexpr (QUANT == kNormQuantMx4) {
+          const uint32_t c = mx_pack8(y);
+          reinterpret_cast<uint32_t *>(p.codes)[first + unit] = b == kMxNan ? 0u : c;
+        } else {
+          const uint2 c = mx8_pack8(y);
+          reinterpret_cast<uint2 *>(p.codes)[first + unit] = b == kMxNan ? make_uint2(0, 0) : c;
+        }
+        if ((t & 3) == 0) p.scales[(first + unit) >> 2] = static_cast<uint8_t>(b);
+      }
+    }
+  }
+}
+
+template <int QUANT, int TPR>
+hipError_t run_norm(const NormParams &p, hipStream_t stream) {
+  const int64_t groups = TPR == 64 ? (p.rows + 3) / 4 : p.rows;
+  if (groups > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(groups)), threads(256);
+  const int per = (p.units + TPR - 1) / TPR;
+  if (per <= 1) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 1>), grid, threads, 0, stream, p);
+  else if (per <= 2) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 2>), grid, threads, 0, stream, p);
+  else if (per <= 4) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 4>), grid, threads, 0, stream, p);
+  else hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 8>), grid, threads, 0, stream, p);
+  return hipGetLastError();
+}
+
+// ---- gradient --------------------------------------------------------------------
+
+struct NormGradParams {
+  int64_t rows;
+  int32_t units;
+  float cols;
+  bool dy_f32, s_f32, weight_f32;
+  const void *dy, *s, *weight, *dsum;
+  const float *rstd;
+  void *dx;
+  float *partial;  // [gridDim.x, cols] sums of dy n, or null
+};
+
+constexpr int kGradThreads = 512;
+
+// 512 / TPR rows of a workgroup at once; workgroups stay and take rows in turn.
+template <int TPR, int V>
+__global__ __launch_bounds__(kGradThreads) void k_rms_norm_grad(NormGradParams p) {
+  constexpr int ROWS = kGradThreads / TPR;
+  __shared__ __attribute__((aligned(16))) float parts[2][8];
+  __shared__ __attribute__((aligned(16))) float meet[(ROWS - 1) * TPR * 8];
+  const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+  float acc[V][8] = {};
+  int turn = 0;
+  // Every wave makes the same number of rounds: the rows' sums contain a barrier.
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * ROWS; base < p.rows; base += static_cast<int64_t>(gridDim.x) * ROWS) {
+    const bool live = base + slot < p.rows;
+    const int64_t row = live ? base + slot : p.rows - 1, first = row * p.units;
+    Raw s[V], dy[V], w[V], ds[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = load_unit(p.s, first + min(t + v * TPR, p.units - 1), p.s_f32);
+#pragma unroll
+    for (int v = 0; v < V; ++v) dy[v] = load_unit(p.dy, first + min(t + v * TPR, p.units - 1), p.dy_f32);
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[v] = load_unit(p.weight, min(t + v * TPR, p.units - 1), p.weight_f32);
+    if (p.dsum) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) ds[v] = load_unit(p.dsum, first + min(t + v * TPR, p.units - 1), p.s_f32);
+    }
+    const float r = p.rstd[row];
+    float n[V][8], d[V][8], dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float g[8];
+      unpack(s[v], p.s_f32, n[v]);
+      unpack(dy[v], p.dy_f32, d[v]);
+      unpack(w[v], p.weight_f32, g);
+      const bool in = live && t + v * TPR < p.units;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n[v][i] *= r;
+        if (in) acc[v][i] = __builtin_fmaf(d[v][i], n[v][i], acc[v][i]);
+        d[v][i] *= g[i];
+        if (in) dot = __builtin_fmaf(d[v][i], n[v][i], dot);
+      }
+    }
+    const float mean = row_sum<TPR>(dot, parts[turn]) / p.cols;
+    turn ^= 1;  // a wave is at most one barrier ahead: the next row's sums go elsewhere
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!live || t + v * TPR >= p.units) continue;
+      float dx[8], e[8];
+      if (p.dsum) unpack(ds[v], p.s_f32, e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dx[i] = r * (d[v][i] - n[v][i] * mean);
+        if (p.dsum) dx[i] += e[i];
+      }
+      store_unit(p.dx, first + t + v * TPR, p.s_f32, dx);
+    }
+  }
+  if (p.partial == nullptr) return;
+  // The workgroup's rows meet unit by unit, in the slots' order.
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (v * TPR >= p.units) break;
+    __syncthreads();
+    if (slot > 0) {
+      float4 *m = reinterpret_cast<float4 *>(meet) + (slot - 1) * TPR * 2 + t;
+      m[0] = make_float4(acc[v][0], acc[v][1], acc[v][2], acc[v][3]);
+      m[TPR] = make_float4(acc[v][4], acc[v][5], acc[v][6], acc[v][7]);
+    }
+    __syncthreads();
+    if (slot == 0 && t + v * TPR < p.units) {
+      for (int k = 0; k < ROWS - 1; ++k) {
+        const float4 *m = reinterpret_cast<const float4 *>(meet) + k * TPR * 2 + t;
+        const float4 a = m[0], b = m[TPR];
+        acc[v][0] += a.x;
+        acc[v][1] += a.y;
+        acc[v][2] += a.z;
+        acc[v][3] += a.w;
+        acc[v][4] += b.x;
+        acc[v][5] += b.y;
+        acc[v][6] += b.z;
+        acc[v][7] += b.w;
+      }
+      store_unit(p.partial, static_cast<int64_t>(blockIdx.x) * p.units + t + v * TPR, true, acc[v]);
+    }
+  }
+}
+
+// dweight = sum of the partial sums in order: 32 columns a workgroup, 32 parts.
+__global__ __launch_bounds__(256) void k_fold_columns(const float *partial, int parts, int32_t cols, float *out) {
+  __shared__ __attribute__((aligned(16))) float4 meet[32][8];
+  const int c4 = threadIdx.x & 7, part = threadIdx.x >> 3;
+  const int32_t col = blockIdx.x * 32 + 4 * c4;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < cols) {
+    for (int k = part; k < parts; k += 32) {
+      const float4 b = *reinterpret_cast<const float4 *>(partial + static_cast<int64_t>(k) * cols + col);
+      a.x += b.x;
+      a.y += b.y;
+      a.z += b.z;
+      a.w += b.w;
+    }
+  }
+  meet[part][c4] = a;
+  __syncthreads();
+  if (part == 0 && col < cols) {
+    for (int k = 1; k < 32; ++k) {
+      const float4 b = meet[k][c4];
+      a.x += b.x;
+      a.y += b.y;
+      a.z += b.z;
+      a.w += b.w;
+    }
+    *reinterpret_cast<float4 *>(out + col) = a;
+  }
+}
+
+// Lanes of a row: a wave where there are rows to fill the card, else four.
+bool wave_rows(int64_t rows, int32_t units) { return units <= 64 * 8 && rows >= 2048; }
+
+int grad_groups(int64_t rows, int32_t units) {
+  const int64_t per = kGradThreads / (wave_rows(rows, units) ? 64 : 256);
+  return static_cast<int>(std::min<int64_t>((rows + per - 1) / per, 512));
+}
+
+template <int TPR>
+void run_norm_grad(const NormGradParams &p, int groups, hipStream_t stream) {
+  const dim3 grid(groups), threads(kGradThreads);
+  const int per = (p.units + TPR - 1) / TPR;
+  if (per <= 1) hipLaunchKernelGGL((k_rms_norm_grad<TPR, 1>), grid, threads, 0, stream, p);
+  else if (per <= 2) hipLaunchKernelGGL((k_rms_norm_grad<TPR, 2>), grid, threads, 0, stream, p);
+  else if (per <= 4) hipLaunchKernelGGL((k_rms_norm_grad<TPR, 4>), grid, threads, 0, stream, p);
+  else hipLaunchKernelGGL((k_rms_norm_grad<TPR, 8>), grid, threads, 0, stream, p);
+}
+
+// ---- MXFP8 back to values ----------------------------------------------------------
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_mx8_dequantize(const uint2 *codes, const uint8_t *scales, int64_t units, void *out) {
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (unit >= units) return;
+  float v[8];
+  mx8_unpack8(codes[unit], v);
+  const float m = mx_scale(scales[unit >> 2]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= m;
+  store_unit(out, unit, !BF16, v);
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormLaunch &a, hipStream_t stream) {
+  if (a.rows == 0) return hipSuccess;
+  NormParams p{};
+  p.rows = a.rows;
+  p.units = a.cols / 8;
+  p.cols = static_cast<float>(a.cols);
+  p.eps = a.eps;
+  p.add = a.even ? kMxEvenAdd : 0u;
+  p.x_f32 = a.x_f32;
+  p.residual_f32 = a.residual_f32;
+  p.weight_f32 = a.weight_f32;
+  p.x = a.x;
+  p.residual = a.residual;
+  p.weight = a.weight;
+  p.sum = a.sum;
+  p.y = a.y;
+  p.codes = a.codes;
+  p.scales = a.scales;
+  p.rstd = a.rstd;
+  const bool wave = wave_rows(a.rows, p.units);
+  switch (a.quant) {
+    case kNormQuantNone: return wave ? run_norm<kNormQuantNone, 64>(p, stream) : run_norm<kNormQuantNone, 256>(p, stream);
+    case kNormQuantMx4: return wave ? run_norm<kNormQuantMx4, 64>(p, stream) : run_norm<kNormQuantMx4, 256>(p, stream);
+    default: return wave ? run_norm<kNormQuantMx8, 64>(p, stream) : run_norm<kNormQuantMx8, 256>(p, stream);
+  }
+}
+
+size_t norm_grad_ws_bytes(int64_t rows, int32_t cols) {
+  return static_cast<size_t>(grad_groups(rows, cols / 8)) * cols * sizeof(float);
+}
+
+hipError_t launch_rms_norm_grad(const NormGradLaunch &a, hipStream_t stream) {
+  NormGradParams p{};
+  p.rows = a.rows;
+  p.units = a.cols / 8;
+  p.cols = static_cast<float>(a.cols);
+  p.dy_f32 = a.dy_f32;
+  p.s_f32 = a.s_f32;
+  p.weight_f32 = a.weight_f32;
+  p.dy = a.dy;
+  p.s = a.s;
+  p.weight = a.weight;
+  p.dsum = a.dsum;
+  p.rstd = a.rstd;
+  p.dx = a.dx;
+  p.partial = a.dweight ? a.ws : nullptr;
+  const int groups = grad_groups(a.rows, p.units);
+  if (groups > 0) {
+    if (wave_rows(a.rows, p.units)) run_norm_grad<64>(p, groups, stream);
+    else run_norm_grad<256>(p, groups, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.dweight)  // of no rows: zeros
+    hipLaunchKernelGGL(k_fold_columns, dim3((a.cols + 31) / 32), dim3(256), 0, stream, a.ws, groups, a.cols, a.dweight);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx8_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t elems, void *out, bool out_bf16,
+                                 hipStream_t stream) {
+  constexpr int64_t kLaunchUnits = int64_t(1) << 31;  // a grid's lanes are counted in 32 bits
+  for (int64_t u = 0, units; u < elems / 8; u += units) {
+    units = std::min(elems / 8 - u, kLaunchUnits);
+    const dim3 grid(static_cast<unsigned>((units + 255) / 256));
+    const uint2 *c = reinterpret_cast<const uint2 *>(codes) + u;
+    uint8_t *o = static_cast<uint8_t *>(out) + u * (out_bf16 ? 16 : 32);
+    if (out_bf16) hipLaunchKernelGGL((k_mx8_dequantize<true>), grid, dim3(256), 0, stream, c, scales + u / 4, units, o);
+    else hipLaunchKernelGGL((k_mx8_dequantize<false>), grid, dim3(256), 0, stream, c, scales + u / 4, units, o);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace quads

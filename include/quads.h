@@ -556,6 +556,118 @@ quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_
                                              const int32_t *expert_offsets, int32_t num_experts, int64_t num_rows,
                                              int64_t hidden, int64_t inter, void *dgu_bf16, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * What a training step of the layer needs around the experts, and the norm in
+ * front of it.  All of them: sums and statistics in fp32 or more, each output
+ * rounded once; sums in a fixed order, so repeated calls give the same bits.
+ * NaN and infinities are defined: they go where the formulas take them.
+ *
+ * quads_rms_norm -- the residual stream's addition and its root-mean-square
+ * norm, row by row (cols columns, a multiple of 16, at most 16384):
+ *   s = x + residual   (fp32, rounded to residual_dtype and written to sum;
+ *                       without a residual s = x and sum is NULL),
+ *   r = 1 / sqrt(mean(s^2) + eps),   y = s r weight.
+ * What is normalised is the stored s.  Outputs, each optional: y_bf16 [rows,
+ * cols]; with q_format QUADS_MXFP4 or QUADS_MXFP8 (cols % 32 == 0) the fp32 y
+ * in that format, q_codes and q_scales (MXFP4: what quads_moe_mxfp4_gemm
+ * takes; flags QUADS_MX_SCALE_EVEN as in quads_quantize_mxfp4); rstd [rows]
+ * fp32 receives r for the backward.  sum may be residual or x (of its type).
+ *
+ * MXFP8: blocks of 32 elements along the row share one E8M0 byte (as MXFP4);
+ * elements are OCP E4M3 bytes [rows, cols].  A block with largest magnitude a
+ * takes E = floor(log2 a) - 8, at least -127, and its elements the E4M3 value
+ * nearest to y * 2^-E, ties to even, saturating at 448.  A block with NaN or
+ * infinities gets byte 255 and codes 0.  quads_dequantize_mxfp8: the values
+ * `q` stands for, bf16 or fp32 (exact where the type holds them).
+ *
+ * quads_rms_norm_backward -- with n = s rstd and d = dy weight:
+ *   dx = rstd (d - n mean(d n)) + dsum,   dweight = sum over rows of dy n.
+ * dx (of s's type) is the gradient of x and of residual alike; dsum (of s's
+ * type, or NULL) is the gradient that reaches s past the norm.  The gradient
+ * passes the outputs' rounding unchanged.  dweight [cols] fp32, or NULL: then
+ * no workspace is needed (else quads_rms_norm_backward_workspace_bytes).  dx
+ * may be dsum, or dy if of one type.  rows == 0: dweight = 0.
+ * ------------------------------------------------------------------------- */
+#define QUADS_NONE (-1) /* quads_rms_norm_args.q_format: no quantized output */
+#define QUADS_MXFP8 3
+
+typedef struct {
+  uint32_t struct_size;   /* sizeof(quads_rms_norm_args) */
+  uint32_t flags;         /* 0 or QUADS_MX_SCALE_EVEN (with QUADS_MXFP4) */
+  int32_t x_dtype, residual_dtype, weight_dtype; /* QUADS_F32 | QUADS_BF16 */
+  int32_t q_format;       /* QUADS_NONE | QUADS_MXFP4 | QUADS_MXFP8 */
+  int64_t rows, cols;
+  const void *x;          /* [rows, cols] */
+  const void *residual;   /* [rows, cols] or NULL */
+  const void *weight;     /* [cols] */
+  void *sum;              /* [rows, cols] of residual_dtype; NULL without a residual */
+  void *y_bf16;           /* [rows, cols] or NULL */
+  uint8_t *q_codes;       /* [rows, cols/2] (MXFP4) or [rows, cols] (MXFP8) */
+  uint8_t *q_scales;      /* [rows, cols/32] */
+  float *rstd;            /* [rows] or NULL */
+  float eps;              /* >= 0 */
+  int32_t reserved;       /* 0 */
+} quads_rms_norm_args;
+
+/* An MXFP8 tensor of `batch` matrices of [rows, cols] (cols % 32 == 0). */
+typedef struct {
+  uint8_t *codes;  /* [batch, rows, cols] E4M3 */
+  uint8_t *scales; /* [batch, rows, cols/32] E8M0 */
+  int64_t batch, rows, cols;
+} quads_mxfp8_t;
+
+quads_status_t quads_rms_norm(const quads_rms_norm_args *a, void *stream);
+quads_status_t quads_dequantize_mxfp8(quads_mxfp8_t q, void *out, quads_dtype_t dt, void *stream);
+
+size_t quads_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+quads_status_t quads_rms_norm_backward(const void *dy, quads_dtype_t dy_dtype, const void *s, quads_dtype_t s_dtype,
+                                       const void *weight, quads_dtype_t weight_dtype, const float *rstd,
+                                       const void *dsum, int64_t rows, int64_t cols, void *dx, float *dweight, void *ws,
+                                       size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The router's training side.  p = softmax(logits) over the E experts of a
+ * token (a row whose logits are all -inf has p = 0), ids [T, top] the experts
+ * chosen (quads_moe_route's topk_ids; values outside [0, E) are passed over),
+ * mask [T] bytes (NULL: all 1) with 0 for tokens that take no part (padding),
+ * n the tokens that do.
+ *
+ * quads_moe_balance_loss:
+ *   counts[e] = choices of expert e by the tokens that take part   (int32 [E]),
+ *   loss = coef E sum_e (counts[e] / (top n)) (1/n sum_t p[t, e])  (fp32 [1]),
+ * which is coef when experts are chosen evenly; n == 0: loss 0.  slope [E]
+ * fp32 receives d loss / d p[t, e] = coef E counts[e] / (top n^2), the same
+ * for all these tokens: the counts are constants in the gradient.
+ *
+ * quads_moe_route_backward: with dp[t, e] = dloss slope[e] + sum over the
+ * slots j with ids[t, j] == e of dw[t, j],
+ *   dlogits[t, e] = p[t, e] (dp[t, e] - sum_e' p[t, e'] dp[t, e']),
+ * and 0 for tokens that take no part.  dw [T, top] fp32 is the gradient of
+ * the combine weights (NULL: none; quads_moe_route's topk_w are the chosen
+ * probabilities), slope [E] that of the loss above (NULL: none), dloss [1]
+ * (device; NULL: 1) what the loss is multiplied by.  E <= 1024, 1 <= top <=
+ * min(E, 16).
+ *
+ * quads_moe_combine_backward -- gradient of quads_moe_combine, from dout [T,
+ * N] (F32 or BF16), y [T*top, N] (F32 or BF16), inverse and topk_w:
+ *   dy[inverse[t, j], :] = bf16(topk_w[t, j] dout[t, :]),
+ *   dw[t, j] = sum over columns of dout[t, :] y[inverse[t, j], :]  (fp32).
+ * dy [T*top, N] bf16 is the dy of quads_moe_gated_backward_bf16 and
+ * quads_moe_wgrad_bf16.  dw NULL: not computed, and y may be NULL.  A slot
+ * whose inverse lies outside [0, T*top) has no row: its dw is 0.  N % 16 == 0,
+ * top <= 16.
+ * ------------------------------------------------------------------------- */
+size_t quads_moe_balance_loss_workspace_bytes(int64_t T, int32_t E);
+quads_status_t quads_moe_balance_loss(const float *logits, const int32_t *ids, const uint8_t *mask, int64_t T, int32_t E,
+                                      int32_t top, float coef, float *loss, int32_t *counts, float *slope, void *ws,
+                                      size_t ws_bytes, void *stream);
+quads_status_t quads_moe_route_backward(const float *logits, const int32_t *ids, const uint8_t *mask, const float *dw,
+                                        const float *slope, const float *dloss, int64_t T, int32_t E, int32_t top,
+                                        float *dlogits, void *stream);
+quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_dtype, const void *y, quads_dtype_t y_dtype,
+                                          const int32_t *inverse, const float *topk_w, int64_t T, int32_t top, int64_t N,
+                                          void *dy_bf16, float *dw, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
