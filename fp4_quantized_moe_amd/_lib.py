@@ -94,7 +94,7 @@ EXPORTS = [
     "quads_moe_gated_forward_bf16", "quads_moe_gated_backward_bf16",
     "quads_rms_norm", "quads_rms_norm_backward_workspace_bytes", "quads_rms_norm_backward", "quads_dequantize_mxfp8",
     "quads_moe_balance_loss_workspace_bytes", "quads_moe_balance_loss", "quads_moe_route_backward",
-    "quads_moe_combine_backward",
+    "quads_moe_combine_backward", "quads_orthogonalize_workspace_bytes", "quads_orthogonalize",
 ]
 
 _lib = None
@@ -190,6 +190,11 @@ def load(path: str = LIB_PATH):
     L.quads_moe_combine_backward.restype = ctypes.c_int
     L.quads_moe_combine_backward.argtypes = [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _c_i64, _c_i32, _c_i64, _vp,
                                              _vp, _vp]
+    L.quads_orthogonalize_workspace_bytes.restype = ctypes.c_size_t
+    L.quads_orthogonalize_workspace_bytes.argtypes = [_c_i64, _c_i64, _c_i64]
+    L.quads_orthogonalize.restype = ctypes.c_int
+    L.quads_orthogonalize.argtypes = [_vp, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i32, ctypes.POINTER(_c_f32), _c_f32,
+                                      _vp, _vp, ctypes.c_size_t, _vp]
     _lib = L
     return L
 
@@ -1200,3 +1205,35 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, inverse: to
     _on_device(dout, load().quads_moe_combine_backward, what, dout.data_ptr(), d_code, None if y is None else y.data_ptr(),
                y_code, inverse.data_ptr(), topk_w.data_ptr(), T, top, N, dy.data_ptr(), None if dw is None else dw.data_ptr())
     return dy, dw
+
+
+# ---- orthogonalised updates --------------------------------------------------------
+
+def orthogonalize_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    return int(load().quads_orthogonalize_workspace_bytes(batch, rows, cols))
+
+
+def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                  out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """quads_orthogonalize: g bf16/fp32 [rows, cols] or [batch, rows, cols] (WgradCall's
+    dw; view stacked gate and up masters [E, 2 I, H] as [2 E, I, H]) -> bf16 of g's
+    shape, near the orthogonal matrix of each.  ws: a uint8 workspace of
+    orthogonalize_workspace_bytes(...) to reuse."""
+    what = "orthogonalize"
+    code = _require_float(what, g, "g")
+    batch, rows, cols = _batch_rows_cols(what, g.shape)
+    a, b, c = coefficients
+    L = load()
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    else:
+        _require(what, out, "out", torch.bfloat16, g)
+        if out.shape != g.shape:
+            raise QuadsError(f"{what}: out must have g's shape")
+    if ws is None:
+        ws = _workspace(L.quads_orthogonalize_workspace_bytes(batch, rows, cols), g.device)
+    else:
+        _require(what, ws, "ws", torch.uint8, g)
+    _on_device(g, L.quads_orthogonalize, what, g.data_ptr(), code, batch, rows, cols, steps, (_c_f32 * 3)(a, b, c), eps,
+               out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out

@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libquads.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.hip", "quantize.hip", "rac.hip", "gemm.hip", "gemm_small.hip", "route.hip", "backward.hip",
-           "mx_quantize.hip", "mx_gemm.hip", "gated.hip", "norm.hip", "route_grad.hip"]
+           "mx_quantize.hip", "mx_gemm.hip", "gated.hip", "norm.hip", "route_grad.hip",
+           "orthogonal.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

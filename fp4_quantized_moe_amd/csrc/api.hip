@@ -13,6 +13,7 @@
 #include "launch.hpp"
 #include "layer_launch.hpp"
 #include "mx_launch.hpp"
+#include "orthogonal_launch.hpp"
 
 namespace {
 
@@ -924,6 +925,52 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
   a.dy = static_cast<uint16_t *>(dy_bf16);
   a.dw = dw;
   return device_status(quads::launch_combine_grad(a, static_cast<hipStream_t>(stream)), "combine_backward");
+}
+
+static quads_status_t orthogonalize_shape(int64_t batch, int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || rows % 16 || cols % 16)
+    return fail(QUADS_ERR_SHAPE, "orthogonalize: rows and cols must be positive multiples of 16");
+  if (rows >= (1 << 20) || cols >= (1 << 20)) return fail(QUADS_ERR_SHAPE, "orthogonalize: rows and cols must be below 2^20");
+  if (batch < 0 || batch > 65535) return fail(QUADS_ERR_SHAPE, "orthogonalize: batch must be in [0, 65535]");
+  const int64_t widest = rows > cols ? rows : cols;
+  if (!mul_ok(batch * widest, widest, kMaxElems)) return fail(QUADS_ERR_SHAPE, "orthogonalize: size overflow");
+  return QUADS_OK;
+}
+
+size_t quads_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+  if (orthogonalize_shape(batch, rows, cols) != QUADS_OK || batch == 0) return 0;
+  return quads::orthogonalize_ws_bytes(batch, rows, cols);
+}
+
+quads_status_t quads_orthogonalize(const void *g, quads_dtype_t dt, int64_t batch, int64_t rows, int64_t cols,
+                                   int32_t steps, const float coefficients[3], float eps, void *out_bf16, void *ws,
+                                   size_t ws_bytes, void *stream) {
+  if (!float_type(dt)) return fail(QUADS_ERR_ARG, "orthogonalize: bad dtype %d", dt);
+  const quads_status_t st = orthogonalize_shape(batch, rows, cols);
+  if (st != QUADS_OK) return st;
+  if (steps < 1 || steps > 64) return fail(QUADS_ERR_ARG, "orthogonalize: steps must be in [1, 64]");
+  if (!coefficients) return fail(QUADS_ERR_ARG, "orthogonalize: null coefficients");
+  if (!(eps >= 0.0f)) return fail(QUADS_ERR_ARG, "orthogonalize: eps must not be negative");
+  if (misaligned({g, out_bf16, ws})) return fail(QUADS_ERR_ARG, "orthogonalize: arrays must be 16-byte aligned");
+  if (batch == 0) return ok();
+  if (!g || !out_bf16) return fail(QUADS_ERR_ARG, "orthogonalize: null pointer");
+  const size_t need = quads::orthogonalize_ws_bytes(batch, rows, cols);
+  if (ws == nullptr || ws_bytes < need)
+    return fail(QUADS_ERR_WORKSPACE, "orthogonalize: workspace too small (need %zu)", need);
+  quads::OrthogonalLaunch o{};
+  o.g = g;
+  o.g_f32 = dt == QUADS_F32;
+  o.batch = batch;
+  o.rows = rows;
+  o.cols = cols;
+  o.steps = steps;
+  o.a = coefficients[0];
+  o.b = coefficients[1];
+  o.c = coefficients[2];
+  o.eps = eps;
+  o.out = static_cast<uint16_t *>(out_bf16);
+  o.ws = ws;
+  return device_status(quads::launch_orthogonalize(o, static_cast<hipStream_t>(stream)), "orthogonalize");
 }
 
 }  // extern "C"

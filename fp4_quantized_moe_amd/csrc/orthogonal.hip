@@ -1,0 +1,211 @@
+// Orthogonalised updates by Newton-Schulz products on gfx950: for each matrix
+//   X = G / (|G|_F + eps),   then `steps` times   A = X X^T,  B = b A + c A^2,
+//   X <- a X + B X   (X <- a X + X B with A = X^T X where G has more rows than
+// columns), which moves every singular value s by s (a + b s^2 + c s^4) and
+// leaves the singular vectors.
+//
+// Precision.  Products take fp16 operands (11 significant bits, the matrix
+// cores' rate is bf16's) and add in fp32.  X itself is kept as a sum hi + lo of
+// two fp16 values (22 bits): hi enters the products, hi + lo the term a X.  A
+// rounding of X is noise in all directions, also in those that G lacks (an
+// expert that saw few tokens has a gradient of low rank), where each further
+// step multiplies it by a: 3.4445^5 = 485 times for X's first rounding.  Without
+// lo an update of rank 16 in 256 is off by 4%, with it by 0.06%; noise in A and B
+// only enters multiplied by X.  Power-of-two scales keep the values in fp16's
+// normal range: X times 2^11, A and B times 2^10.
+//
+// Bound: the matrix cores, 3 m^2 n + m^3 operations a step for the short side m
+// and the long side n: A and A^2 are symmetric, and only tiles on and below the
+// diagonal are computed; each is stored a second time transposed.
+#include <algorithm>
+
+#include "batched_tile.hpp"
+#include "orthogonal_launch.hpp"
+
+namespace quads {
+namespace {
+
+constexpr float kXScale = 2048.0f, kAScale = 1024.0f;
+
+// ---- normalisation -------------------------------------------------------------
+
+constexpr int kNormThreads = 256;
+constexpr int kMostParts = 64;  // partial sums of a matrix: folded by a wave
+
+struct SplitParams {
+  const void *g;
+  bool f32;
+  int64_t units;  // of 8 elements, of a matrix
+  double eps;
+  double *partial;  // [batch, parts]
+  uint16_t *hi, *lo;
+};
+
+__device__ __forceinline__ void load_values(const SplitParams &p, int64_t unit, float (&v)[8]) {
+  if (p.f32) {
+    const float4 *q = static_cast<const float4 *>(p.g) + 2 * unit;
+    const float4 a = q[0], b = q[1];
+    const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = w[i];
+  } else {
+    const uint4 r = static_cast<const uint4 *>(p.g)[unit];
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+// Part blockIdx.x of matrix blockIdx.y's sum of squares, in 64 bits: squares of
+// fp32 neither overflow nor vanish.
+__global__ __launch_bounds__(kNormThreads) void k_square_sums(SplitParams p) {
+  __shared__ double parts[kNormThreads / 64];
+  const int64_t per = (p.units + gridDim.x - 1) / gridDim.x, base = blockIdx.y * p.units;
+  const int64_t end = min(p.units, (blockIdx.x + 1) * per);
+  double s = 0.0;
+  for (int64_t u = blockIdx.x * per + threadIdx.x; u < end; u += kNormThreads) {
+    float v[8];
+    load_values(p, base + u, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += static_cast<double>(v[i]) * static_cast<double>(v[i]);
+  }
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    p.partial[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = ((parts[0] + parts[1]) + parts[2]) + parts[3];
+}
+
+// The matrix divided by its norm, as hi + lo.
+__global__ __launch_bounds__(kNormThreads) void k_split(SplitParams p) {
+  const int lane = threadIdx.x & 63, parts = static_cast<int>(gridDim.x);
+  const double ss = wave_sum(lane < parts ? p.partial[static_cast<int64_t>(blockIdx.y) * parts + lane] : 0.0);
+  const double scale = static_cast<double>(kXScale) / (sqrt(ss) + p.eps);
+  const int64_t per = (p.units + gridDim.x - 1) / gridDim.x, base = blockIdx.y * p.units;
+  const int64_t end = min(p.units, (blockIdx.x + 1) * per);
+  for (int64_t u = blockIdx.x * per + threadIdx.x; u < end; u += kNormThreads) {
+    float v[8], lo[8];
+    load_values(p, base + u, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(v[i] * scale);
+    split_f16(v, lo);
+    reinterpret_cast<uint4 *>(p.hi)[base + u] = make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+    reinterpret_cast<uint4 *>(p.lo)[base + u] = make_uint4(pack_f16(lo[0], lo[1]), pack_f16(lo[2], lo[3]), pack_f16(lo[4], lo[5]), pack_f16(lo[6], lo[7]));
+  }
+}
+
+int parts_of(int64_t units) { return static_cast<int>(std::min<int64_t>((units + 1023) / 1024, kMostParts)); }
+
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// The workspace: for every matrix of a pass hi twice (a step reads one and
+// writes the other), lo, A and B; partial sums.
+struct Layout {
+  int64_t hi[2], lo, a, b, partial, bytes;
+};
+
+Layout layout(int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t m = std::min(rows, cols), x = up256(2 * batch * rows * cols), s = up256(2 * batch * m * m);
+  Layout l{};
+  l.hi[0] = 0;
+  l.hi[1] = x;
+  l.lo = 2 * x;
+  l.a = 3 * x;
+  l.b = l.a + s;
+  l.partial = l.b + s;
+  l.bytes = l.partial + up256(8 * batch * parts_of(rows * cols / 8));
+  return l;
+}
+
+}  // namespace
+
+size_t orthogonalize_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
+  return static_cast<size_t>(layout(batch, rows, cols).bytes);
+}
+
+hipError_t launch_orthogonalize(const OrthogonalLaunch &o, hipStream_t stream) {
+  const int64_t rows = o.rows, cols = o.cols, m = std::min(rows, cols), n = std::max(rows, cols);
+  const bool tall = rows > cols;
+  const Layout l = layout(o.batch, rows, cols);
+  uint8_t *ws = static_cast<uint8_t *>(o.ws);
+  const auto at = [&](int64_t offset) { return reinterpret_cast<uint16_t *>(ws + offset); };
+
+  const SplitParams s{o.g, o.g_f32, rows * cols / 8, o.eps, reinterpret_cast<double *>(ws + l.partial), at(l.hi[0]), at(l.lo)};
+  const dim3 parts(parts_of(s.units), static_cast<unsigned>(o.batch));
+  hipLaunchKernelGGL(k_square_sums, parts, dim3(kNormThreads), 0, stream, s);
+  hipLaunchKernelGGL(k_split, parts, dim3(kNormThreads), 0, stream, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+
+  BatchedParams gram{};  // A = X X^T or X^T X
+  gram.batch = static_cast<int32_t>(o.batch);
+  gram.M = gram.N = static_cast<int32_t>(m);
+  gram.chunks = static_cast<int32_t>(n / 8);
+  gram.x_row = gram.w_row = 2 * cols;
+  gram.x_mat = gram.w_mat = 2 * rows * cols;
+  gram.out = at(l.a);
+  gram.alpha = kAScale / (kXScale * kXScale);
+
+  BatchedParams poly = gram;  // B = b A + c A A
+  poly.chunks = static_cast<int32_t>(m / 8);
+  poly.x = poly.w = ws + l.a;
+  poly.x_row = poly.w_row = 2 * m;
+  poly.x_mat = poly.w_mat = 2 * m * m;
+  poly.in = at(l.a);
+  poly.out = at(l.b);
+  poly.alpha = o.c / kAScale;
+  poly.beta = o.b;
+
+  BatchedParams next = poly;  // X <- a X + B X or a X + X B
+  next.M = static_cast<int32_t>(rows);
+  next.N = static_cast<int32_t>(cols);
+  next.in2 = next.out2 = at(l.lo);
+  next.alpha = 1.0f / kAScale;
+  next.beta = o.a;
+
+  for (int step = 0; step < o.steps; ++step) {
+    const uint8_t *x = ws + l.hi[step & 1];
+    gram.x = gram.w = x;
+    e = tall ? launch_batched<true, true, kEpiGram>(gram, stream) : launch_batched<false, false, kEpiGram>(gram, stream);
+    if (e != hipSuccess) return e;
+    e = launch_batched<false, false, kEpiPoly>(poly, stream);
+    if (e != hipSuccess) return e;
+    const bool last = step + 1 == o.steps;
+    next.in = reinterpret_cast<const uint16_t *>(x);
+    next.out = last ? o.out : at(l.hi[(step + 1) & 1]);
+    if (last) {
+      next.alpha /= kXScale;
+      next.beta /= kXScale;
+    }
+    if (tall) {  // rows of X against rows of B, which is symmetric
+      next.x = x;
+      next.x_row = 2 * cols;
+      next.x_mat = 2 * rows * cols;
+      next.w = ws + l.b;
+      next.w_row = 2 * m;
+      next.w_mat = 2 * m * m;
+      e = last ? launch_batched<false, false, kEpiLast>(next, stream) : launch_batched<false, false, kEpiNext>(next, stream);
+    } else {  // rows of B against columns of X
+      next.x = ws + l.b;
+      next.x_row = 2 * m;
+      next.x_mat = 2 * m * m;
+      next.w = x;
+      next.w_row = 2 * cols;
+      next.w_mat = 2 * rows * cols;
+      e = last ? launch_batched<false, true, kEpiLast>(next, stream) : launch_batched<false, true, kEpiNext>(next, stream);
+    }
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace quads

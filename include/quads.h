@@ -668,6 +668,35 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
                                           const int32_t *inverse, const float *topk_w, int64_t T, int32_t top, int64_t N,
                                           void *dy_bf16, float *dw, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * quads_orthogonalize -- what the trainer does with a gradient (or momentum)
+ * of the masters before they move: each of `batch` matrices g [rows, cols] (F32
+ * or BF16; of stacked gate and up masters, each its own matrix) is brought
+ * near the orthogonal matrix with its singular vectors by Newton-Schulz
+ * products,
+ *   X = g / (|g|_F + eps),
+ *   `steps` times  X <- a X + (b A + c A^2) X  with A = X X^T
+ * (for rows > cols the same from the right, with X^T X), and written as bf16
+ * to out [batch, rows, cols].  |g|_F is summed in 64 bits.  The products take
+ * fp16 operands and add in fp32; X is kept to 22 bits between the steps, so
+ * the result is within about 2e-3 of the formula's (relative, 2-norm) before
+ * its rounding to bf16, also for matrices of low rank.  coefficients: the
+ * host's a, b, c.  Entries of X, A and b A + c A^2 have to stay below 31, 63
+ * and 63 (they are below 5 for coefficients that keep the singular values
+ * below 1.3, as 3.4445, -4.775, 2.0315 do); past that they become infinities
+ * and NaN.  A matrix with NaN or infinities gives NaN throughout, one of zeros
+ * zeros (NaN with eps 0).
+ * rows and cols are multiples of 16, below 2^20; batch <= 65535; 1 <= steps <=
+ * 64.  ws: quads_orthogonalize_workspace_bytes(batch, rows, cols) bytes; calls
+ * in flight at the same time need a workspace each.  The order of every sum is
+ * fixed: repeated calls give the same bits, and matrices of a call do not touch
+ * each other; between calls of different sizes the last bits may differ.  batch == 0: nothing is launched.
+ * ------------------------------------------------------------------------- */
+size_t quads_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+quads_status_t quads_orthogonalize(const void *g, quads_dtype_t dt, int64_t batch, int64_t rows, int64_t cols,
+                                   int32_t steps, const float coefficients[3], float eps, void *out_bf16, void *ws,
+                                   size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

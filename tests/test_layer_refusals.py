@@ -136,3 +136,26 @@ def test_binding_refuses_cpu_tensors():
             call()
     with pytest.raises(Q.QuadsError):
         Q.rms_norm(torch.zeros(4, 64, dtype=torch.float16), h[0])
+
+
+@pytest.mark.parametrize("kw, status, word", [
+    (dict(dt=2), ARG, b"dtype"), (dict(rows=0), SHAPE, b"multiples of 16"), (dict(cols=40), SHAPE, b"multiples of 16"),
+    (dict(rows=1 << 20), SHAPE, b"below 2^20"), (dict(batch=-1), SHAPE, b"batch"), (dict(batch=65536), SHAPE, b"batch"),
+    (dict(batch=60000, rows=16, cols=(1 << 20) - 16), SHAPE, b"overflow"), (dict(steps=0), ARG, b"steps"),
+    (dict(steps=65), ARG, b"steps"), (dict(co=None), ARG, b"coefficients"), (dict(eps=-1e-9), ARG, b"eps"),
+    (dict(g=8), ARG, b"aligned"), (dict(g=None), ARG, b"null"), (dict(out=None), ARG, b"null"),
+    (dict(ws=None), WORKSPACE, b"workspace"), (dict(nws=1000), WORKSPACE, b"workspace"),
+])
+def test_orthogonalize(L, kw, status, word):
+    d = dict(g=P, dt=0, batch=2, rows=32, cols=48, steps=5, co=(ctypes.c_float * 3)(3.4, -4.8, 2.0), eps=1e-7, out=P, ws=P,
+             nws=1 << 20, stream=None)
+    assert L.quads_orthogonalize(*{**d, **kw}.values()) == status
+    assert word in L.quads_last_error()
+
+
+def test_orthogonalize_without_matrices(L):
+    f = L.quads_orthogonalize_workspace_bytes
+    assert f(2, 32, 48) >= 2 * (3 * 32 * 48 + 2 * 32 * 32) * 2 and f(0, 32, 48) == 0 and f(2, 24, 48) == 0
+    assert L.quads_orthogonalize(None, 0, 0, 32, 48, 5, (ctypes.c_float * 3)(1, 1, 1), 0.0, None, None, 0, None) == 0
+    with pytest.raises(Q.QuadsError, match="contiguous and on the GPU"):
+        Q.orthogonalize(torch.zeros(32, 32))
