@@ -2,11 +2,22 @@
 // for each, with the epilogues of a Newton-Schulz step.  Either operand may be
 // stored with the contraction along its rows (X as [K, M], W as [K, N]).
 //
-// Stages, swizzles, fragment reads and the pipeline are those of
-// grouped_staged.hpp (its comments say why); what differs: fp16, every matrix
-// of the same size, either operand by transposing reads, and symmetric
-// results, of which only the tiles on and below the diagonal are computed and
-// those below it stored twice.
+// Stages and pipeline are those of grouped_staged.hpp (its comments say why).
+// What differs: fp16; every matrix of the same size; either operand by
+// transposing reads; symmetric results, of which only the tiles on and below
+// the diagonal are computed and those below it stored twice; and the way out.
+//
+// A step's epilogue reads and writes more bytes than its stages bring (X comes
+// in as hi and lo and leaves as both), so it takes no turn through LDS: X's
+// rows are MFMA's first operand and W's the second, so a lane holds one column
+// of 16 rows, and the columns are dealt to lanes and fragments so that a
+// lane's V fragments of a row are V neighbours (V = 4 with the large tile).  A
+// wave's access is then two rows of 256 bytes, 8 a lane.  Where W's rows are
+// staged, that is a permutation of the rows that the DMA fetches; where its
+// columns are, the transposing reads give a quad of lanes 4 neighbouring
+// columns of every fragment, and a 4 x 4 transpose inside the quad follows.
+// X's rows are dealt so that a lane's 16 are neighbours too: 32 bytes of a row
+// of the transposed tile.
 #pragma once
 
 #include "grouped_staged.hpp"
@@ -25,12 +36,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, p);
 }
 
-__device__ __forceinline__ void unpack_f16(uint32_t w, float &lo, float &hi) {
-  const f16x2 p = __builtin_bit_cast(f16x2, w);
-  lo = static_cast<float>(p[0]);
-  hi = static_cast<float>(p[1]);
-}
-
 // lo = v less its fp16 rounding (exact in fp32).
 template <int N>
 __device__ __forceinline__ void split_f16(const float (&v)[N], float (&lo)[N]) {
@@ -38,11 +43,19 @@ __device__ __forceinline__ void split_f16(const float (&v)[N], float (&lo)[N]) {
   for (int i = 0; i < N; ++i) lo[i] = v[i] - static_cast<float>(static_cast<_Float16>(v[i]));
 }
 
+// fp16(a - x.lo), fp16(b - x.hi): the differences are exact in fp32.
+__device__ __forceinline__ uint32_t residual_f16(uint32_t x, float a, float b) {
+  uint32_t d;
+  asm("v_fma_mixlo_f16 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(d) : "v"(x), "v"(a));
+  asm("v_fma_mixhi_f16 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "+v"(d) : "v"(x), "v"(b));
+  return d;
+}
+
 enum BatchedEpi {
   kEpiGram = 0,  // out = alpha Y, symmetric
   kEpiPoly = 1,  // out = beta in + alpha Y, symmetric
-  kEpiNext = 2,  // v = beta (in + in2) + alpha Y; out = fp16(v), out2 = fp16(v - out)
-  kEpiLast = 3   // out = bf16(beta (in + in2) + alpha Y)
+  kEpiNext = 2,  // v = beta (in + in2) + Y; out = fp16(v), out2 = fp16(v - out)
+  kEpiLast = 3   // out = bf16(alpha (beta (in + in2) + Y))
 };
 
 struct BatchedParams {
@@ -64,35 +77,78 @@ struct BatchedCfg {
   static constexpr int LOADS = TILE / 16;              // staging instructions of a wave and stage, both operands
   static constexpr int LATE = LOADS * 3 / 4;
   static constexpr int KROWS = 512 / TILE;             // transposed operand: stored rows of an instruction
-  static constexpr int TURN = 2 * STAGE, TURN_BYTES = 32 * 128;
-  static constexpr int LDS = TURN + 4 * TURN_BYTES;
+  static constexpr int LDS = 2 * STAGE;
+  // Position p of 32 (a lane of a fragment, or a row of the accumulators) and
+  // fragment t of a wave's half tile -> column or row inside the half.
+  // W by rows: lane p of fragment t has column MI p + t.  W by columns: in
+  // units of 4 columns, unit p / 4 of fragment t is 2 MI (p / 8) + 2 t + p / 4 % 2
+  // (two units lie in one 16-byte chunk).  X: position 8 q + 4 h + r (lanes of
+  // half h, register 4 q + r) is row 16 h + 4 q + r.
+  static __device__ __forceinline__ int w_row(int p, int t) { return MI * p + t; }
+  static __device__ __forceinline__ int w_unit(int p4, int t) { return 2 * MI * (p4 >> 1) + 2 * t + (p4 & 1); }
+  static __device__ __forceinline__ int x_unit(int p4) { return 4 * (p4 & 1) + (p4 >> 1); }
+  // Slot of a chunk of a transposed stage is chunk ^ slot(k): the four rows k
+  // that a group of 16 lanes reads lie in different banks than its units.
+  static __device__ __forceinline__ int w_slot(int k) { return MI == 4 ? k & 3 : (k & 1) | ((k & 2) << 2); }
+  static __device__ __forceinline__ int x_slot(int k) { return (k & 3) << 2; }
 };
 
-// One 32 x 32 tile as fp16 columns [32 i, 32 i + 32) of a turned-around block of 32 rows of 64.
-__device__ __forceinline__ void turn_put_f16(uint8_t *turn, int lane, int i, const float (&v)[16]) {
-  const int half = lane >> 5, fr = lane & 31;
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    *reinterpret_cast<uint2 *>(turn + turn_at<128>(fr, 4 * i + q) + 8 * half) =
-        make_uint2(pack_f16(v[4 * q], v[4 * q + 1]), pack_f16(v[4 * q + 2], v[4 * q + 3]));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// V neighbouring fp16 (or bf16) values of a row, in V / 2 dwords.
+template <int V>
+struct Neighbours {
+  uint32_t w[V / 2];
+};
+template <int V>
+__device__ __forceinline__ Neighbours<V> load_neighbours(const uint8_t *p) {
+  Neighbours<V> n;
+  if constexpr (V == 4) {
+    const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+    n.w[0] = v[0];
+    n.w[1] = v[1];
+  } else {
+    n.w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+  return n;
+}
+template <int V>
+__device__ __forceinline__ void store_neighbours(uint8_t *p, const Neighbours<V> &n) {
+  if constexpr (V == 4) *reinterpret_cast<u32x2 *>(p) = u32x2{n.w[0], n.w[1]};
+  else *reinterpret_cast<uint32_t *>(p) = n.w[0];
 }
 
-// Its transpose, as columns [32 i, 32 i + 32) of the block.
-__device__ __forceinline__ void turn_put_f16_t(uint8_t *turn, int lane, int i, const f32x16 &v) {
-  const int half = lane >> 5, col = 32 * i + (lane & 31);
-#pragma unroll
-  for (int r = 0; r < 16; ++r)
-    *reinterpret_cast<_Float16 *>(turn + turn_at<128>(8 * (r >> 2) + 4 * half + (r & 3), col >> 3) + 2 * (col & 7)) =
-        static_cast<_Float16>(v[r]);
+template <int CTRL>
+__device__ __forceinline__ float quad_move(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
 }
 
-__device__ __forceinline__ void turn_get_f16(const uint8_t *turn, int lane, int i, float (&v)[16]) {
-  const int half = lane >> 5, fr = lane & 31;
+// v[t] of lane c of a quad -> V neighbours: column 4 t + c becomes lane c's
+// column V c + e (V = 4: the 4 x 4 transpose; V = 2: lane c takes two of
+// fragment c / 2).
+template <int V>
+__device__ __forceinline__ void quad_transpose(float (&v)[V], int lane) {
+  if constexpr (V == 4) {
+    const bool odd = lane & 1, high = lane & 2;
+    float w[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(turn + turn_at<128>(fr, 4 * i + q) + 8 * half);
-    unpack_f16(w.x, v[4 * q], v[4 * q + 1]);
-    unpack_f16(w.y, v[4 * q + 2], v[4 * q + 3]);
+    for (int t = 0; t < 4; t += 2) {
+      const float a = quad_move<0xB1>(v[t]), b = quad_move<0xB1>(v[t + 1]);  // lane ^ 1
+      w[t] = odd ? b : v[t];
+      w[t + 1] = odd ? v[t + 1] : a;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float a = quad_move<0x4E>(w[t]), b = quad_move<0x4E>(w[t + 2]);  // lane ^ 2
+      v[t] = high ? b : w[t];
+      v[t + 2] = high ? w[t + 2] : a;
+    }
+  } else {
+    const bool high = lane & 2;
+    const float a0 = quad_move<0x88>(v[0]), a1 = quad_move<0xDD>(v[0]);  // lanes 0 2 0 2, 1 3 1 3
+    const float b0 = quad_move<0x88>(v[1]), b1 = quad_move<0xDD>(v[1]);
+    v[0] = high ? b0 : a0;
+    v[1] = high ? b1 : a1;
   }
 }
 
@@ -139,7 +195,7 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
   const auto aim = [&](const BatchedTile &u) {
     const int lane = fresh_lane(), lr = lane >> 3, chunk = (lane & 7) ^ ((4 * wave + (lr >> 1)) & 7);
     const int wk = wave * C::KROWS + lane / (64 / C::KROWS);
-    const int tc = 8 * ((lane % (64 / C::KROWS)) ^ ((wk & 3) << 2));
+    const int slot = lane % (64 / C::KROWS);
     const uint8_t *we = p.w + u.e * p.w_mat, *xe = p.x + u.e * p.x_mat;
 #pragma unroll
     for (int j = 0; j < C::LOADS; ++j) {
@@ -148,10 +204,14 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
       const int64_t stride = weight ? p.w_row : p.x_row;
       const int32_t first = weight ? u.n0 : u.m0, size = weight ? p.N : p.M;
       const int jj = weight ? j : j - WL;
-      if (weight ? C::WT : C::XT)
-        from[j] = base + (wk + jj * 4 * C::KROWS) * stride + 2 * min(first + tc, size - 8);
-      else
-        from[j] = base + min(first + (jj * 4 + wave) * 8 + lr, size - 1) * stride + 16 * chunk;
+      if (weight ? C::WT : C::XT) {
+        const int column = first + 8 * (slot ^ (weight ? C::w_slot(wk) : C::x_slot(wk)));
+        from[j] = base + (wk + jj * 4 * C::KROWS) * stride + 2 * min(column, size - 8);
+      } else {
+        const int r = (jj * 4 + wave) * 8 + lr, part = r & ~(C::HALF - 1), t = r % C::HALF / 32, q = r & 31;
+        const int row = first + part + (weight ? C::w_row(q, t) : 32 * t + 4 * C::x_unit(q >> 2) + (q & 3));
+        from[j] = base + min(row, size - 1) * stride + 16 * chunk;
+      }
     }
   };
   const auto fetch_one = [&](int s, uint8_t *base, auto jc) {
@@ -168,19 +228,17 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
 
   // Fragment addresses inside an operand's part of a stage.
   const int fr = lane & 31;
-  const auto column = [&](int first) {  // of a transposed operand: of the 32 columns from `first` on
-    const int j = (lane >> 2) & 3;
-    const int c = first / 8 + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
-    return (32 * half + j) * (2 * C::TILE) + 16 * (c ^ (j << 2)) + 8 * (lane & 1);
-  };
+  // Lane 16 g + 4 j + b of a transposing read addresses row j and unit 4 (g % 2) + b
+  // of the fragment's 8, in half g / 2.
   int wcol[C::WT ? C::MI : 1], xcol[C::XT ? C::MI : 1];
-  if constexpr (C::WT) {
+  {
+    const int j = (lane >> 2) & 3, unit = 4 * ((lane >> 4) & 1) + (lane & 3);
 #pragma unroll
-    for (int i = 0; i < C::MI; ++i) wcol[i] = column(wn * C::HALF + 32 * i);
-  }
-  if constexpr (C::XT) {
-#pragma unroll
-    for (int i = 0; i < C::MI; ++i) xcol[i] = column(wm * C::HALF + 32 * i);
+    for (int i = 0; i < C::MI; ++i) {
+      const int wu = wn * (C::HALF / 4) + C::w_unit(unit, i), xu = wm * (C::HALF / 4) + 8 * i + C::x_unit(unit);
+      if constexpr (C::WT) wcol[i] = (32 * half + j) * (2 * C::TILE) + 16 * ((wu >> 1) ^ C::w_slot(j)) + 8 * (wu & 1);
+      if constexpr (C::XT) xcol[i] = (32 * half + j) * (2 * C::TILE) + 16 * ((xu >> 1) ^ C::x_slot(j)) + 8 * (xu & 1);
+    }
   }
   struct Frag {
     uint4 a[C::MI], b[C::MI];
@@ -212,7 +270,7 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
     constexpr int READS = 2 * C::MI, RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
     each<SLOTS>([&](auto slot) {
       constexpr int n = decltype(slot)::value, i = n / C::MI, k = n % C::MI;
-      acc[i][k] = mfma_f16(f.a[i], f.b[k], acc[i][k]);
+      acc[i][k] = mfma_f16(f.b[k], f.a[i], acc[i][k]);
       each<RPS>([&](auto q) {
         constexpr int r = n * RPS + decltype(q)::value;
         if constexpr (r < READS) read_item(g, gbase, gs, std::integral_constant<int, r>{});
@@ -272,100 +330,130 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
     stage(0, 1, [] {});
     pin();
 
-    // ---- the tile's results, a block of 32 rows and 64 columns at a time
-    uint8_t *turn = lds + C::TURN + wave * C::TURN_BYTES;
-    const int fl = fresh_lane();
+    // ---- the tile's results, 4 registers' rows of all fragments at a time
+    constexpr int V = C::MI, GROUPS = 4 * C::MI, AHEAD = 3;  // group g: row fragment g / 4, registers 4 (g % 4) ..
+    const int fl = fresh_lane(), fh = fl >> 5, fp = fl & 31;
     const int32_t wm0 = t.m0 + wm * C::HALF, wn0 = t.n0 + wn * C::HALF;
-    const int64_t mat = static_cast<int64_t>(t.e) * p.M * p.N, stride = 2 * static_cast<int64_t>(p.N);
+    // The lane's V columns.
+    const int32_t col = wn0 + (!C::WT ? V * fp
+                               : V == 4 ? 4 * C::w_unit(fp >> 2, fp & 3)
+                                        : 4 * C::w_unit(fp >> 2, (fp >> 1) & 1) + 2 * (fp & 1));
+    const bool col_ok = col < p.N;
+    const uint32_t at_col = 2 * static_cast<uint32_t>(col_ok ? col : 0);
+    // Addresses are a uniform row (in scalar registers) and the lane's offset
+    // from it: its columns, and 16 rows with half 1.  A row fragment's halves
+    // lie inside the matrix or behind it (sizes are multiples of 16); lanes
+    // behind it read other rows, and store nothing.  No branch around loads:
+    // where paths with different numbers of loads meet, the compiler can only
+    // wait for all of them, also for those sent ahead.
+    const int64_t stride = 2 * static_cast<int64_t>(p.N);
+    const int64_t matrix = 2 * static_cast<int64_t>(t.e) * p.M * p.N;
+    const auto rows_left = [&](int k) { return p.M - (wm0 + 32 * k); };
+    const auto offset = [&](int k) {
+      return at_col + (fh != 0 && rows_left(k) > 16 ? 16 * static_cast<uint32_t>(stride) : 0u);
+    };
+    // Byte of a group's first row.  Made where the compiler does not see it
+    // before: it would compute all groups' at once and has no registers for them.
+    const auto group_at = [&](int g) -> int64_t {
+      int32_t row = min(wm0 + 32 * (g / 4), p.M - 16) + 4 * (g % 4);
+      asm volatile("" : "+s"(row));
+      return matrix + row * stride;
+    };
+    struct Group {
+      Neighbours<V> in[4], in2[4];
+    };
+    Group ring[AHEAD + 1];
+    const auto load_group = [&](Group &u, int g) {
+      if constexpr (EPI != kEpiGram) {
+        const uint32_t lane_at = offset(g / 4);
+        const int64_t at = group_at(g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          u.in[r] = load_neighbours<V>(reinterpret_cast<const uint8_t *>(p.in) + (at + r * stride) + lane_at);
+          if constexpr (EPI == kEpiNext || EPI == kEpiLast)
+            u.in2[r] = load_neighbours<V>(reinterpret_cast<const uint8_t *>(p.in2) + (at + r * stride) + lane_at);
+        }
+      }
+    };
+    each<AHEAD>([&](auto gc) { load_group(ring[decltype(gc)::value], decltype(gc)::value); });
     const bool mirror = SYM && t.m0 != t.n0;
-    each<C::MI / 2>([&](auto kp) {
-      constexpr int k0 = 2 * decltype(kp)::value;
-      each<C::MI / 2>([&](auto ip) {
-        constexpr int i0 = 2 * decltype(ip)::value;
-        const int32_t n = wn0 + 32 * i0;
-        each<2>([&](auto kk) {
-          constexpr int k = k0 + decltype(kk)::value;
-          const int32_t row = wm0 + 32 * k;
-          const int rows = p.M - row, limit_bytes = 2 * (p.N - n);
-          const int64_t first = mat + static_cast<int64_t>(row) * p.N + n;
-          float v[2][16];
+    each<GROUPS>([&](auto gc) {
+      constexpr int g = decltype(gc)::value, k = g / 4, r0 = 4 * (g % 4);
+      if constexpr (g + AHEAD < GROUPS) load_group(ring[(g + AHEAD) % (AHEAD + 1)], g + AHEAD);
+      __builtin_amdgcn_sched_barrier(0);
+      {
+        const Group &u = ring[g % (AHEAD + 1)];
+        Neighbours<V> out[4], out2[4];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            asm volatile("" : "+a"(acc[i0 + q][k]));  // not read before its turn
+        for (int r = 0; r < 4; ++r) {
+          float v[V];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) v[q][r] = p.alpha * acc[i0 + q][k][r];
+          for (int i = 0; i < V; ++i) {
+            v[i] = acc[i][k][r0 + r];
+            if constexpr (SYM) v[i] *= p.alpha;
           }
-          if (rows > 0 && limit_bytes > 0) {
+          if constexpr (C::WT) quad_transpose<V>(v, fl);
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
             if constexpr (EPI != kEpiGram) {
-              TurnLoad<128> in, in2;
-              in.load(reinterpret_cast<const uint8_t *>(p.in + first), fl, stride, rows, limit_bytes);
-              if constexpr (EPI != kEpiPoly) in2.load(reinterpret_cast<const uint8_t *>(p.in2 + first), fl, stride, rows, limit_bytes);
-              float w[2][16];
-              in.put(turn, fl);
-#pragma unroll
-              for (int q = 0; q < 2; ++q) turn_get_f16(turn, fl, q, w[q]);
-              if constexpr (EPI != kEpiPoly) {
-                in2.put(turn, fl);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  float lo[16];
-                  turn_get_f16(turn, fl, q, lo);
-#pragma unroll
-                  for (int r = 0; r < 16; ++r) w[q][r] += lo[r];
-                }
-              }
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) v[q][r] = __builtin_fmaf(p.beta, w[q][r], v[q][r]);
+              const f16x2 x = __builtin_bit_cast(f16x2, u.in[r].w[i / 2]);
+              v[i] = __builtin_fmaf(static_cast<float>(x[0]), p.beta, v[i]);
+              v[i + 1] = __builtin_fmaf(static_cast<float>(x[1]), p.beta, v[i + 1]);
+            }
+            if constexpr (EPI == kEpiNext || EPI == kEpiLast) {
+              const f16x2 x = __builtin_bit_cast(f16x2, u.in2[r].w[i / 2]);
+              v[i] = __builtin_fmaf(static_cast<float>(x[0]), p.beta, v[i]);
+              v[i + 1] = __builtin_fmaf(static_cast<float>(x[1]), p.beta, v[i + 1]);
             }
             if constexpr (EPI == kEpiLast) {
-#pragma unroll
-              for (int q = 0; q < 2; ++q) turn_put_bf16<128>(turn, fl, q, v[q]);
+              out[r].w[i / 2] = pack_bf16(p.alpha * v[i], p.alpha * v[i + 1]);
             } else {
-#pragma unroll
-              for (int q = 0; q < 2; ++q) turn_put_f16(turn, fl, q, v[q]);
-            }
-            turn_store<128>(turn, fl, reinterpret_cast<uint8_t *>(p.out + first), stride, rows, limit_bytes);
-            if constexpr (EPI == kEpiNext) {
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                float lo[16];
-                split_f16(v[q], lo);
-                turn_put_f16(turn, fl, q, lo);
-              }
-              turn_store<128>(turn, fl, reinterpret_cast<uint8_t *>(p.out2 + first), stride, rows, limit_bytes);
+              const f16x2 x = {static_cast<_Float16>(v[i]), static_cast<_Float16>(v[i + 1])};
+              out[r].w[i / 2] = __builtin_bit_cast(uint32_t, x);
+              if constexpr (EPI == kEpiNext) out2[r].w[i / 2] = residual_f16(out[r].w[i / 2], v[i], v[i + 1]);
             }
           }
+          if constexpr (EPI == kEpiPoly) {  // for the transposed tile
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            if constexpr (SYM) {
-#pragma unroll
-              for (int r = 0; r < 16; ++r) acc[i0 + q][k][r] = v[q][r];
-            } else {
-              acc[i0 + q][k] = f32x16{};
-            }
+            for (int i = 0; i < V; ++i) acc[i][k][r0 + r] = v[i];
           }
-          __builtin_amdgcn_sched_barrier(0);
-        });
-        if constexpr (SYM) {
-          // Columns n + 32 q .. of the 64 rows are rows of the transposed tile.
-          each<2>([&](auto qc) {
-            constexpr int q = decltype(qc)::value;
-            const int32_t row = wn0 + 32 * (i0 + q), col = wm0 + 32 * k0;
-            if (mirror) {
-              turn_put_f16_t(turn, fl, 0, acc[i0 + q][k0]);
-              turn_put_f16_t(turn, fl, 1, acc[i0 + q][k0 + 1]);
-              if (p.N > row && p.M > col)
-                turn_store<128>(turn, fl, reinterpret_cast<uint8_t *>(p.out + mat + static_cast<int64_t>(row) * p.N + col), stride,
-                                p.N - row, 2 * (p.M - col));
-            }
-            acc[i0 + q][k0] = f32x16{};
-            acc[i0 + q][k0 + 1] = f32x16{};
-            __builtin_amdgcn_sched_barrier(0);
-          });
         }
-      });
+        const uint32_t lane_at = offset(k);
+        if (col_ok && rows_left(k) > 16 * fh) {
+          const int64_t at = group_at(g);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            store_neighbours<V>(reinterpret_cast<uint8_t *>(p.out) + (at + r * stride) + lane_at, out[r]);
+            if constexpr (EPI == kEpiNext)
+              store_neighbours<V>(reinterpret_cast<uint8_t *>(p.out2) + (at + r * stride) + lane_at, out2[r]);
+          }
+        }
+      }
+      if constexpr (SYM && g % 4 == 3) {
+        if (mirror) {
+          const int32_t at_row = wm0 + 32 * k + 16 * fh;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {  // a lane's 16 rows of column i are neighbours in a row
+            const int32_t row = wn0 + (C::WT ? 4 * C::w_unit(fp >> 2, i) + (fp & 3) : C::w_row(fp, i));
+            if (row < p.N && at_row < p.M) {
+              uint32_t w[8];
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {
+                const float scale = EPI == kEpiGram ? p.alpha : 1.0f;
+                w[r] = pack_f16(scale * acc[i][k][2 * r], scale * acc[i][k][2 * r + 1]);
+              }
+              uint4 *to = reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(p.out) + matrix + row * stride + 2 * at_row);
+              to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+        }
+      }
+      if constexpr (g % 4 == 3) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i][k] = f32x16{};
+      }
+      __builtin_amdgcn_sched_barrier(0);
     });
     if (nt.e < 0) break;
     t = nt;

@@ -11,8 +11,9 @@
 // expert that saw few tokens has a gradient of low rank), where each further
 // step multiplies it by a: 3.4445^5 = 485 times for X's first rounding.  Without
 // lo an update of rank 16 in 256 is off by 4%, with it by 0.06%; noise in A and B
-// only enters multiplied by X.  Power-of-two scales keep the values in fp16's
-// normal range: X times 2^11, A and B times 2^10.
+// only enters multiplied by X.  Power-of-two scales keep X and A in fp16's
+// normal range: X times 2^11, A times 2^10.  B's entries below 2^-14 are rounded
+// by up to 2^-25 where B's norm is of the order of 1, or B X does not matter.
 //
 // Bound: the matrix cores, 3 m^2 n + m^3 operations a step for the short side m
 // and the long side n: A and A^2 are symmetric, and only tiles on and below the
@@ -162,14 +163,14 @@ hipError_t launch_orthogonalize(const OrthogonalLaunch &o, hipStream_t stream) {
   poly.x_mat = poly.w_mat = 2 * m * m;
   poly.in = at(l.a);
   poly.out = at(l.b);
-  poly.alpha = o.c / kAScale;
-  poly.beta = o.b;
+  poly.alpha = o.c / (kAScale * kAScale);
+  poly.beta = o.b / kAScale;
 
   BatchedParams next = poly;  // X <- a X + B X or a X + X B
   next.M = static_cast<int32_t>(rows);
   next.N = static_cast<int32_t>(cols);
   next.in2 = next.out2 = at(l.lo);
-  next.alpha = 1.0f / kAScale;
+  next.alpha = 1.0f / kXScale;
   next.beta = o.a;
 
   for (int step = 0; step < o.steps; ++step) {
@@ -182,10 +183,6 @@ hipError_t launch_orthogonalize(const OrthogonalLaunch &o, hipStream_t stream) {
     const bool last = step + 1 == o.steps;
     next.in = reinterpret_cast<const uint16_t *>(x);
     next.out = last ? o.out : at(l.hi[(step + 1) & 1]);
-    if (last) {
-      next.alpha /= kXScale;
-      next.beta /= kXScale;
-    }
     if (tall) {  // rows of X against rows of B, which is symmetric
       next.x = x;
       next.x_row = 2 * cols;

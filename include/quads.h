@@ -682,7 +682,7 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
  * the result is within about 2e-3 of the formula's (relative, 2-norm) before
  * its rounding to bf16, also for matrices of low rank.  coefficients: the
  * host's a, b, c.  Entries of X, A and b A + c A^2 have to stay below 31, 63
- * and 63 (they are below 5 for coefficients that keep the singular values
+ * and 65504 (they are below 5 for coefficients that keep the singular values
  * below 1.3, as 3.4445, -4.775, 2.0315 do); past that they become infinities
  * and NaN.  A matrix with NaN or infinities gives NaN throughout, one of zeros
  * zeros (NaN with eps 0).
