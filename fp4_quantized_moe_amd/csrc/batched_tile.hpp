@@ -2,10 +2,16 @@
 // for each, with the epilogues of a Newton-Schulz step.  Either operand may be
 // stored with the contraction along its rows (X as [K, M], W as [K, N]).
 //
-// Stages and pipeline are those of grouped_staged.hpp (its comments say why).
-// What differs: fp16; every matrix of the same size; either operand by
-// transposing reads; symmetric results, of which only the tiles on and below
-// the diagonal are computed and those below it stored twice; and the way out.
+// A stage is 32 of K of TILE rows of X and of W; four stages in LDS, brought by
+// DMA three stages before they are read.  Rows are 64 bytes; row r keeps its
+// chunk c in slot c ^ (r / 4 % 4), so that 16 rows of a fragment read take each
+// of the banks once.  (Two stages of 64, as in grouped_staged.hpp, are as fast
+// with many matrices and slower with few: one 1536 x 2048 361 against 324 us.)
+//
+// What differs from there besides: fp16; every matrix of the same size; either
+// operand by transposing reads; symmetric results, of which only the tiles on
+// and below the diagonal are computed and those below it stored twice; and the
+// way out.
 //
 // A step's epilogue reads and writes more bytes than its stages bring (X comes
 // in as hi and lo and leaves as both), so it takes no turn through LDS: X's
@@ -73,11 +79,11 @@ struct BatchedCfg {
   static constexpr int TILE = TILE_, HALF = TILE / 2;  // 2 x 2 waves
   static constexpr bool XT = XT_, WT = WT_;
   static constexpr int MI = HALF / 32;                 // 32 x 32 tiles of a wave, each way
-  static constexpr int STAGE = 2 * TILE * 128;
-  static constexpr int LOADS = TILE / 16;              // staging instructions of a wave and stage, both operands
-  static constexpr int LATE = LOADS * 3 / 4;
+  static constexpr int BUFFERS = 4;
+  static constexpr int STAGE = 2 * TILE * 64;          // 32 of K: 64 bytes of a row
+  static constexpr int LOADS = TILE / 32;              // staging instructions of a wave and stage, both operands
   static constexpr int KROWS = 512 / TILE;             // transposed operand: stored rows of an instruction
-  static constexpr int LDS = 2 * STAGE;
+  static constexpr int LDS = BUFFERS * STAGE;
   // Position p of 32 (a lane of a fragment, or a row of the accumulators) and
   // fragment t of a wave's half tile -> column or row inside the half.
   // W by rows: lane p of fragment t has column MI p + t.  W by columns: in
@@ -189,11 +195,11 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
   constexpr int WL = C::LOADS / 2;
   const uint8_t *from[C::LOADS];
   const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_chunk);
-  const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
+  const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
   const int wk = wave * C::KROWS + lane / (64 / C::KROWS);
   int32_t limit = p.chunks;  // 0: no tile, zeros are staged
   const auto aim = [&](const BatchedTile &u) {
-    const int lane = fresh_lane(), lr = lane >> 3, chunk = (lane & 7) ^ ((4 * wave + (lr >> 1)) & 7);
+    const int lane = fresh_lane(), lr = lane >> 2, chunk = (lane & 3) ^ ((lane >> 4) & 3);
     const int wk = wave * C::KROWS + lane / (64 / C::KROWS);
     const int slot = lane % (64 / C::KROWS);
     const uint8_t *we = p.w + u.e * p.w_mat, *xe = p.x + u.e * p.x_mat;
@@ -208,7 +214,7 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
         const int column = first + 8 * (slot ^ (weight ? C::w_slot(wk) : C::x_slot(wk)));
         from[j] = base + (wk + jj * 4 * C::KROWS) * stride + 2 * min(column, size - 8);
       } else {
-        const int r = (jj * 4 + wave) * 8 + lr, part = r & ~(C::HALF - 1), t = r % C::HALF / 32, q = r & 31;
+        const int r = (jj * 4 + wave) * 16 + lr, part = r & ~(C::HALF - 1), t = r % C::HALF / 32, q = r & 31;
         const int row = first + part + (weight ? C::w_row(q, t) : 32 * t + 4 * C::x_unit(q >> 2) + (q & 3));
         from[j] = base + min(row, size - 1) * stride + 16 * chunk;
       }
@@ -216,13 +222,13 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
   };
   const auto fetch_one = [&](int s, uint8_t *base, auto jc) {
     constexpr int j = decltype(jc)::value, jj = j < WL ? j : j - WL;
-    uint8_t *to = base + (j < WL ? 0 : C::TILE * 128) + (jj * 4 + wave) * 1024;
+    uint8_t *to = base + (j < WL ? 0 : C::TILE * 64) + (jj * 4 + wave) * 1024;
     if constexpr (j < WL ? C::WT : C::XT) {
-      dma_wave(64 * s + wk + jj * 4 * C::KROWS < 8 * limit ? from[j] : zero, to, 16);
-      from[j] += 64 * (j < WL ? p.w_row : p.x_row);
+      dma_wave(32 * s + wk + jj * 4 * C::KROWS < 8 * limit ? from[j] : zero, to, 16);
+      from[j] += 32 * (j < WL ? p.w_row : p.x_row);
     } else {
-      dma_wave(8 * s + chunk < limit ? from[j] : zero, to, 16);
-      from[j] += 128;
+      dma_wave(4 * s + chunk < limit ? from[j] : zero, to, 16);
+      from[j] += 64;
     }
   };
 
@@ -236,8 +242,8 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
 #pragma unroll
     for (int i = 0; i < C::MI; ++i) {
       const int wu = wn * (C::HALF / 4) + C::w_unit(unit, i), xu = wm * (C::HALF / 4) + 8 * i + C::x_unit(unit);
-      if constexpr (C::WT) wcol[i] = (32 * half + j) * (2 * C::TILE) + 16 * ((wu >> 1) ^ C::w_slot(j)) + 8 * (wu & 1);
-      if constexpr (C::XT) xcol[i] = (32 * half + j) * (2 * C::TILE) + 16 * ((xu >> 1) ^ C::x_slot(j)) + 8 * (xu & 1);
+      if constexpr (C::WT) wcol[i] = (8 * half + j) * (2 * C::TILE) + 16 * ((wu >> 1) ^ C::w_slot(j)) + 8 * (wu & 1);
+      if constexpr (C::XT) xcol[i] = (8 * half + j) * (2 * C::TILE) + 16 * ((xu >> 1) ^ C::x_slot(j)) + 8 * (xu & 1);
     }
   }
   struct Frag {
@@ -249,14 +255,14 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
     constexpr int r = decltype(rc)::value;
     constexpr bool x = r >= 1 && r <= C::MI;
     constexpr int i = x ? r - 1 : r == 0 ? 0 : r - C::MI;
-    const uint8_t *part = base + (x ? C::TILE * 128 : 0);
+    const uint8_t *part = base + (x ? C::TILE * 64 : 0);
     uint4 v;
     if constexpr (x ? C::XT : C::WT) {
-      const uint8_t *src = part + (x ? xcol[C::XT ? i : 0] : wcol[C::WT ? i : 0]) + 8 * s * (2 * C::TILE);
+      const uint8_t *src = part + (x ? xcol[C::XT ? i : 0] : wcol[C::WT ? i : 0]) + 16 * s * (2 * C::TILE);
       const uint2 lo = read_tr(src), hi = read_tr(src + 4 * (2 * C::TILE));
       v = make_uint4(lo.x, lo.y, hi.x, hi.y);
     } else {
-      v = *reinterpret_cast<const uint4 *>(part + ((x ? wm : wn) * C::HALF + 32 * i + fr) * 128 + 16 * ((4 * half + s) ^ ((fr >> 1) & 7)));
+      v = *reinterpret_cast<const uint4 *>(part + ((x ? wm : wn) * C::HALF + 32 * i + fr) * 64 + 16 * ((2 * s + half) ^ ((fr >> 2) & 3)));
     }
     if constexpr (x) f.b[i] = v;
     else f.a[i] = v;
@@ -264,9 +270,11 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
 
   f32x16 acc[C::MI][C::MI];  // [columns][rows]
   Frag f0, f1;
+  // One step of 16 of K: the products of `f` with the reads of `g` (step gs of
+  // the stage at gbase) and, in a stage's second, the staging of stage ds
+  // between them, in exactly this order.
   const auto step = [&](auto sel, const Frag &f, Frag &g, const uint8_t *gbase, int gs, int ds, uint8_t *dbase) {
-    constexpr int S = decltype(sel)::value, SLOTS = C::MI * C::MI;
-    constexpr int DF = S == 3 ? 0 : C::LATE, DN = S == 3 ? C::LATE : S == 0 ? C::LOADS - C::LATE : 0;
+    constexpr int SLOTS = C::MI * C::MI, DN = decltype(sel)::value == 1 ? C::LOADS : 0;
     constexpr int READS = 2 * C::MI, RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
     each<SLOTS>([&](auto slot) {
       constexpr int n = decltype(slot)::value, i = n / C::MI, k = n % C::MI;
@@ -277,31 +285,32 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
       });
       each<DPS>([&](auto q) {
         constexpr int d = n * DPS + decltype(q)::value;
-        if constexpr (d < DN) fetch_one(ds, dbase, std::integral_constant<int, DF + d>{});
+        if constexpr (d < DN) fetch_one(ds, dbase, std::integral_constant<int, d>{});
       });
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  uint8_t *cur = lds;
-  const auto stage = [&](int now, int ds, auto between) {
-    uint8_t *nxt = lds + (cur == lds ? C::STAGE : 0);
-    step(std::integral_constant<int, 0>{}, f0, f1, cur, 1, now, nxt);
-    step(std::integral_constant<int, 1>{}, f1, f0, cur, 2, 0, cur);
-    between();
-    step(std::integral_constant<int, 2>{}, f0, f1, cur, 3, 0, cur);
-    wait_lgkm0();  // step 3's fragments are in registers: this wave is done with the stage's LDS
-    wait_vm<0>();  // and its part of the next stage has landed
+  // One stage.  Its second step's fragments are in registers after the first,
+  // so behind one barrier its buffer is free for the stage four further on (ds
+  // of its tile), and the next stage has landed.
+  uint32_t cur = 0;  // the stage's buffer
+  const auto stage = [&](int ds) {
+    const uint32_t nxt = cur == (C::BUFFERS - 1) * C::STAGE ? 0 : cur + C::STAGE;
+    step(std::integral_constant<int, 0>{}, f0, f1, lds + cur, 1, 0, lds);
+    wait_lgkm0();
+    wait_vm<(C::BUFFERS - 2) * C::LOADS>();  // all but the youngest stages have landed
     barrier_no_fence();
-    step(std::integral_constant<int, 3>{}, f1, f0, nxt, 0, ds, cur);
+    step(std::integral_constant<int, 1>{}, f1, f0, lds + nxt, 0, ds, lds + cur);
     cur = nxt;
   };
 
-  const int stages = max((p.chunks + 7) / 8, 2);  // at least both buffers: one of zeros for a short K
+  const int stages = max((p.chunks + 3) / 4, C::BUFFERS);  // a short K: stages of zeros
   aim(t);
-  each<C::LOADS>([&](auto j) { fetch_one(0, lds, j); });
-  each<C::LATE>([&](auto j) { fetch_one(1, lds + C::STAGE, j); });
+  each<C::BUFFERS>([&](auto b) {
+    each<C::LOADS>([&](auto j) { fetch_one(decltype(b)::value, lds + decltype(b)::value * C::STAGE, j); });
+  });
   advance();
-  wait_vm<C::LATE>();
+  wait_vm<(C::BUFFERS - 1) * C::LOADS>();
   barrier_no_fence();
   each<2 * C::MI>([&](auto r) { read_item(f0, lds, 0, r); });
 #pragma unroll
@@ -316,18 +325,17 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
   };
 
   while (true) {
-    for (int s = 2; s < stages; ++s) {
+    for (int s = C::BUFFERS; s < stages; ++s) {
       pin();
-      stage(s - 1, s, [] {});
+      stage(s);
     }
-    pin();
-    // The last two stages bring the next tile's first two.
-    stage(stages - 1, 0, [&] {
-      limit = nt.e < 0 ? 0 : p.chunks;
-      if (nt.e >= 0) aim(nt);
-    });
-    pin();
-    stage(0, 1, [] {});
+    // The last stages bring the next tile's first.
+    limit = nt.e < 0 ? 0 : p.chunks;
+    if (nt.e >= 0) aim(nt);
+    for (int s = 0; s < C::BUFFERS; ++s) {
+      pin();
+      stage(s);
+    }
     pin();
 
     // ---- the tile's results, 4 registers' rows of all fragments at a time
