@@ -30,6 +30,29 @@
 
 namespace quads {
 
+// Global-memory-to-LDS DMA from a uniform address and the lane's offset: 16
+// bytes a lane, to consecutive LDS addresses.
+__device__ __forceinline__ void dma_uniform(uint32_t offset, const uint8_t *base, uint32_t lds) {
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds)
+               : "memory", "m0");
+#pragma clang diagnostic pop
+}
+
+// LDS reads at an address of their own address space.
+__device__ __forceinline__ uint4 read_lds16(uint32_t at) {
+  typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+  const u32x4 v = *reinterpret_cast<lds_u32x4 *>(static_cast<uintptr_t>(at));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ uint2 read_tr_at(uint32_t at) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(static_cast<uintptr_t>(at)));
+  return __builtin_bit_cast(uint2, v);
+}
+
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ f32x16 mfma_f16(uint4 a, uint4 b, f32x16 c) {
@@ -60,17 +83,20 @@ __device__ __forceinline__ uint32_t residual_f16(uint32_t x, float a, float b) {
 enum BatchedEpi {
   kEpiGram = 0,  // out = alpha Y, symmetric
   kEpiPoly = 1,  // out = beta in + alpha Y, symmetric
-  kEpiNext = 2,  // v = beta (in + in2) + Y; out = fp16(v), out2 = fp16(v - out)
-  kEpiLast = 3   // out = bf16(alpha (beta (in + in2) + Y))
+  kEpiNext = 2,   // v = beta (in + in2) + Y; out = fp16(v), out2 = fp16(v - out)
+  kEpiRound = 3,  // v = beta (in + in2) + Y; out = fp16(v)
+  kEpiLast = 4,   // out = bf16(alpha (beta in + Y))
+  kEpiOnly = 5    // out = bf16(alpha (beta (in + in2) + Y))
 };
 
 struct BatchedParams {
   const uint8_t *x, *w;
   int64_t x_row, w_row, x_mat, w_mat;  // strides in bytes of stored rows and of matrices
   int32_t batch, M, N;                 // multiples of 16
-  int32_t chunks;                      // K / 8
-  const uint16_t *in, *in2;            // [batch, M, N]; in2 may be out2
-  uint16_t *out, *out2;                // [batch, M, N]
+  int32_t K;                           // a multiple of 32, at least 128
+  int64_t in_row, in_mat, out_row, out_mat;  // strides in bytes of the arrays below
+  const uint16_t *in, *in2;            // [batch, M, N]; in2 may be out2, or null
+  uint16_t *out, *out2;                // [batch, M, N]; out2 may be null
   float alpha, beta;
 };
 
@@ -165,6 +191,7 @@ struct BatchedTile {
 template <class C, int EPI>
 __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *lds, uint32_t per_matrix, uint32_t col_tiles) {
   constexpr bool SYM = EPI == kEpiGram || EPI == kEpiPoly;
+  constexpr bool LOW = EPI == kEpiNext || EPI == kEpiRound || EPI == kEpiOnly;  // in2 is read
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
   const int wn = wave / 2, wm = wave % 2;
 
@@ -191,78 +218,83 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
     nt = tile_at(at);
   };
 
-  // Staging: instruction j < LOADS / 2 brings weights, the others rows of X.
+  // Staging: instruction j < LOADS / 2 brings W, the others X.  A lane's source
+  // is a uniform address, which moves on from stage to stage in scalar
+  // registers, and an offset that it keeps for the tile: nothing for the vector
+  // unit between the products (64-bit addresses and a selected source behind K
+  // instead: 128 experts' gate and up 14.3 ms, so 13.9; down 7.2 and 6.8).
+  // Behind the matrix rows and columns repeat the last one.
   constexpr int WL = C::LOADS / 2;
-  const uint8_t *from[C::LOADS];
-  const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_chunk);
-  const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
-  const int wk = wave * C::KROWS + lane / (64 / C::KROWS);
-  int32_t limit = p.chunks;  // 0: no tile, zeros are staged
+  uint32_t from[C::LOADS];
+  const uint8_t *wbase, *xbase;
+  const int64_t wstep = C::WT ? 32 * p.w_row : 64, xstep = C::XT ? 32 * p.x_row : 64;
   const auto aim = [&](const BatchedTile &u) {
     const int lane = fresh_lane(), lr = lane >> 2, chunk = (lane & 3) ^ ((lane >> 4) & 3);
     const int wk = wave * C::KROWS + lane / (64 / C::KROWS);
     const int slot = lane % (64 / C::KROWS);
-    const uint8_t *we = p.w + u.e * p.w_mat, *xe = p.x + u.e * p.x_mat;
+    wbase = p.w + u.e * p.w_mat + (C::WT ? 2 * static_cast<int64_t>(u.n0) : u.n0 * p.w_row);
+    xbase = p.x + u.e * p.x_mat + (C::XT ? 2 * static_cast<int64_t>(u.m0) : u.m0 * p.x_row);
 #pragma unroll
     for (int j = 0; j < C::LOADS; ++j) {
       const bool weight = j < WL;
-      const uint8_t *base = weight ? we : xe;
-      const int64_t stride = weight ? p.w_row : p.x_row;
-      const int32_t first = weight ? u.n0 : u.m0, size = weight ? p.N : p.M;
+      const uint32_t stride = static_cast<uint32_t>(weight ? p.w_row : p.x_row);
+      const int32_t left = weight ? p.N - u.n0 : p.M - u.m0;
       const int jj = weight ? j : j - WL;
       if (weight ? C::WT : C::XT) {
-        const int column = first + 8 * (slot ^ (weight ? C::w_slot(wk) : C::x_slot(wk)));
-        from[j] = base + (wk + jj * 4 * C::KROWS) * stride + 2 * min(column, size - 8);
+        const int column = 8 * (slot ^ (weight ? C::w_slot(wk) : C::x_slot(wk)));
+        from[j] = (wk + jj * 4 * C::KROWS) * stride + 2 * min(column, left - 8);
       } else {
         const int r = (jj * 4 + wave) * 16 + lr, part = r & ~(C::HALF - 1), t = r % C::HALF / 32, q = r & 31;
-        const int row = first + part + (weight ? C::w_row(q, t) : 32 * t + 4 * C::x_unit(q >> 2) + (q & 3));
-        from[j] = base + min(row, size - 1) * stride + 16 * chunk;
+        const int row = part + (weight ? C::w_row(q, t) : 32 * t + 4 * C::x_unit(q >> 2) + (q & 3));
+        from[j] = min(row, left - 1) * stride + 16 * chunk;
       }
     }
   };
-  const auto fetch_one = [&](int s, uint8_t *base, auto jc) {
+  const uint32_t lds0 = lds_address(lds);
+  // Instruction j of the stage that wbase and xbase point at, into the buffer at `to`.
+  const auto fetch_one = [&](uint32_t to, auto jc) {
     constexpr int j = decltype(jc)::value, jj = j < WL ? j : j - WL;
-    uint8_t *to = base + (j < WL ? 0 : C::TILE * 64) + (jj * 4 + wave) * 1024;
-    if constexpr (j < WL ? C::WT : C::XT) {
-      dma_wave(32 * s + wk + jj * 4 * C::KROWS < 8 * limit ? from[j] : zero, to, 16);
-      from[j] += 32 * (j < WL ? p.w_row : p.x_row);
-    } else {
-      dma_wave(4 * s + chunk < limit ? from[j] : zero, to, 16);
-      from[j] += 64;
-    }
+    dma_uniform(from[j], j < WL ? wbase : xbase, to + (j < WL ? 0 : C::TILE * 64) + (jj * 4 + wave) * 1024);
+    if constexpr (j == WL - 1) wbase += wstep;
+    if constexpr (j == C::LOADS - 1) xbase += xstep;
   };
 
-  // Fragment addresses inside an operand's part of a stage.
+  // This lane's fragment addresses inside a stage, by step.
   const int fr = lane & 31;
   // Lane 16 g + 4 j + b of a transposing read addresses row j and unit 4 (g % 2) + b
   // of the fragment's 8, in half g / 2.
-  int wcol[C::WT ? C::MI : 1], xcol[C::XT ? C::MI : 1];
+  uint32_t wat[C::WT ? C::MI : 2], xat[C::XT ? C::MI : 2];
   {
     const int j = (lane >> 2) & 3, unit = 4 * ((lane >> 4) & 1) + (lane & 3);
 #pragma unroll
-    for (int i = 0; i < C::MI; ++i) {
-      const int wu = wn * (C::HALF / 4) + C::w_unit(unit, i), xu = wm * (C::HALF / 4) + 8 * i + C::x_unit(unit);
-      if constexpr (C::WT) wcol[i] = (8 * half + j) * (2 * C::TILE) + 16 * ((wu >> 1) ^ C::w_slot(j)) + 8 * (wu & 1);
-      if constexpr (C::XT) xcol[i] = (8 * half + j) * (2 * C::TILE) + 16 * ((xu >> 1) ^ C::x_slot(j)) + 8 * (xu & 1);
+    for (int i = 0; i < (C::WT ? C::MI : 2); ++i) {
+      const int wu = wn * (C::HALF / 4) + C::w_unit(unit, i);
+      wat[i] = C::WT ? (8 * half + j) * (2 * C::TILE) + 16 * ((wu >> 1) ^ C::w_slot(j)) + 8 * (wu & 1)
+                     : (wn * C::HALF + fr) * 64 + 16 * ((2 * i + half) ^ ((fr >> 2) & 3));
+    }
+#pragma unroll
+    for (int i = 0; i < (C::XT ? C::MI : 2); ++i) {
+      const int xu = wm * (C::HALF / 4) + 8 * i + C::x_unit(unit);
+      xat[i] = C::TILE * 64 + (C::XT ? (8 * half + j) * (2 * C::TILE) + 16 * ((xu >> 1) ^ C::x_slot(j)) + 8 * (xu & 1)
+                                     : (wm * C::HALF + fr) * 64 + 16 * ((2 * i + half) ^ ((fr >> 2) & 3)));
     }
   }
   struct Frag {
     uint4 a[C::MI], b[C::MI];
   };
-  // Item r of a step's fragment reads, in the order the products need them:
-  // a[0], all of b, then the other a.
-  const auto read_item = [&](Frag &f, const uint8_t *base, int s, auto rc) {
-    constexpr int r = decltype(rc)::value;
+  // Item r of the fragment reads of step S of the stage at `base`, in the order
+  // the products need them: a[0], all of b, then the other a.
+  const auto read_item = [&](Frag &f, uint32_t base, auto sc, auto rc) {
+    constexpr int S = decltype(sc)::value, r = decltype(rc)::value;
     constexpr bool x = r >= 1 && r <= C::MI;
     constexpr int i = x ? r - 1 : r == 0 ? 0 : r - C::MI;
-    const uint8_t *part = base + (x ? C::TILE * 64 : 0);
     uint4 v;
     if constexpr (x ? C::XT : C::WT) {
-      const uint8_t *src = part + (x ? xcol[C::XT ? i : 0] : wcol[C::WT ? i : 0]) + 16 * s * (2 * C::TILE);
-      const uint2 lo = read_tr(src), hi = read_tr(src + 4 * (2 * C::TILE));
+      const uint32_t src = base + (x ? xat[C::XT ? i : 0] : wat[C::WT ? i : 0]) + 16 * S * (2 * C::TILE);
+      const uint2 lo = read_tr_at(src), hi = read_tr_at(src + 4 * (2 * C::TILE));
       v = make_uint4(lo.x, lo.y, hi.x, hi.y);
     } else {
-      v = *reinterpret_cast<const uint4 *>(part + ((x ? wm : wn) * C::HALF + 32 * i + fr) * 64 + 16 * ((2 * s + half) ^ ((fr >> 2) & 3)));
+      v = read_lds16(base + (x ? xat[C::XT ? 0 : S] : wat[C::WT ? 0 : S]) + 2048 * i);
     }
     if constexpr (x) f.b[i] = v;
     else f.a[i] = v;
@@ -270,11 +302,11 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
 
   f32x16 acc[C::MI][C::MI];  // [columns][rows]
   Frag f0, f1;
-  // One step of 16 of K: the products of `f` with the reads of `g` (step gs of
-  // the stage at gbase) and, in a stage's second, the staging of stage ds
-  // between them, in exactly this order.
-  const auto step = [&](auto sel, const Frag &f, Frag &g, const uint8_t *gbase, int gs, int ds, uint8_t *dbase) {
-    constexpr int SLOTS = C::MI * C::MI, DN = decltype(sel)::value == 1 ? C::LOADS : 0;
+  // One step of 16 of K: the products of `f` with the reads of `g` (step GS of
+  // the stage at gbase) and, in a stage's second, the staging of another into
+  // its own buffer between them, in exactly this order.
+  const auto step = [&](auto gs, const Frag &f, Frag &g, uint32_t gbase, uint32_t to) {
+    constexpr int GS = decltype(gs)::value, SLOTS = C::MI * C::MI, DN = GS == 0 ? C::LOADS : 0;
     constexpr int READS = 2 * C::MI, RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
     each<SLOTS>([&](auto slot) {
       constexpr int n = decltype(slot)::value, i = n / C::MI, k = n % C::MI;
@@ -283,36 +315,36 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
         constexpr int r = n * RPS + decltype(q)::value;
         if constexpr (r < READS) read_item(g, gbase, gs, std::integral_constant<int, r>{});
       });
-      each<DPS>([&](auto q) {
-        constexpr int d = n * DPS + decltype(q)::value;
-        if constexpr (d < DN) fetch_one(ds, dbase, std::integral_constant<int, d>{});
+      each<DPS>([&](auto q) {  // the later slots: the earlier ones have the reads
+        constexpr int d = n * DPS + decltype(q)::value - (SLOTS * DPS - DN);
+        if constexpr (d >= 0) fetch_one(to, std::integral_constant<int, d>{});
       });
       __builtin_amdgcn_sched_barrier(0);
     });
   };
   // One stage.  Its second step's fragments are in registers after the first,
-  // so behind one barrier its buffer is free for the stage four further on (ds
-  // of its tile), and the next stage has landed.
-  uint32_t cur = 0;  // the stage's buffer
-  const auto stage = [&](int ds) {
-    const uint32_t nxt = cur == (C::BUFFERS - 1) * C::STAGE ? 0 : cur + C::STAGE;
-    step(std::integral_constant<int, 0>{}, f0, f1, lds + cur, 1, 0, lds);
+  // so behind one barrier its buffer is free for the stage four further on, and
+  // the next stage has landed.
+  uint32_t cur = lds0;  // the stage's buffer
+  const auto stage = [&] {
+    const uint32_t nxt = cur == lds0 + (C::BUFFERS - 1) * C::STAGE ? lds0 : cur + C::STAGE;
+    step(std::integral_constant<int, 1>{}, f0, f1, cur, cur);
     wait_lgkm0();
     wait_vm<(C::BUFFERS - 2) * C::LOADS>();  // all but the youngest stages have landed
     barrier_no_fence();
-    step(std::integral_constant<int, 1>{}, f1, f0, lds + nxt, 0, ds, lds + cur);
+    step(std::integral_constant<int, 0>{}, f1, f0, nxt, cur);
     cur = nxt;
   };
 
-  const int stages = max((p.chunks + 3) / 4, C::BUFFERS);  // a short K: stages of zeros
+  const int stages = p.K / 32;  // at least BUFFERS
   aim(t);
   each<C::BUFFERS>([&](auto b) {
-    each<C::LOADS>([&](auto j) { fetch_one(decltype(b)::value, lds + decltype(b)::value * C::STAGE, j); });
+    each<C::LOADS>([&](auto j) { fetch_one(lds0 + decltype(b)::value * C::STAGE, j); });
   });
   advance();
   wait_vm<(C::BUFFERS - 1) * C::LOADS>();
   barrier_no_fence();
-  each<2 * C::MI>([&](auto r) { read_item(f0, lds, 0, r); });
+  each<2 * C::MI>([&](auto r) { read_item(f0, lds0, std::integral_constant<int, 0>{}, r); });
 #pragma unroll
   for (int i = 0; i < C::MI; ++i)
 #pragma unroll
@@ -327,14 +359,13 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
   while (true) {
     for (int s = C::BUFFERS; s < stages; ++s) {
       pin();
-      stage(s);
+      stage();
     }
-    // The last stages bring the next tile's first.
-    limit = nt.e < 0 ? 0 : p.chunks;
-    if (nt.e >= 0) aim(nt);
+    // The last stages bring the next tile's first (there being none, this one's again).
+    aim(nt.e >= 0 ? nt : t);
     for (int s = 0; s < C::BUFFERS; ++s) {
       pin();
-      stage(s);
+      stage();
     }
     pin();
 
@@ -354,18 +385,16 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
     // behind it read other rows, and store nothing.  No branch around loads:
     // where paths with different numbers of loads meet, the compiler can only
     // wait for all of them, also for those sent ahead.
-    const int64_t stride = 2 * static_cast<int64_t>(p.N);
-    const int64_t matrix = 2 * static_cast<int64_t>(t.e) * p.M * p.N;
     const auto rows_left = [&](int k) { return p.M - (wm0 + 32 * k); };
-    const auto offset = [&](int k) {
-      return at_col + (fh != 0 && rows_left(k) > 16 ? 16 * static_cast<uint32_t>(stride) : 0u);
+    const auto offset = [&](int k, int64_t row) {
+      return at_col + (fh != 0 && rows_left(k) > 16 ? 16 * static_cast<uint32_t>(row) : 0u);
     };
     // Byte of a group's first row.  Made where the compiler does not see it
     // before: it would compute all groups' at once and has no registers for them.
-    const auto group_at = [&](int g) -> int64_t {
+    const auto group_at = [&](int g, int64_t row_bytes, int64_t mat_bytes) -> int64_t {
       int32_t row = min(wm0 + 32 * (g / 4), p.M - 16) + 4 * (g % 4);
       asm volatile("" : "+s"(row));
-      return matrix + row * stride;
+      return t.e * mat_bytes + row * row_bytes;
     };
     struct Group {
       Neighbours<V> in[4], in2[4];
@@ -373,13 +402,13 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
     Group ring[AHEAD + 1];
     const auto load_group = [&](Group &u, int g) {
       if constexpr (EPI != kEpiGram) {
-        const uint32_t lane_at = offset(g / 4);
-        const int64_t at = group_at(g);
+        const uint32_t lane_at = offset(g / 4, p.in_row);
+        const int64_t at = group_at(g, p.in_row, p.in_mat);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          u.in[r] = load_neighbours<V>(reinterpret_cast<const uint8_t *>(p.in) + (at + r * stride) + lane_at);
-          if constexpr (EPI == kEpiNext || EPI == kEpiLast)
-            u.in2[r] = load_neighbours<V>(reinterpret_cast<const uint8_t *>(p.in2) + (at + r * stride) + lane_at);
+          u.in[r] = load_neighbours<V>(reinterpret_cast<const uint8_t *>(p.in) + (at + r * p.in_row) + lane_at);
+          if constexpr (LOW)
+            u.in2[r] = load_neighbours<V>(reinterpret_cast<const uint8_t *>(p.in2) + (at + r * p.in_row) + lane_at);
         }
       }
     };
@@ -408,12 +437,12 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
               v[i] = __builtin_fmaf(static_cast<float>(x[0]), p.beta, v[i]);
               v[i + 1] = __builtin_fmaf(static_cast<float>(x[1]), p.beta, v[i + 1]);
             }
-            if constexpr (EPI == kEpiNext || EPI == kEpiLast) {
+            if constexpr (LOW) {
               const f16x2 x = __builtin_bit_cast(f16x2, u.in2[r].w[i / 2]);
               v[i] = __builtin_fmaf(static_cast<float>(x[0]), p.beta, v[i]);
               v[i + 1] = __builtin_fmaf(static_cast<float>(x[1]), p.beta, v[i + 1]);
             }
-            if constexpr (EPI == kEpiLast) {
+            if constexpr (EPI == kEpiLast || EPI == kEpiOnly) {
               out[r].w[i / 2] = pack_bf16(p.alpha * v[i], p.alpha * v[i + 1]);
             } else {
               const f16x2 x = {static_cast<_Float16>(v[i]), static_cast<_Float16>(v[i + 1])};
@@ -426,14 +455,14 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
             for (int i = 0; i < V; ++i) acc[i][k][r0 + r] = v[i];
           }
         }
-        const uint32_t lane_at = offset(k);
+        const uint32_t lane_at = offset(k, p.out_row);
         if (col_ok && rows_left(k) > 16 * fh) {
-          const int64_t at = group_at(g);
+          const int64_t at = group_at(g, p.out_row, p.out_mat);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            store_neighbours<V>(reinterpret_cast<uint8_t *>(p.out) + (at + r * stride) + lane_at, out[r]);
+            store_neighbours<V>(reinterpret_cast<uint8_t *>(p.out) + (at + r * p.out_row) + lane_at, out[r]);
             if constexpr (EPI == kEpiNext)
-              store_neighbours<V>(reinterpret_cast<uint8_t *>(p.out2) + (at + r * stride) + lane_at, out2[r]);
+              store_neighbours<V>(reinterpret_cast<uint8_t *>(p.out2) + (at + r * p.out_row) + lane_at, out2[r]);
           }
         }
       }
@@ -450,7 +479,7 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
                 const float scale = EPI == kEpiGram ? p.alpha : 1.0f;
                 w[r] = pack_f16(scale * acc[i][k][2 * r], scale * acc[i][k][2 * r + 1]);
               }
-              uint4 *to = reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(p.out) + matrix + row * stride + 2 * at_row);
+              uint4 *to = reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(p.out) + t.e * p.out_mat + row * p.out_row + 2 * at_row);
               to[0] = make_uint4(w[0], w[1], w[2], w[3]);
               to[1] = make_uint4(w[4], w[5], w[6], w[7]);
             }

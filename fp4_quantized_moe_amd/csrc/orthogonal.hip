@@ -36,7 +36,8 @@ constexpr int kMostParts = 64;  // partial sums of a matrix: folded by a wave
 struct SplitParams {
   const void *g;
   bool f32;
-  int64_t units;  // of 8 elements, of a matrix
+  int32_t rows, row_units;          // of a matrix; units of 8 elements
+  int32_t pad_rows, pad_row_units;  // of hi and lo, which hold zeros outside it
   double eps;
   double *partial;  // [batch, parts]
   uint16_t *hi, *lo;
@@ -70,8 +71,8 @@ __device__ __forceinline__ double wave_sum(double v) {
 // fp32 neither overflow nor vanish.
 __global__ __launch_bounds__(kNormThreads) void k_square_sums(SplitParams p) {
   __shared__ double parts[kNormThreads / 64];
-  const int64_t per = (p.units + gridDim.x - 1) / gridDim.x, base = blockIdx.y * p.units;
-  const int64_t end = min(p.units, (blockIdx.x + 1) * per);
+  const int64_t units = static_cast<int64_t>(p.rows) * p.row_units, base = blockIdx.y * units;
+  const int64_t per = (units + gridDim.x - 1) / gridDim.x, end = min(units, (blockIdx.x + 1) * per);
   double s = 0.0;
   for (int64_t u = blockIdx.x * per + threadIdx.x; u < end; u += kNormThreads) {
     float v[8];
@@ -86,21 +87,36 @@ __global__ __launch_bounds__(kNormThreads) void k_square_sums(SplitParams p) {
     p.partial[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = ((parts[0] + parts[1]) + parts[2]) + parts[3];
 }
 
-// The matrix divided by its norm, as hi + lo.
+// The matrix divided by its norm, as hi + lo.  A workgroup has rows of its own.
 __global__ __launch_bounds__(kNormThreads) void k_split(SplitParams p) {
   const int lane = threadIdx.x & 63, parts = static_cast<int>(gridDim.x);
   const double ss = wave_sum(lane < parts ? p.partial[static_cast<int64_t>(blockIdx.y) * parts + lane] : 0.0);
   const double scale = static_cast<double>(kXScale) / (sqrt(ss) + p.eps);
-  const int64_t per = (p.units + gridDim.x - 1) / gridDim.x, base = blockIdx.y * p.units;
-  const int64_t end = min(p.units, (blockIdx.x + 1) * per);
-  for (int64_t u = blockIdx.x * per + threadIdx.x; u < end; u += kNormThreads) {
-    float v[8], lo[8];
-    load_values(p, base + u, v);
+  const int32_t per = (p.pad_rows + parts - 1) / parts, first = blockIdx.x * per, last = min(p.pad_rows, first + per);
+  if (first >= last) return;
+  const uint32_t units = static_cast<uint32_t>(last - first) * p.pad_row_units;  // below 2^20 x 2^17 / 64 parts, or few rows
+  for (uint32_t u = threadIdx.x; u < units; u += kNormThreads) {
+    const int32_t row = first + static_cast<int32_t>(u / p.pad_row_units), col = static_cast<int32_t>(u % p.pad_row_units);
+    float v[8] = {}, lo[8];
+    if (row < p.rows && col < p.row_units) {
+      load_values(p, (static_cast<int64_t>(blockIdx.y) * p.rows + row) * p.row_units + col, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(v[i] * scale);
+      for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(v[i] * scale);
+    }
     split_f16(v, lo);
-    reinterpret_cast<uint4 *>(p.hi)[base + u] = make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
-    reinterpret_cast<uint4 *>(p.lo)[base + u] = make_uint4(pack_f16(lo[0], lo[1]), pack_f16(lo[2], lo[3]), pack_f16(lo[4], lo[5]), pack_f16(lo[6], lo[7]));
+    const int64_t at = (static_cast<int64_t>(blockIdx.y) * p.pad_rows + row) * p.pad_row_units + col;
+    reinterpret_cast<uint4 *>(p.hi)[at] = make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+    reinterpret_cast<uint4 *>(p.lo)[at] = make_uint4(pack_f16(lo[0], lo[1]), pack_f16(lo[2], lo[3]), pack_f16(lo[4], lo[5]), pack_f16(lo[6], lo[7]));
+  }
+}
+
+template <bool WT>
+hipError_t launch_next(int epi, const BatchedParams &p, hipStream_t stream) {
+  switch (epi) {
+    case kEpiNext: return launch_batched<false, WT, kEpiNext>(p, stream);
+    case kEpiRound: return launch_batched<false, WT, kEpiRound>(p, stream);
+    case kEpiLast: return launch_batched<false, WT, kEpiLast>(p, stream);
+    default: return launch_batched<false, WT, kEpiOnly>(p, stream);
   }
 }
 
@@ -108,15 +124,24 @@ int parts_of(int64_t units) { return static_cast<int>(std::min<int64_t>((units +
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
+// A side of the workspace's matrices: contractions are whole stages, and no
+// fewer than the products have under way.  The rows and columns behind the
+// matrix are zeros, and zeros they stay.
+int64_t padded(int64_t side) { return std::max<int64_t>(128, (side + 31) / 32 * 32); }
+
 // The workspace: for every matrix of a pass hi twice (a step reads one and
 // writes the other), lo, A and B; partial sums.
 struct Layout {
+  int64_t rows, cols, m;  // padded
   int64_t hi[2], lo, a, b, partial, bytes;
 };
 
 Layout layout(int64_t batch, int64_t rows, int64_t cols) {
-  const int64_t m = std::min(rows, cols), x = up256(2 * batch * rows * cols), s = up256(2 * batch * m * m);
   Layout l{};
+  l.rows = padded(rows);
+  l.cols = padded(cols);
+  l.m = std::min(l.rows, l.cols);
+  const int64_t x = up256(2 * batch * l.rows * l.cols), s = up256(2 * batch * l.m * l.m);
   l.hi[0] = 0;
   l.hi[1] = x;
   l.lo = 2 * x;
@@ -127,48 +152,56 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
   return l;
 }
 
-}  // namespace
-
-size_t orthogonalize_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
-  return static_cast<size_t>(layout(batch, rows, cols).bytes);
+// Matrices of a pass: in as few even passes as keep the workspace at 2.7 GB.
+// (Two passes of 128 matrices of 1024 x 2048 take as long as one of 256.)
+int64_t pass_of(int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t most = std::max<int64_t>(1, (int64_t(5) << 29) / layout(1, rows, cols).bytes);
+  const int64_t passes = (batch + most - 1) / most;
+  return (batch + passes - 1) / passes;
 }
 
-hipError_t launch_orthogonalize(const OrthogonalLaunch &o, hipStream_t stream) {
-  const int64_t rows = o.rows, cols = o.cols, m = std::min(rows, cols), n = std::max(rows, cols);
+hipError_t launch_pass(const OrthogonalLaunch &o, hipStream_t stream) {
+  const int64_t rows = o.rows, cols = o.cols;
   const bool tall = rows > cols;
   const Layout l = layout(o.batch, rows, cols);
   uint8_t *ws = static_cast<uint8_t *>(o.ws);
   const auto at = [&](int64_t offset) { return reinterpret_cast<uint16_t *>(ws + offset); };
 
-  const SplitParams s{o.g, o.g_f32, rows * cols / 8, o.eps, reinterpret_cast<double *>(ws + l.partial), at(l.hi[0]), at(l.lo)};
-  const dim3 parts(parts_of(s.units), static_cast<unsigned>(o.batch));
+  const SplitParams s{o.g, o.g_f32, static_cast<int32_t>(rows), static_cast<int32_t>(cols / 8), static_cast<int32_t>(l.rows),
+                      static_cast<int32_t>(l.cols / 8), o.eps, reinterpret_cast<double *>(ws + l.partial), at(l.hi[0]), at(l.lo)};
+  const dim3 parts(parts_of(rows * cols / 8), static_cast<unsigned>(o.batch));
   hipLaunchKernelGGL(k_square_sums, parts, dim3(kNormThreads), 0, stream, s);
   hipLaunchKernelGGL(k_split, parts, dim3(kNormThreads), 0, stream, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
 
+  const int64_t xrow = 2 * l.cols, xmat = l.rows * xrow, arow = 2 * l.m, amat = l.m * arow;
   BatchedParams gram{};  // A = X X^T or X^T X
   gram.batch = static_cast<int32_t>(o.batch);
-  gram.M = gram.N = static_cast<int32_t>(m);
-  gram.chunks = static_cast<int32_t>(n / 8);
-  gram.x_row = gram.w_row = 2 * cols;
-  gram.x_mat = gram.w_mat = 2 * rows * cols;
+  gram.M = gram.N = static_cast<int32_t>(l.m);
+  gram.K = static_cast<int32_t>(std::max(l.rows, l.cols));
+  gram.x_row = gram.w_row = xrow;
+  gram.x_mat = gram.w_mat = xmat;
   gram.out = at(l.a);
+  gram.out_row = arow;
+  gram.out_mat = amat;
   gram.alpha = kAScale / (kXScale * kXScale);
 
   BatchedParams poly = gram;  // B = b A + c A A
-  poly.chunks = static_cast<int32_t>(m / 8);
+  poly.K = static_cast<int32_t>(l.m);
   poly.x = poly.w = ws + l.a;
-  poly.x_row = poly.w_row = 2 * m;
-  poly.x_mat = poly.w_mat = 2 * m * m;
+  poly.x_row = poly.w_row = poly.in_row = arow;
+  poly.x_mat = poly.w_mat = poly.in_mat = amat;
   poly.in = at(l.a);
   poly.out = at(l.b);
   poly.alpha = o.c / (kAScale * kAScale);
   poly.beta = o.b / kAScale;
 
   BatchedParams next = poly;  // X <- a X + B X or a X + X B
-  next.M = static_cast<int32_t>(rows);
-  next.N = static_cast<int32_t>(cols);
+  next.M = static_cast<int32_t>(l.rows);
+  next.N = static_cast<int32_t>(l.cols);
+  next.in_row = next.out_row = xrow;
+  next.in_mat = next.out_mat = xmat;
   next.in2 = next.out2 = at(l.lo);
   next.alpha = 1.0f / kXScale;
   next.beta = o.a;
@@ -180,26 +213,47 @@ hipError_t launch_orthogonalize(const OrthogonalLaunch &o, hipStream_t stream) {
     if (e != hipSuccess) return e;
     e = launch_batched<false, false, kEpiPoly>(poly, stream);
     if (e != hipSuccess) return e;
-    const bool last = step + 1 == o.steps;
     next.in = reinterpret_cast<const uint16_t *>(x);
-    next.out = last ? o.out : at(l.hi[(step + 1) & 1]);
-    if (tall) {  // rows of X against rows of B, which is symmetric
-      next.x = x;
-      next.x_row = 2 * cols;
-      next.x_mat = 2 * rows * cols;
-      next.w = ws + l.b;
-      next.w_row = 2 * m;
-      next.w_mat = 2 * m * m;
-      e = last ? launch_batched<false, false, kEpiLast>(next, stream) : launch_batched<false, false, kEpiNext>(next, stream);
-    } else {  // rows of B against columns of X
-      next.x = ws + l.b;
-      next.x_row = 2 * m;
-      next.x_mat = 2 * m * m;
-      next.w = x;
-      next.w_row = 2 * cols;
-      next.w_mat = 2 * rows * cols;
-      e = last ? launch_batched<false, true, kEpiLast>(next, stream) : launch_batched<false, true, kEpiNext>(next, stream);
+    next.out = at(l.hi[(step + 1) & 1]);
+    if (step + 1 == o.steps) {
+      next.M = static_cast<int32_t>(rows);
+      next.N = static_cast<int32_t>(cols);
+      next.out = o.out;
+      next.out_row = 2 * cols;
+      next.out_mat = 2 * rows * cols;
     }
+    // tall: rows of X against rows of B, which is symmetric; else rows of B against columns of X
+    const uint8_t *b = ws + l.b;
+    next.x = tall ? x : b;
+    next.x_row = tall ? xrow : arow;
+    next.x_mat = tall ? xmat : amat;
+    next.w = tall ? b : x;
+    next.w_row = tall ? arow : xrow;
+    next.w_mat = tall ? amat : xmat;
+    // The last step's X is hi alone: what its rounding adds is multiplied by a
+    // once (0.05%), and neither written nor read lo is 2 of a call's 19 passes
+    // over a matrix of X's size.
+    const int epi = o.steps == 1 ? kEpiOnly : step + 1 == o.steps ? kEpiLast : step + 2 == o.steps ? kEpiRound : kEpiNext;
+    e = tall ? launch_next<false>(epi, next, stream) : launch_next<true>(epi, next, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t orthogonalize_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
+  return static_cast<size_t>(layout(pass_of(batch, rows, cols), rows, cols).bytes);
+}
+
+hipError_t launch_orthogonalize(const OrthogonalLaunch &o, hipStream_t stream) {
+  const int64_t pass = pass_of(o.batch, o.rows, o.cols), elems = o.rows * o.cols;
+  for (int64_t first = 0; first < o.batch; first += pass) {
+    OrthogonalLaunch part = o;
+    part.batch = std::min(pass, o.batch - first);
+    part.g = static_cast<const uint8_t *>(o.g) + first * elems * (o.g_f32 ? 4 : 2);
+    part.out = o.out + first * elems;
+    const hipError_t e = launch_pass(part, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

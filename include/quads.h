@@ -678,8 +678,8 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
  *   `steps` times  X <- a X + (b A + c A^2) X  with A = X X^T
  * (for rows > cols the same from the right, with X^T X), and written as bf16
  * to out [batch, rows, cols].  |g|_F is summed in 64 bits.  The products take
- * fp16 operands and add in fp32; X is kept to 22 bits between the steps, so
- * the result is within about 2e-3 of the formula's (relative, 2-norm) before
+ * fp16 operands and add in fp32; X is kept to 22 bits between the steps (11
+ * before the last), so the result is within about 2e-3 of the formula's (relative, 2-norm) before
  * its rounding to bf16, also for matrices of low rank.  coefficients: the
  * host's a, b, c.  Entries of X, A and b A + c A^2 have to stay below 31, 63
  * and 65504 (they are below 5 for coefficients that keep the singular values
