@@ -3,7 +3,7 @@
 // stored with the contraction along its rows (X as [K, M], W as [K, N]).
 //
 // A stage is 32 of K of TILE rows of X and of W; four stages in LDS, brought by
-// DMA three stages before they are read.  Rows are 64 bytes; row r keeps its
+// DMA three stages before they are read (two with the smallest tile, one before).  Rows are 64 bytes; row r keeps its
 // chunk c in slot c ^ (r / 4 % 4), so that 16 rows of a fragment read take each
 // of the banks once.  (Two stages of 64, as in grouped_staged.hpp, are as fast
 // with many matrices and slower with few: one 1536 x 2048 361 against 324 us.)
@@ -45,6 +45,11 @@ __device__ __forceinline__ uint4 read_lds16(uint32_t at) {
   typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
   const u32x4 v = *reinterpret_cast<lds_u32x4 *>(static_cast<uintptr_t>(at));
   return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void write_lds16(uint32_t at, const float (&v)[4]) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+  *reinterpret_cast<lds_f32x4 *>(static_cast<uintptr_t>(at)) = f32x4{v[0], v[1], v[2], v[3]};
 }
 __device__ __forceinline__ uint2 read_tr_at(uint32_t at) {
   typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -100,16 +105,23 @@ struct BatchedParams {
   float alpha, beta;
 };
 
+// A tile's K is contracted by SPLIT groups of waves, each a part of it.
+// TILE 256 and 128: one group of 2 x 2 waves with a quarter of the tile each.
+// TILE 64: four groups of one wave, for the whole tile; their sums meet in LDS,
+// and each takes a quarter of the rows out.
 template <int TILE_, bool XT_, bool WT_>
 struct BatchedCfg {
-  static constexpr int TILE = TILE_, HALF = TILE / 2;  // 2 x 2 waves
+  static constexpr int TILE = TILE_, SPLIT = TILE == 64 ? 4 : 1, WAVES = 4 / SPLIT, SIDE = WAVES == 4 ? 2 : 1;
+  static constexpr int HALF = TILE / SIDE;             // a wave's part, each way
   static constexpr bool XT = XT_, WT = WT_;
   static constexpr int MI = HALF / 32;                 // 32 x 32 tiles of a wave, each way
-  static constexpr int BUFFERS = 4;
+  static constexpr int BUFFERS = TILE == 64 ? 2 : 4;   // (two workgroups of the smallest tile a CU)
   static constexpr int STAGE = 2 * TILE * 64;          // 32 of K: 64 bytes of a row
-  static constexpr int LOADS = TILE / 32;              // staging instructions of a wave and stage, both operands
+  static constexpr int LOADS = STAGE / 1024 / WAVES;   // staging instructions of a wave and stage, both operands
   static constexpr int KROWS = 512 / TILE;             // transposed operand: stored rows of an instruction
-  static constexpr int LDS = BUFFERS * STAGE;
+  static constexpr int RING = BUFFERS * STAGE, LDS = SPLIT * RING;
+  static constexpr int ROWS = SPLIT == 1 ? MI : 1;     // row fragments that a wave takes out, and
+  static constexpr int REGS = SPLIT == 1 ? 16 : 8;     // registers of each
   // Position p of 32 (a lane of a fragment, or a row of the accumulators) and
   // fragment t of a wave's half tile -> column or row inside the half.
   // W by rows: lane p of fragment t has column MI p + t.  W by columns: in
@@ -121,8 +133,11 @@ struct BatchedCfg {
   static __device__ __forceinline__ int x_unit(int p4) { return 4 * (p4 & 1) + (p4 >> 1); }
   // Slot of a chunk of a transposed stage is chunk ^ slot(k): the four rows k
   // that a group of 16 lanes reads lie in different banks than its units.
-  static __device__ __forceinline__ int w_slot(int k) { return MI == 4 ? k & 3 : (k & 1) | ((k & 2) << 2); }
-  static __device__ __forceinline__ int x_slot(int k) { return (k & 3) << 2; }
+  // (Rows of the smallest tile are 128 bytes: two of them have banks of their own.)
+  static __device__ __forceinline__ int w_slot(int k) {
+    return TILE == 256 ? k & 3 : TILE == 128 ? (k & 1) | ((k & 2) << 2) : (k >> 1) & 1;
+  }
+  static __device__ __forceinline__ int x_slot(int k) { return TILE == 64 ? (k & 2) << 1 : (k & 3) << 2; }
 };
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -192,8 +207,9 @@ template <class C, int EPI>
 __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *lds, uint32_t per_matrix, uint32_t col_tiles) {
   constexpr bool SYM = EPI == kEpiGram || EPI == kEpiPoly;
   constexpr bool LOW = EPI == kEpiNext || EPI == kEpiRound || EPI == kEpiOnly;  // in2 is read
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
-  const int wn = wave / 2, wm = wave % 2;
+  const int lane = threadIdx.x & 63, all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+  const int wave = all_waves % C::WAVES, group = all_waves / C::WAVES;
+  const int wn = wave / C::SIDE, wm = wave % C::SIDE;
 
   // The tiles of this workgroup: at, at + step, ... below end, out of its XCD's eighth.
   const uint32_t tiles = static_cast<uint32_t>(p.batch) * per_matrix, per = (tiles + 7) / 8;
@@ -212,7 +228,7 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
     }
     return BatchedTile{static_cast<int32_t>(e), static_cast<int32_t>(i) * C::TILE, static_cast<int32_t>(r) * C::TILE};
   };
-  BatchedTile t = tile_at(at), nt;
+  BatchedTile t = tile_at(at), nt{-1, 0, 0};
   const auto advance = [&] {
     at += step_tiles;
     nt = tile_at(at);
@@ -227,13 +243,16 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
   constexpr int WL = C::LOADS / 2;
   uint32_t from[C::LOADS];
   const uint8_t *wbase, *xbase;
+  // The group's stages, at least BUFFERS, and those of the groups before it.
+  const int all_stages = p.K / 32, before = group * all_stages / C::SPLIT;
+  const int stages = (group + 1) * all_stages / C::SPLIT - before;
   const int64_t wstep = C::WT ? 32 * p.w_row : 64, xstep = C::XT ? 32 * p.x_row : 64;
   const auto aim = [&](const BatchedTile &u) {
     const int lane = fresh_lane(), lr = lane >> 2, chunk = (lane & 3) ^ ((lane >> 4) & 3);
     const int wk = wave * C::KROWS + lane / (64 / C::KROWS);
     const int slot = lane % (64 / C::KROWS);
-    wbase = p.w + u.e * p.w_mat + (C::WT ? 2 * static_cast<int64_t>(u.n0) : u.n0 * p.w_row);
-    xbase = p.x + u.e * p.x_mat + (C::XT ? 2 * static_cast<int64_t>(u.m0) : u.m0 * p.x_row);
+    wbase = p.w + u.e * p.w_mat + (C::WT ? 2 * static_cast<int64_t>(u.n0) : u.n0 * p.w_row) + before * wstep;
+    xbase = p.x + u.e * p.x_mat + (C::XT ? 2 * static_cast<int64_t>(u.m0) : u.m0 * p.x_row) + before * xstep;
 #pragma unroll
     for (int j = 0; j < C::LOADS; ++j) {
       const bool weight = j < WL;
@@ -242,19 +261,19 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
       const int jj = weight ? j : j - WL;
       if (weight ? C::WT : C::XT) {
         const int column = 8 * (slot ^ (weight ? C::w_slot(wk) : C::x_slot(wk)));
-        from[j] = (wk + jj * 4 * C::KROWS) * stride + 2 * min(column, left - 8);
+        from[j] = (wk + jj * C::WAVES * C::KROWS) * stride + 2 * min(column, left - 8);
       } else {
-        const int r = (jj * 4 + wave) * 16 + lr, part = r & ~(C::HALF - 1), t = r % C::HALF / 32, q = r & 31;
+        const int r = (jj * C::WAVES + wave) * 16 + lr, part = r & ~(C::HALF - 1), t = r % C::HALF / 32, q = r & 31;
         const int row = part + (weight ? C::w_row(q, t) : 32 * t + 4 * C::x_unit(q >> 2) + (q & 3));
         from[j] = min(row, left - 1) * stride + 16 * chunk;
       }
     }
   };
-  const uint32_t lds0 = lds_address(lds);
+  const uint32_t lds0 = lds_address(lds) + group * C::RING;
   // Instruction j of the stage that wbase and xbase point at, into the buffer at `to`.
   const auto fetch_one = [&](uint32_t to, auto jc) {
     constexpr int j = decltype(jc)::value, jj = j < WL ? j : j - WL;
-    dma_uniform(from[j], j < WL ? wbase : xbase, to + (j < WL ? 0 : C::TILE * 64) + (jj * 4 + wave) * 1024);
+    dma_uniform(from[j], j < WL ? wbase : xbase, to + (j < WL ? 0 : C::TILE * 64) + (jj * C::WAVES + wave) * 1024);
     if constexpr (j == WL - 1) wbase += wstep;
     if constexpr (j == C::LOADS - 1) xbase += xstep;
   };
@@ -305,8 +324,8 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
   // One step of 16 of K: the products of `f` with the reads of `g` (step GS of
   // the stage at gbase) and, in a stage's second, the staging of another into
   // its own buffer between them, in exactly this order.
-  const auto step = [&](auto gs, const Frag &f, Frag &g, uint32_t gbase, uint32_t to) {
-    constexpr int GS = decltype(gs)::value, SLOTS = C::MI * C::MI, DN = GS == 0 ? C::LOADS : 0;
+  const auto step = [&](auto gs, auto fetch, const Frag &f, Frag &g, uint32_t gbase, uint32_t to) {
+    constexpr int GS = decltype(gs)::value, SLOTS = C::MI * C::MI, DN = GS == 0 && decltype(fetch)::value ? C::LOADS : 0;
     constexpr int READS = 2 * C::MI, RPS = (READS + SLOTS - 1) / SLOTS, DPS = (DN + SLOTS - 1) / SLOTS;
     each<SLOTS>([&](auto slot) {
       constexpr int n = decltype(slot)::value, i = n / C::MI, k = n % C::MI;
@@ -326,24 +345,24 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
   // so behind one barrier its buffer is free for the stage four further on, and
   // the next stage has landed.
   uint32_t cur = lds0;  // the stage's buffer
-  const auto stage = [&] {
+  const auto stage = [&](auto fetch) {
+    constexpr bool FETCH = decltype(fetch)::value;
     const uint32_t nxt = cur == lds0 + (C::BUFFERS - 1) * C::STAGE ? lds0 : cur + C::STAGE;
-    step(std::integral_constant<int, 1>{}, f0, f1, cur, cur);
+    step(std::integral_constant<int, 1>{}, fetch, f0, f1, cur, cur);
     wait_lgkm0();
-    wait_vm<(C::BUFFERS - 2) * C::LOADS>();  // all but the youngest stages have landed
-    barrier_no_fence();
-    step(std::integral_constant<int, 0>{}, f1, f0, nxt, cur);
+    wait_vm<FETCH ? (C::BUFFERS - 2) * C::LOADS : 0>();  // all but the youngest stages have landed
+    if constexpr (C::WAVES > 1) barrier_no_fence();
+    step(std::integral_constant<int, 0>{}, fetch, f1, f0, nxt, cur);
     cur = nxt;
   };
 
-  const int stages = p.K / 32;  // at least BUFFERS
   aim(t);
   each<C::BUFFERS>([&](auto b) {
     each<C::LOADS>([&](auto j) { fetch_one(lds0 + decltype(b)::value * C::STAGE, j); });
   });
-  advance();
+  if constexpr (C::SPLIT == 1) advance();
   wait_vm<(C::BUFFERS - 1) * C::LOADS>();
-  barrier_no_fence();
+  if constexpr (C::WAVES > 1) barrier_no_fence();
   each<2 * C::MI>([&](auto r) { read_item(f0, lds0, std::integral_constant<int, 0>{}, r); });
 #pragma unroll
   for (int i = 0; i < C::MI; ++i)
@@ -359,20 +378,60 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
   while (true) {
     for (int s = C::BUFFERS; s < stages; ++s) {
       pin();
-      stage();
+      stage(std::true_type{});
     }
-    // The last stages bring the next tile's first (there being none, this one's again).
-    aim(nt.e >= 0 ? nt : t);
-    for (int s = 0; s < C::BUFFERS; ++s) {
-      pin();
-      stage();
+    if constexpr (C::SPLIT == 1) {
+      // The last stages bring the next tile's first (there being none, this one's again).
+      aim(nt.e >= 0 ? nt : t);
+      for (int s = 0; s < C::BUFFERS; ++s) {
+        pin();
+        stage(std::true_type{});
+      }
+    } else {  // one tile a workgroup
+      for (int s = 0; s < C::BUFFERS; ++s) {
+        pin();
+        stage(std::false_type{});
+      }
+      // The waves' sums, a fragment at a time; wave g takes registers 8 (g % 2) ..
+      // of row fragment g / 2, from all waves in their order.
+      wait_lgkm0();
+      barrier_no_fence();  // every wave is done with the stages
+      const uint32_t exchange = lds_address(lds) + 16 * lane;
+#pragma unroll
+      for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+        for (int k = 0; k < C::MI; ++k)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float v[4] = {acc[i][k][4 * q], acc[i][k][4 * q + 1], acc[i][k][4 * q + 2], acc[i][k][4 * q + 3]};
+            write_lds16(exchange + 16384 * group + 1024 * ((i * C::MI + k) * 4 + q), v);
+          }
+      wait_lgkm0();
+      barrier_no_fence();
+#pragma unroll
+      for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float sum[4] = {};
+#pragma unroll
+          for (int g = 0; g < C::SPLIT; ++g) {
+            const uint4 v = read_lds16(exchange + 16384 * g + 1024 * ((i * C::MI + (group >> 1)) * 4 + 2 * (group & 1) + q));
+            sum[0] += __uint_as_float(v.x);
+            sum[1] += __uint_as_float(v.y);
+            sum[2] += __uint_as_float(v.z);
+            sum[3] += __uint_as_float(v.w);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][0][4 * q + r] = sum[r];
+        }
     }
     pin();
 
     // ---- the tile's results, 4 registers' rows of all fragments at a time
-    constexpr int V = C::MI, GROUPS = 4 * C::MI, AHEAD = 3;  // group g: row fragment g / 4, registers 4 (g % 4) ..
+    constexpr int V = C::MI, PER = C::REGS / 4, GROUPS = PER * C::ROWS;  // group g: row fragment g / PER, registers 4 (g % PER) ..
+    constexpr int AHEAD = GROUPS > 3 ? 3 : GROUPS - 1;
     const int fl = fresh_lane(), fh = fl >> 5, fp = fl & 31;
-    const int32_t wm0 = t.m0 + wm * C::HALF, wn0 = t.n0 + wn * C::HALF;
+    const int32_t wm0 = t.m0 + wm * C::HALF + 32 * (group >> 1), wn0 = t.n0 + wn * C::HALF;
     // The lane's V columns.
     const int32_t col = wn0 + (!C::WT ? V * fp
                                : V == 4 ? 4 * C::w_unit(fp >> 2, fp & 3)
@@ -392,7 +451,7 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
     // Byte of a group's first row.  Made where the compiler does not see it
     // before: it would compute all groups' at once and has no registers for them.
     const auto group_at = [&](int g, int64_t row_bytes, int64_t mat_bytes) -> int64_t {
-      int32_t row = min(wm0 + 32 * (g / 4), p.M - 16) + 4 * (g % 4);
+      int32_t row = min(wm0 + 32 * (g / PER), p.M - 16) + C::REGS * (group & 1) + 4 * (g % PER);
       asm volatile("" : "+s"(row));
       return t.e * mat_bytes + row * row_bytes;
     };
@@ -402,7 +461,7 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
     Group ring[AHEAD + 1];
     const auto load_group = [&](Group &u, int g) {
       if constexpr (EPI != kEpiGram) {
-        const uint32_t lane_at = offset(g / 4, p.in_row);
+        const uint32_t lane_at = offset(g / PER, p.in_row);
         const int64_t at = group_at(g, p.in_row, p.in_mat);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -415,7 +474,7 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
     each<AHEAD>([&](auto gc) { load_group(ring[decltype(gc)::value], decltype(gc)::value); });
     const bool mirror = SYM && t.m0 != t.n0;
     each<GROUPS>([&](auto gc) {
-      constexpr int g = decltype(gc)::value, k = g / 4, r0 = 4 * (g % 4);
+      constexpr int g = decltype(gc)::value, k = g / PER, r0 = 4 * (g % PER);
       if constexpr (g + AHEAD < GROUPS) load_group(ring[(g + AHEAD) % (AHEAD + 1)], g + AHEAD);
       __builtin_amdgcn_sched_barrier(0);
       {
@@ -466,33 +525,33 @@ __device__ __forceinline__ void batched_tiles(const BatchedParams &p, uint8_t *l
           }
         }
       }
-      if constexpr (SYM && g % 4 == 3) {
+      if constexpr (SYM && g % PER == PER - 1) {
         if (mirror) {
-          const int32_t at_row = wm0 + 32 * k + 16 * fh;
+          const int32_t at_row = wm0 + 32 * k + 16 * fh + C::REGS * (group & 1);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {  // a lane's 16 rows of column i are neighbours in a row
+          for (int i = 0; i < V; ++i) {  // a lane's rows of column i are neighbours in a row
             const int32_t row = wn0 + (C::WT ? 4 * C::w_unit(fp >> 2, i) + (fp & 3) : C::w_row(fp, i));
             if (row < p.N && at_row < p.M) {
-              uint32_t w[8];
+              uint8_t *to = reinterpret_cast<uint8_t *>(p.out) + t.e * p.out_mat + row * p.out_row + 2 * at_row;
+              const float scale = EPI == kEpiGram ? p.alpha : 1.0f;
 #pragma unroll
-              for (int r = 0; r < 8; ++r) {
-                const float scale = EPI == kEpiGram ? p.alpha : 1.0f;
-                w[r] = pack_f16(scale * acc[i][k][2 * r], scale * acc[i][k][2 * r + 1]);
+              for (int r = 0; r < C::REGS; r += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = pack_f16(scale * acc[i][k][r + 2 * q], scale * acc[i][k][r + 2 * q + 1]);
+                *reinterpret_cast<uint4 *>(to + 2 * r) = make_uint4(w[0], w[1], w[2], w[3]);
               }
-              uint4 *to = reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(p.out) + t.e * p.out_mat + row * p.out_row + 2 * at_row);
-              to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              to[1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
           }
         }
       }
-      if constexpr (g % 4 == 3) {
+      if constexpr (g % PER == PER - 1) {
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i][k] = f32x16{};
       }
       __builtin_amdgcn_sched_barrier(0);
     });
-    if (nt.e < 0) break;
+    if (C::SPLIT > 1 || nt.e < 0) break;
     t = nt;
     advance();
   }
@@ -513,22 +572,27 @@ hipError_t launch_batched_tiles(const BatchedParams &p, hipStream_t stream) {
   const int64_t per_matrix = SYM ? r * (r + 1) / 2 : r * c;
   const int64_t tiles = (p.batch * per_matrix + 7) / 8 * 8;
   if (tiles > 0x3FFFFFFF) return hipErrorInvalidConfiguration;
-  const int64_t grid = std::min<int64_t>(tiles, 256 * PER_CU);
+  const int64_t grid = C::SPLIT > 1 ? tiles : std::min<int64_t>(tiles, 256 * PER_CU);  // with SPLIT one tile a workgroup
   hipLaunchKernelGGL((k_batched<C, EPI>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, p,
                      static_cast<uint32_t>(per_matrix), static_cast<uint32_t>(c));
   return hipGetLastError();
 }
 
-// The large tile reads each operand half as often; small ones, two a CU, fill
-// the card with few matrices.
+// The large tile reads each operand half as often; smaller ones, two a CU, fill
+// the card with few matrices.  The smallest where all of them run at once: one
+// matrix of 1024 x 1024 in five steps 198 -> 140 us, of 512 x 512 138 -> 98, 8 of
+// 512 x 512 144 -> 128; beyond, one of 2048 x 2048 takes 375 us with 128 x 128
+// and 653 with it.
 template <bool XT, bool WT, int EPI>
 hipError_t launch_batched(const BatchedParams &p, hipStream_t stream) {
   constexpr bool SYM = EPI == kEpiGram || EPI == kEpiPoly;
-  const auto rounds = [&](int64_t tile, int64_t places) {
+  const auto tiles = [&](int64_t tile) {
     const int64_t r = (p.M + tile - 1) / tile, c = (p.N + tile - 1) / tile;
-    return (p.batch * (SYM ? r * (r + 1) / 2 : r * c) + places - 1) / places;
+    return p.batch * (SYM ? r * (r + 1) / 2 : r * c);
   };
-  if (100 * rounds(256, 256) <= 60 * rounds(128, 512)) return launch_batched_tiles<BatchedCfg<256, XT, WT>, EPI>(p, stream);
+  if (100 * ((tiles(256) + 255) / 256) <= 60 * ((tiles(128) + 511) / 512))
+    return launch_batched_tiles<BatchedCfg<256, XT, WT>, EPI>(p, stream);
+  if (tiles(64) <= 512 && p.K >= 256) return launch_batched_tiles<BatchedCfg<64, XT, WT>, EPI>(p, stream);
   return launch_batched_tiles<BatchedCfg<128, XT, WT>, EPI>(p, stream);
 }
 

@@ -31,7 +31,6 @@ constexpr float kXScale = 2048.0f, kAScale = 1024.0f;
 // ---- normalisation -------------------------------------------------------------
 
 constexpr int kNormThreads = 256;
-constexpr int kMostParts = 64;  // partial sums of a matrix: folded by a wave
 
 struct SplitParams {
   const void *g;
@@ -89,12 +88,14 @@ __global__ __launch_bounds__(kNormThreads) void k_square_sums(SplitParams p) {
 
 // The matrix divided by its norm, as hi + lo.  A workgroup has rows of its own.
 __global__ __launch_bounds__(kNormThreads) void k_split(SplitParams p) {
-  const int lane = threadIdx.x & 63, parts = static_cast<int>(gridDim.x);
-  const double ss = wave_sum(lane < parts ? p.partial[static_cast<int64_t>(blockIdx.y) * parts + lane] : 0.0);
+  const int parts = static_cast<int>(gridDim.x);
+  double ss = 0.0;
+  for (int i = threadIdx.x & 63; i < parts; i += 64) ss += p.partial[static_cast<int64_t>(blockIdx.y) * parts + i];
+  ss = wave_sum(ss);
   const double scale = static_cast<double>(kXScale) / (sqrt(ss) + p.eps);
   const int32_t per = (p.pad_rows + parts - 1) / parts, first = blockIdx.x * per, last = min(p.pad_rows, first + per);
   if (first >= last) return;
-  const uint32_t units = static_cast<uint32_t>(last - first) * p.pad_row_units;  // below 2^20 x 2^17 / 64 parts, or few rows
+  const uint32_t units = static_cast<uint32_t>(last - first) * p.pad_row_units;  // at most 2^20 / 64 rows of 2^17
   for (uint32_t u = threadIdx.x; u < units; u += kNormThreads) {
     const int32_t row = first + static_cast<int32_t>(u / p.pad_row_units), col = static_cast<int32_t>(u % p.pad_row_units);
     float v[8] = {}, lo[8];
@@ -120,7 +121,11 @@ hipError_t launch_next(int epi, const BatchedParams &p, hipStream_t stream) {
   }
 }
 
-int parts_of(int64_t units) { return static_cast<int>(std::min<int64_t>((units + 1023) / 1024, kMostParts)); }
+// Workgroups of a matrix: at least 64 for a large one, more where there are few
+// matrices (one of 1536 x 2048 with 64: 10 and 14 us for the two kernels).
+int parts_of(int64_t batch, int64_t units) {
+  return static_cast<int>(std::min<int64_t>((units + 1023) / 1024, std::max<int64_t>(64, 512 / batch)));
+}
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -148,7 +153,7 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
   l.a = 3 * x;
   l.b = l.a + s;
   l.partial = l.b + s;
-  l.bytes = l.partial + up256(8 * batch * parts_of(rows * cols / 8));
+  l.bytes = l.partial + up256(8 * batch * parts_of(batch, rows * cols / 8));
   return l;
 }
 
@@ -169,7 +174,7 @@ hipError_t launch_pass(const OrthogonalLaunch &o, hipStream_t stream) {
 
   const SplitParams s{o.g, o.g_f32, static_cast<int32_t>(rows), static_cast<int32_t>(cols / 8), static_cast<int32_t>(l.rows),
                       static_cast<int32_t>(l.cols / 8), o.eps, reinterpret_cast<double *>(ws + l.partial), at(l.hi[0]), at(l.lo)};
-  const dim3 parts(parts_of(rows * cols / 8), static_cast<unsigned>(o.batch));
+  const dim3 parts(parts_of(o.batch, rows * cols / 8), static_cast<unsigned>(o.batch));
   hipLaunchKernelGGL(k_square_sums, parts, dim3(kNormThreads), 0, stream, s);
   hipLaunchKernelGGL(k_split, parts, dim3(kNormThreads), 0, stream, s);
   hipError_t e = hipGetLastError();
