@@ -33,7 +33,7 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// Sum over the TPR lanes of a row: a wave, or the four waves of a workgroup
+// Sum over the TPR lanes of a row: a wave, or four or eight of a workgroup's
 // (`parts`: their meeting place; a barrier).
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *parts) {
@@ -42,8 +42,14 @@ __device__ __forceinline__ float row_sum(float v, float *parts) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (lane == 0) parts[wave] = v;
   __syncthreads();
-  const float4 p = *reinterpret_cast<const float4 *>(parts + (wave & ~3));
-  return ((p.x + p.y) + p.z) + p.w;
+  const float4 *row = reinterpret_cast<const float4 *>(parts + (wave & ~(TPR / 64 - 1)));
+  const float4 p = row[0];
+  v = ((p.x + p.y) + p.z) + p.w;
+  if constexpr (TPR == 512) {
+    const float4 q = row[1];
+    v = (((v + q.x) + q.y) + q.z) + q.w;
+  }
+  return v;
 }
 
 // A unit of 8 values as loaded: bf16 fills `lo` alone.
@@ -200,7 +206,7 @@ struct NormGradParams {
   int64_t rows;
   int32_t units;
   float cols;
-  bool dy_f32, s_f32, weight_f32;
+  bool weight_f32;
   const void *dy, *s, *weight, *dsum;
   const float *rstd;
   void *dx;
@@ -209,44 +215,45 @@ struct NormGradParams {
 
 constexpr int kGradThreads = 512;
 
-// 512 / TPR rows of a workgroup at once; workgroups stay and take rows in turn.
-template <int TPR, int V>
+// 512 / TPR rows of a workgroup at once; workgroups stay and take rows in turn,
+// their columns' weights and sums of dy n in registers.  Few units a lane, so
+// that two workgroups fit a CU: with a wave a row (8192 x 2048: four units a
+// lane, 256 registers) the kernel took 45 us.
+template <bool DY32, bool S32, int TPR, int V>
 __global__ __launch_bounds__(kGradThreads) void k_rms_norm_grad(NormGradParams p) {
   constexpr int ROWS = kGradThreads / TPR;
   __shared__ __attribute__((aligned(16))) float parts[2][8];
-  __shared__ __attribute__((aligned(16))) float meet[(ROWS - 1) * TPR * 8];
+  __shared__ __attribute__((aligned(16))) float meet[ROWS > 1 ? (ROWS - 1) * TPR * 8 : 1];
   const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
-  float acc[V][8] = {};
+  float acc[V][8] = {}, w[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) unpack(load_unit(p.weight, min(t + v * TPR, p.units - 1), p.weight_f32), p.weight_f32, w[v]);
   int turn = 0;
   // Every wave makes the same number of rounds: the rows' sums contain a barrier.
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * ROWS; base < p.rows; base += static_cast<int64_t>(gridDim.x) * ROWS) {
     const bool live = base + slot < p.rows;
     const int64_t row = live ? base + slot : p.rows - 1, first = row * p.units;
-    Raw s[V], dy[V], w[V], ds[V];
+    Raw s[V], dy[V], ds[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = load_unit(p.s, first + min(t + v * TPR, p.units - 1), p.s_f32);
+    for (int v = 0; v < V; ++v) s[v] = load_unit(p.s, first + min(t + v * TPR, p.units - 1), S32);
 #pragma unroll
-    for (int v = 0; v < V; ++v) dy[v] = load_unit(p.dy, first + min(t + v * TPR, p.units - 1), p.dy_f32);
-#pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = load_unit(p.weight, min(t + v * TPR, p.units - 1), p.weight_f32);
+    for (int v = 0; v < V; ++v) dy[v] = load_unit(p.dy, first + min(t + v * TPR, p.units - 1), DY32);
     if (p.dsum) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) ds[v] = load_unit(p.dsum, first + min(t + v * TPR, p.units - 1), p.s_f32);
+      for (int v = 0; v < V; ++v) ds[v] = load_unit(p.dsum, first + min(t + v * TPR, p.units - 1), S32);
     }
     const float r = p.rstd[row];
     float n[V][8], d[V][8], dot = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float g[8];
-      unpack(s[v], p.s_f32, n[v]);
-      unpack(dy[v], p.dy_f32, d[v]);
-      unpack(w[v], p.weight_f32, g);
+      unpack(s[v], S32, n[v]);
+      unpack(dy[v], DY32, d[v]);
       const bool in = live && t + v * TPR < p.units;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         n[v][i] *= r;
         if (in) acc[v][i] = __builtin_fmaf(d[v][i], n[v][i], acc[v][i]);
-        d[v][i] *= g[i];
+        d[v][i] *= w[v][i];
         if (in) dot = __builtin_fmaf(d[v][i], n[v][i], dot);
       }
     }
@@ -256,13 +263,13 @@ __global__ __launch_bounds__(kGradThreads) void k_rms_norm_grad(NormGradParams p
     for (int v = 0; v < V; ++v) {
       if (!live || t + v * TPR >= p.units) continue;
       float dx[8], e[8];
-      if (p.dsum) unpack(ds[v], p.s_f32, e);
+      if (p.dsum) unpack(ds[v], S32, e);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         dx[i] = r * (d[v][i] - n[v][i] * mean);
         if (p.dsum) dx[i] += e[i];
       }
-      store_unit(p.dx, first + t + v * TPR, p.s_f32, dx);
+      store_unit(p.dx, first + t + v * TPR, S32, dx);
     }
   }
   if (p.partial == nullptr) return;
@@ -270,13 +277,15 @@ __global__ __launch_bounds__(kGradThreads) void k_rms_norm_grad(NormGradParams p
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (v * TPR >= p.units) break;
-    __syncthreads();
-    if (slot > 0) {
-      float4 *m = reinterpret_cast<float4 *>(meet) + (slot - 1) * TPR * 2 + t;
-      m[0] = make_float4(acc[v][0], acc[v][1], acc[v][2], acc[v][3]);
-      m[TPR] = make_float4(acc[v][4], acc[v][5], acc[v][6], acc[v][7]);
+    if constexpr (ROWS > 1) {
+      __syncthreads();
+      if (slot > 0) {
+        float4 *m = reinterpret_cast<float4 *>(meet) + (slot - 1) * TPR * 2 + t;
+        m[0] = make_float4(acc[v][0], acc[v][1], acc[v][2], acc[v][3]);
+        m[TPR] = make_float4(acc[v][4], acc[v][5], acc[v][6], acc[v][7]);
+      }
+      __syncthreads();
     }
-    __syncthreads();
     if (slot == 0 && t + v * TPR < p.units) {
       for (int k = 0; k < ROWS - 1; ++k) {
         const float4 *m = reinterpret_cast<const float4 *>(meet) + k * TPR * 2 + t;
@@ -295,31 +304,25 @@ __global__ __launch_bounds__(kGradThreads) void k_rms_norm_grad(NormGradParams p
   }
 }
 
-// dweight = sum of the partial sums in order: 32 columns a workgroup, 32 parts.
+// dweight = sum of the partial sums in order: 16 columns a workgroup, 64 parts.
+constexpr int kFoldCols = 16;
 __global__ __launch_bounds__(256) void k_fold_columns(const float *partial, int parts, int32_t cols, float *out) {
-  __shared__ __attribute__((aligned(16))) float4 meet[32][8];
-  const int c4 = threadIdx.x & 7, part = threadIdx.x >> 3;
-  const int32_t col = blockIdx.x * 32 + 4 * c4;
+  __shared__ __attribute__((aligned(16))) float4 meet[64][4];
+  const int c4 = threadIdx.x & 3, part = threadIdx.x >> 2;
+  const int32_t col = blockIdx.x * kFoldCols + 4 * c4;  // cols % 16 == 0
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (col < cols) {
-    for (int k = part; k < parts; k += 32) {
-      const float4 b = *reinterpret_cast<const float4 *>(partial + static_cast<int64_t>(k) * cols + col);
-      a.x += b.x;
-      a.y += b.y;
-      a.z += b.z;
-      a.w += b.w;
-    }
-  }
+  const auto add = [&](const float4 &b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+  };
+#pragma unroll 8
+  for (int k = part; k < parts; k += 64) add(*reinterpret_cast<const float4 *>(partial + static_cast<int64_t>(k) * cols + col));
   meet[part][c4] = a;
   __syncthreads();
-  if (part == 0 && col < cols) {
-    for (int k = 1; k < 32; ++k) {
-      const float4 b = meet[k][c4];
-      a.x += b.x;
-      a.y += b.y;
-      a.z += b.z;
-      a.w += b.w;
-    }
+  if (part == 0) {
+    for (int k = 1; k < 64; ++k) add(meet[k][c4]);
     *reinterpret_cast<float4 *>(out + col) = a;
   }
 }
@@ -327,19 +330,24 @@ __global__ __launch_bounds__(256) void k_fold_columns(const float *partial, int 
 // Lanes of a row: a wave where there are rows to fill the card, else four.
 bool wave_rows(int64_t rows, int32_t units) { return units <= 64 * 8 && rows >= 2048; }
 
+// In the gradient a wave has at most two units a lane.
+int grad_lanes(int64_t rows, int32_t units) { return units <= 64 * 2 && rows >= 2048 ? 64 : units <= 256 * 4 ? 256 : 512; }
+
 int grad_groups(int64_t rows, int32_t units) {
-  const int64_t per = kGradThreads / (wave_rows(rows, units) ? 64 : 256);
+  const int64_t per = kGradThreads / grad_lanes(rows, units);
   return static_cast<int>(std::min<int64_t>((rows + per - 1) / per, 512));
 }
 
-template <int TPR>
+template <bool DY32, bool S32>
 void run_norm_grad(const NormGradParams &p, int groups, hipStream_t stream) {
   const dim3 grid(groups), threads(kGradThreads);
-  const int per = (p.units + TPR - 1) / TPR;
-  if (per <= 1) hipLaunchKernelGGL((k_rms_norm_grad<TPR, 1>), grid, threads, 0, stream, p);
-  else if (per <= 2) hipLaunchKernelGGL((k_rms_norm_grad<TPR, 2>), grid, threads, 0, stream, p);
-  else if (per <= 4) hipLaunchKernelGGL((k_rms_norm_grad<TPR, 4>), grid, threads, 0, stream, p);
-  else hipLaunchKernelGGL((k_rms_norm_grad<TPR, 8>), grid, threads, 0, stream, p);
+  const int lanes = grad_lanes(p.rows, p.units), per = (p.units + lanes - 1) / lanes;
+  if (lanes == 64 && per <= 1) hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 64, 1>), grid, threads, 0, stream, p);
+  else if (lanes == 64) hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 64, 2>), grid, threads, 0, stream, p);
+  else if (lanes == 256 && per <= 1) hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 256, 1>), grid, threads, 0, stream, p);
+  else if (lanes == 256 && per <= 2) hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 256, 2>), grid, threads, 0, stream, p);
+  else if (lanes == 256) hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 256, 4>), grid, threads, 0, stream, p);
+  else hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 512, 4>), grid, threads, 0, stream, p);
 }
 
 // ---- MXFP8 back to values ----------------------------------------------------------
@@ -394,8 +402,6 @@ hipError_t launch_rms_norm_grad(const NormGradLaunch &a, hipStream_t stream) {
   p.rows = a.rows;
   p.units = a.cols / 8;
   p.cols = static_cast<float>(a.cols);
-  p.dy_f32 = a.dy_f32;
-  p.s_f32 = a.s_f32;
   p.weight_f32 = a.weight_f32;
   p.dy = a.dy;
   p.s = a.s;
@@ -406,13 +412,15 @@ hipError_t launch_rms_norm_grad(const NormGradLaunch &a, hipStream_t stream) {
   p.partial = a.dweight ? a.ws : nullptr;
   const int groups = grad_groups(a.rows, p.units);
   if (groups > 0) {
-    if (wave_rows(a.rows, p.units)) run_norm_grad<64>(p, groups, stream);
-    else run_norm_grad<256>(p, groups, stream);
+    if (a.dy_f32 && a.s_f32) run_norm_grad<true, true>(p, groups, stream);
+    else if (a.dy_f32) run_norm_grad<true, false>(p, groups, stream);
+    else if (a.s_f32) run_norm_grad<false, true>(p, groups, stream);
+    else run_norm_grad<false, false>(p, groups, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.dweight)  // of no rows: zeros
-    hipLaunchKernelGGL(k_fold_columns, dim3((a.cols + 31) / 32), dim3(256), 0, stream, a.ws, groups, a.cols, a.dweight);
+    hipLaunchKernelGGL(k_fold_columns, dim3(a.cols / kFoldCols), dim3(256), 0, stream, a.ws, groups, a.cols, a.dweight);
   return hipGetLastError();
 }
 
