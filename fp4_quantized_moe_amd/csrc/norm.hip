@@ -194,9 +194,9 @@ hipError_t run_norm(const NormParams &p, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(groups)), threads(256);
   const int per = (p.units + TPR - 1) / TPR;
   if (per <= 1) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 1>), grid, threads, 0, stream, p);
-  else if (per <= 2) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 2>), grid, threads, 0, stream, p);
-  else if (per <= 4) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 4>), grid, threads, 0, stream, p);
-  else hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 8>), grid, threads, 0, stream, p);
+  else if (per <= 2 || TPR == 64) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 2>), grid, threads, 0, stream, p);
+  else if (per <= 4) hipLaunchKernelGGL((k_rms_norm<QUANT, 256, 4>), grid, threads, 0, stream, p);
+  else hipLaunchKernelGGL((k_rms_norm<QUANT, 256, 8>), grid, threads, 0, stream, p);
   return hipGetLastError();
 }
 
@@ -327,10 +327,11 @@ __global__ __launch_bounds__(256) void k_fold_columns(const float *partial, int 
   }
 }
 
-// Lanes of a row: a wave where there are rows to fill the card, else four.
-bool wave_rows(int64_t rows, int32_t units) { return units <= 64 * 8 && rows >= 2048; }
+// Lanes of a row: a wave where it has at most two units a lane and there are
+// rows to fill the card, else four (16384 x 2048 to bf16 and MXFP8: a wave a
+// row, four units a lane, 80 us; four waves, one unit, 67).
+bool wave_rows(int64_t rows, int32_t units) { return units <= 64 * 2 && rows >= 2048; }
 
-// In the gradient a wave has at most two units a lane.
 int grad_lanes(int64_t rows, int32_t units) { return units <= 64 * 2 && rows >= 2048 ? 64 : units <= 256 * 4 ? 256 : 512; }
 
 int grad_groups(int64_t rows, int32_t units) {

@@ -434,8 +434,10 @@ hipError_t launch_route_grad(const RouteGradLaunch &a, hipStream_t stream) {
 
 hipError_t launch_combine_grad(const CombineGradLaunch &a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
-  // Four waves a token where one wave each would leave the card idle.
-  return a.T < 1024 ? run_combine_grad<4>(a, stream) : run_combine_grad<1>(a, stream);
+  // Four waves a token where one each would leave the card idle, or where all
+  // four have whole lines to read (8192 x 8 rows of 2048 198 -> 174 us, 4096 x 16
+  // of 2048 205 -> 177; but 16384 x 8 of 512 92 -> 102, of 1024 in bf16 129 -> 137).
+  return a.T < 1024 || a.N >= 2048 ? run_combine_grad<4>(a, stream) : run_combine_grad<1>(a, stream);
 }
 
 }  // namespace quads
