@@ -7,6 +7,8 @@
 
 namespace quads {
 
+constexpr int64_t kLaunchGroups = int64_t(1) << 23;  // of 256 lanes: a grid's lanes are counted in 32 bits
+
 // ---- norm.hip ------------------------------------------------------------------
 enum NormQuant { kNormQuantNone = 0, kNormQuantMx4 = 1, kNormQuantMx8 = 2 };
 

@@ -99,7 +99,7 @@ __device__ __forceinline__ void store_unit(void *p, int64_t unit, bool f32, cons
 }
 
 struct NormParams {
-  int64_t rows;
+  int64_t rows, base;  // a launch has the rows from base on
   int32_t units;  // of 8 columns
   float cols, eps;
   uint32_t add;  // MXFP4's scale rule
@@ -116,7 +116,7 @@ template <int QUANT, int TPR, int V>
 __global__ __launch_bounds__(256) void k_rms_norm(NormParams p) {
   __shared__ __attribute__((aligned(16))) float parts[4];
   const int t = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t row = TPR == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t row = p.base + (TPR == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x);
   if (TPR == 64 && row >= p.rows) return;  // whole waves, and no barrier with TPR == 64
   const int64_t first = row * p.units;
 
@@ -188,16 +188,20 @@ __global__ __launch_bounds__(256) void k_rms_norm(NormParams p) {
 }
 
 template <int QUANT, int TPR>
-hipError_t run_norm(const NormParams &p, hipStream_t stream) {
-  const int64_t groups = TPR == 64 ? (p.rows + 3) / 4 : p.rows;
-  if (groups > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 grid(static_cast<unsigned>(groups)), threads(256);
+hipError_t run_norm(NormParams p, hipStream_t stream) {
+  constexpr int64_t ROWS = 256 / TPR;  // of a workgroup
   const int per = (p.units + TPR - 1) / TPR;
-  if (per <= 1) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 1>), grid, threads, 0, stream, p);
-  else if (per <= 2 || TPR == 64) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 2>), grid, threads, 0, stream, p);
-  else if (per <= 4) hipLaunchKernelGGL((k_rms_norm<QUANT, 256, 4>), grid, threads, 0, stream, p);
-  else hipLaunchKernelGGL((k_rms_norm<QUANT, 256, 8>), grid, threads, 0, stream, p);
-  return hipGetLastError();
+  for (p.base = 0; p.base < p.rows; p.base += kLaunchGroups * ROWS) {
+    const int64_t groups = std::min((p.rows - p.base + ROWS - 1) / ROWS, kLaunchGroups);
+    const dim3 grid(static_cast<unsigned>(groups)), threads(256);
+    if (per <= 1) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 1>), grid, threads, 0, stream, p);
+    else if (per <= 2 || TPR == 64) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 2>), grid, threads, 0, stream, p);
+    else if (per <= 4) hipLaunchKernelGGL((k_rms_norm<QUANT, 256, 4>), grid, threads, 0, stream, p);
+    else hipLaunchKernelGGL((k_rms_norm<QUANT, 256, 8>), grid, threads, 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // ---- gradient --------------------------------------------------------------------
@@ -368,7 +372,6 @@ __global__ __launch_bounds__(256) void k_mx8_dequantize(const uint2 *codes, cons
 }  // namespace
 
 hipError_t launch_rms_norm(const NormLaunch &a, hipStream_t stream) {
-  if (a.rows == 0) return hipSuccess;
   NormParams p{};
   p.rows = a.rows;
   p.units = a.cols / 8;

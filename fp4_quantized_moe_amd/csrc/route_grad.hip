@@ -243,7 +243,7 @@ struct RouteGradParams {
   const int32_t *ids;
   const uint8_t *mask;
   const float *dw, *slope, *dloss;
-  int64_t T;
+  int64_t T, base;  // a launch has the tokens from base on
   int32_t E, top;
   float *dlogits;
 };
@@ -251,7 +251,7 @@ struct RouteGradParams {
 template <int LANES, int PER>
 __global__ __launch_bounds__(256) void k_route_grad(RouteGradParams p) {
   const int lane = threadIdx.x % LANES;
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t token = p.base + static_cast<int64_t>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
   const int64_t at = min(token, p.T - 1);  // lanes behind the last token take part in the DPP moves
   const bool live = p.mask == nullptr || p.mask[at] != 0;
   float l[PER], dp[PER];
@@ -288,7 +288,7 @@ struct CombineGradParams {
   const void *dout, *y;
   const int32_t *inverse;
   const float *w;
-  int64_t T, rows, N;
+  int64_t T, base, rows, N;  // a launch has the tokens from base on
   int32_t top;
   uint16_t *dy;
   float *dw;
@@ -325,7 +325,7 @@ template <int SLOTS, int WAVES, bool DOUT_BF16, bool Y_BF16>
 __global__ __launch_bounds__(256) void k_combine_grad(CombineGradParams p) {
   __shared__ float parts[4][SLOTS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, part = wave % WAVES;
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * (4 / WAVES) + wave / WAVES;
+  const int64_t token = p.base + static_cast<int64_t>(blockIdx.x) * (4 / WAVES) + wave / WAVES;
   if (WAVES == 1 && token >= p.T) return;  // whole waves; with WAVES == 4 every workgroup has a token
   const int64_t units = p.N / 8;
   int64_t row[SLOTS];
@@ -380,15 +380,19 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineGradParams p) {
 
 template <int SLOTS, int WAVES>
 hipError_t run_combine_grad(const CombineGradLaunch &a, hipStream_t stream) {
-  const CombineGradParams p{a.dout, a.y, a.inverse, a.w, a.T, a.rows, a.N, a.top, a.dy, a.dw};
-  const int64_t groups = (a.T + 4 / WAVES - 1) / (4 / WAVES);
-  if (groups > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const dim3 grid(static_cast<unsigned>(groups)), threads(256);
-  if (a.dout_bf16 && a.y_bf16) hipLaunchKernelGGL((k_combine_grad<SLOTS, WAVES, true, true>), grid, threads, 0, stream, p);
-  else if (a.dout_bf16) hipLaunchKernelGGL((k_combine_grad<SLOTS, WAVES, true, false>), grid, threads, 0, stream, p);
-  else if (a.y_bf16) hipLaunchKernelGGL((k_combine_grad<SLOTS, WAVES, false, true>), grid, threads, 0, stream, p);
-  else hipLaunchKernelGGL((k_combine_grad<SLOTS, WAVES, false, false>), grid, threads, 0, stream, p);
-  return hipGetLastError();
+  constexpr int64_t TOKENS = 4 / WAVES;  // of a workgroup
+  CombineGradParams p{a.dout, a.y, a.inverse, a.w, a.T, 0, a.rows, a.N, a.top, a.dy, a.dw};
+  for (; p.base < a.T; p.base += kLaunchGroups * TOKENS) {
+    const int64_t groups = std::min((a.T - p.base + TOKENS - 1) / TOKENS, kLaunchGroups);
+    const dim3 grid(static_cast<unsigned>(groups)), threads(256);
+    if (a.dout_bf16 && a.y_bf16) hipLaunchKernelGGL((k_combine_grad<SLOTS, WAVES, true, true>), grid, threads, 0, stream, p);
+    else if (a.dout_bf16) hipLaunchKernelGGL((k_combine_grad<SLOTS, WAVES, true, false>), grid, threads, 0, stream, p);
+    else if (a.y_bf16) hipLaunchKernelGGL((k_combine_grad<SLOTS, WAVES, false, true>), grid, threads, 0, stream, p);
+    else hipLaunchKernelGGL((k_combine_grad<SLOTS, WAVES, false, false>), grid, threads, 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int WAVES>
@@ -422,18 +426,21 @@ hipError_t launch_balance(const BalanceLaunch &a, hipStream_t stream) {
 }
 
 hipError_t launch_route_grad(const RouteGradLaunch &a, hipStream_t stream) {
-  if (a.T == 0) return hipSuccess;
-  const RouteGradParams p{a.logits, a.ids, a.mask, a.dw, a.slope, a.dloss, a.T, a.E, a.top, a.dlogits};
+  RouteGradParams p{a.logits, a.ids, a.mask, a.dw, a.slope, a.dloss, a.T, 0, a.E, a.top, a.dlogits};
+  hipError_t e = hipSuccess;
   by_experts(a.E, [&](auto lanes, auto per) {
-    constexpr int TOKENS = 256 / decltype(lanes)::value;
-    hipLaunchKernelGGL((k_route_grad<decltype(lanes)::value, decltype(per)::value>),
-                       dim3(static_cast<unsigned>((a.T + TOKENS - 1) / TOKENS)), dim3(256), 0, stream, p);
+    constexpr int64_t TOKENS = 256 / decltype(lanes)::value;
+    for (; p.base < a.T && e == hipSuccess; p.base += kLaunchGroups * TOKENS) {
+      const int64_t groups = std::min((a.T - p.base + TOKENS - 1) / TOKENS, kLaunchGroups);
+      hipLaunchKernelGGL((k_route_grad<decltype(lanes)::value, decltype(per)::value>), dim3(static_cast<unsigned>(groups)),
+                         dim3(256), 0, stream, p);
+      e = hipGetLastError();
+    }
   });
-  return hipGetLastError();
+  return e;
 }
 
 hipError_t launch_combine_grad(const CombineGradLaunch &a, hipStream_t stream) {
-  if (a.T == 0) return hipSuccess;
   // Four waves a token where one each would leave the card idle, or where all
   // four have whole lines to read (8192 x 8 rows of 2048 198 -> 174 us, 4096 x 16
   // of 2048 205 -> 177; but 16384 x 8 of 512 92 -> 102, of 1024 in bf16 129 -> 137).

@@ -572,6 +572,8 @@ quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_
  * in that format, q_codes and q_scales (MXFP4: what quads_moe_mxfp4_gemm
  * takes; flags QUADS_MX_SCALE_EVEN as in quads_quantize_mxfp4); rstd [rows]
  * fp32 receives r for the backward.  sum may be residual or x (of its type).
+ * The squares are added in fp32: a row that holds a magnitude of 2e19 or more
+ * has r = 0, one of nothing above 1e-23 r = 1 / sqrt(eps).
  *
  * MXFP8: blocks of 32 elements along the row share one E8M0 byte (as MXFP4);
  * elements are OCP E4M3 bytes [rows, cols].  A block with largest magnitude a
@@ -654,8 +656,9 @@ quads_status_t quads_rms_norm_backward(const void *dy, quads_dtype_t dy_dtype, c
  *   dw[t, j] = sum over columns of dout[t, :] y[inverse[t, j], :]  (fp32).
  * dy [T*top, N] bf16 is the dy of quads_moe_gated_backward_bf16 and
  * quads_moe_wgrad_bf16.  dw NULL: not computed, and y may be NULL.  A slot
- * whose inverse lies outside [0, T*top) has no row: its dw is 0.  N % 16 == 0,
- * top <= 16.
+ * whose inverse lies outside [0, T*top) has no row: its dw is 0.  A row that
+ * no slot names is left as it was; one that several name gets the dy of one of
+ * them (quads_moe_route names each once).  N % 16 == 0, top <= 16.
  * ------------------------------------------------------------------------- */
 size_t quads_moe_balance_loss_workspace_bytes(int64_t T, int32_t E);
 quads_status_t quads_moe_balance_loss(const float *logits, const int32_t *ids, const uint8_t *mask, int64_t T, int32_t E,
@@ -679,9 +682,9 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
  * (for rows > cols the same from the right, with X^T X), and written as bf16
  * to out [batch, rows, cols].  |g|_F is summed in 64 bits.  The products take
  * fp16 operands and add in fp32; X is kept to 22 bits between the steps (11
- * before the last), so the result is within about 2e-3 of the formula's (relative, 2-norm) before
- * its rounding to bf16, also for matrices of low rank.  coefficients: the
- * host's a, b, c.  Entries of X, A and b A + c A^2 have to stay below 31, 63
+ * before the last; entries below 2^-25 to 2^-36), so the result is within about
+ * 2e-3 of the formula's (relative, 2-norm) before its rounding to bf16, also
+ * for matrices of low rank.  coefficients: the host's a, b, c.  Entries of X, A and b A + c A^2 have to stay below 31, 63
  * and 65504 (they are below 5 for coefficients that keep the singular values
  * below 1.3, as 3.4445, -4.775, 2.0315 do); past that they become infinities
  * and NaN.  A matrix with NaN or infinities gives NaN throughout, one of zeros
@@ -690,7 +693,8 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
  * 64.  ws: quads_orthogonalize_workspace_bytes(batch, rows, cols) bytes; calls
  * in flight at the same time need a workspace each.  The order of every sum is
  * fixed: repeated calls give the same bits, and matrices of a call do not touch
- * each other; between calls of different sizes the last bits may differ.  batch == 0: nothing is launched.
+ * each other; between calls of different sizes the last bits may differ.  out
+ * may be g (BF16).  batch == 0: nothing is launched.
  * ------------------------------------------------------------------------- */
 size_t quads_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
 quads_status_t quads_orthogonalize(const void *g, quads_dtype_t dt, int64_t batch, int64_t rows, int64_t cols,
