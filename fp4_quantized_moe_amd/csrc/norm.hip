@@ -10,6 +10,10 @@
 // every element is read and written once.  A lane holds units of 8 consecutive
 // elements (16 bytes of bf16); the four lanes of an aligned quad hold a block
 // of 32, whose largest magnitude crosses the quad by two DPP permutations.
+// Measured: 16384 x 2048 (fp32 added to a bf16 stream, out in bf16 and MXFP8,
+// 370 MB) 67 us, 5.5 TB/s; the gradient of 8192 x 2048 (168 MB) 26 us and 4 for
+// the fold of dw; MXFP8 back to bf16 (102 MB) 16.5 us, 6.2 TB/s.  256 rows of
+// 2048 take 3.6 us, a launch and two trips to memory.
 #include <algorithm>
 
 #include "layer_launch.hpp"

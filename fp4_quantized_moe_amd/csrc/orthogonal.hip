@@ -18,6 +18,14 @@
 // Bound: the matrix cores, 3 m^2 n + m^3 operations a step for the short side m
 // and the long side n: A and A^2 are symmetric, and only tiles on and below the
 // diagonal are computed; each is stored a second time transposed.
+//
+// Measured, 128 matrices of 1024 x 2048 in fp32, five steps, 7.1 ms: k_square_sums
+// 208 us (1.07 GB, 5.2 TB/s), k_split 398 (2.15 GB, 5.4 TB/s); a step's A 340 us
+// (1.01 PFLOP/s with the tiles on the diagonal in full), B 214 (0.80), X 800 in
+// hi and lo (0.69; 3.0 GB at 3.8 TB/s), 697 in hi alone, 634 as the result.
+// The X products' epilogue moves its planes after a tile's products; with it
+// left out 596 us.  256 matrices of 1024 x 2048 13.9 to 14.3 ms, 128 of 2048 x
+// 1024 in bf16 6.8 to 7.0.
 #include <algorithm>
 
 #include "batched_tile.hpp"
@@ -158,7 +166,7 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
 }
 
 // Matrices of a pass: in as few even passes as keep the workspace at 2.7 GB.
-// (Two passes of 128 matrices of 1024 x 2048 take as long as one of 256.)
+// (256 matrices of 1024 x 2048 take as long in two passes as in one.)
 int64_t pass_of(int64_t batch, int64_t rows, int64_t cols) {
   const int64_t most = std::max<int64_t>(1, (int64_t(5) << 29) / layout(1, rows, cols).bytes);
   const int64_t passes = (batch + most - 1) / most;
