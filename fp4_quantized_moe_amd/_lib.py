@@ -1118,14 +1118,15 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, r
     rows, cols = dy.shape
     L = load()
     dx = torch.empty_like(s)
-    dweight = ws = None
+    dweight, ws, nbytes = None, None, 0
     if want_dweight:
         dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
-        ws = _workspace(L.quads_rms_norm_backward_workspace_bytes(rows, cols), dy.device)
+        nbytes = L.quads_rms_norm_backward_workspace_bytes(rows, cols)
+        if nbytes:  # none for few rows
+            ws = _workspace(nbytes, dy.device)
     _on_device(dy, L.quads_rms_norm_backward, what, dy.data_ptr(), dy_code, s.data_ptr(), s_code, weight.data_ptr(), w_code,
                rstd.data_ptr(), None if dsum is None else dsum.data_ptr(), rows, cols, dx.data_ptr(),
-               None if dweight is None else dweight.data_ptr(), None if ws is None else ws.data_ptr(),
-               0 if ws is None else ws.numel())
+               None if dweight is None else dweight.data_ptr(), None if ws is None else ws.data_ptr(), nbytes)
     return dx, dweight
 
 
@@ -1155,10 +1156,11 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float, mask:
     L = load()
     out = BalanceLoss(torch.empty(1, dtype=torch.float32, device=dev), torch.empty(E, dtype=torch.int32, device=dev),
                       torch.empty(E, dtype=torch.float32, device=dev))
-    ws = _workspace(L.quads_moe_balance_loss_workspace_bytes(T, E), dev)
+    nbytes = L.quads_moe_balance_loss_workspace_bytes(T, E)
+    ws = _workspace(nbytes, dev) if nbytes else None  # none for few tokens
     _on_device(logits, L.quads_moe_balance_loss, what, logits.data_ptr(), ids.data_ptr(),
                None if mask is None else mask.data_ptr(), T, E, top, coef, out.loss.data_ptr(), out.counts.data_ptr(),
-               out.slope.data_ptr(), ws.data_ptr(), ws.numel())
+               out.slope.data_ptr(), None if ws is None else ws.data_ptr(), nbytes)
     return out
 
 
@@ -1174,13 +1176,15 @@ def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dw: torch.Tensor
     for t, name, shape in ((dw, "dw", (T, top)), (slope, "slope", (E,)), (dloss, "dloss", (1,))):
         if t is not None:
             _require(what, t, name, torch.float32, logits)
-            if tuple(t.shape) != shape:
+            if t.shape != shape:
                 raise QuadsError(f"{what}: {name} must be {list(shape)}, not {list(t.shape)}")
     if dloss is not None and slope is None:
         raise QuadsError(f"{what}: dloss without slope")
     dlogits = torch.empty_like(logits)
     _on_device(logits, load().quads_moe_route_backward, what, logits.data_ptr(), ids.data_ptr(),
-               *(None if t is None else t.data_ptr() for t in (mask, dw, slope, dloss)), T, E, top, dlogits.data_ptr())
+               None if mask is None else mask.data_ptr(), None if dw is None else dw.data_ptr(),
+               None if slope is None else slope.data_ptr(), None if dloss is None else dloss.data_ptr(), T, E, top,
+               dlogits.data_ptr())
     return dlogits
 
 

@@ -218,18 +218,67 @@ struct NormGradParams {
   const void *dy, *s, *weight, *dsum;
   const float *rstd;
   void *dx;
-  float *partial;  // [gridDim.x, cols] sums of dy n, or null
+  float *partial;      // [row workgroups, cols] sums of dy n, or null
+  float *dweight;      // with column workgroups
+  int32_t col_groups;  // the first workgroups of the grid have columns of dweight, the others rows
 };
 
-constexpr int kGradThreads = 512;
+constexpr int kGradThreads = 512, kColUnits = 4;
 
-// 512 / TPR rows of a workgroup at once; workgroups stay and take rows in turn,
+// 32 columns of dweight from all rows: 128 rows at once, four such loads under way.
+template <bool DY32, bool S32>
+__device__ __forceinline__ void weight_columns(const NormGradParams &p, int block) {
+  constexpr int SLOTS = kGradThreads / kColUnits, AHEAD = 4;
+  __shared__ float meet[kGradThreads / 64][kColUnits * 8];
+  const int t = threadIdx.x, slot = t / kColUnits, unit = block * kColUnits + t % kColUnits, at = min(unit, p.units - 1);
+  float acc[8] = {};
+  for (int64_t base = slot; base < p.rows; base += AHEAD * SLOTS) {
+    Raw s[AHEAD], dy[AHEAD];
+    float r[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int64_t row = min(base + k * SLOTS, p.rows - 1);
+      s[k] = load_unit(p.s, row * p.units + at, S32);
+      dy[k] = load_unit(p.dy, row * p.units + at, DY32);
+      r[k] = p.rstd[row];
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      float n[8], d[8];
+      unpack(s[k], S32, n);
+      unpack(dy[k], DY32, d);
+      if (base + k * SLOTS < p.rows) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(d[i], n[i] * r[k], acc[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int off = kColUnits; off < 64; off *= 2) acc[i] += __shfl_xor(acc[i], off);
+    if ((t & 63) < kColUnits) meet[t >> 6][t % kColUnits * 8 + i] = acc[i];
+  }
+  __syncthreads();
+  if (t < kColUnits * 8 && block * kColUnits + t / 8 < p.units) {
+    float sum = meet[0][t];
+    for (int w = 1; w < kGradThreads / 64; ++w) sum += meet[w][t];
+    p.dweight[block * kColUnits * 8 + t] = sum;
+  }
+}
+
+// Workgroups behind those of dweight's columns.  512 / TPR rows of one at once; workgroups stay and take rows in turn,
 // their columns' weights and sums of dy n in registers.  Few units a lane, so
 // that two workgroups fit a CU: with a wave a row (8192 x 2048: four units a
 // lane, 256 registers) the kernel took 45 us.
 template <bool DY32, bool S32, int TPR, int V>
 __global__ __launch_bounds__(kGradThreads) void k_rms_norm_grad(NormGradParams p) {
   constexpr int ROWS = kGradThreads / TPR;
+  const int block = static_cast<int>(blockIdx.x) - p.col_groups, blocks = static_cast<int>(gridDim.x) - p.col_groups;
+  if (block < 0) {
+    weight_columns<DY32, S32>(p, blockIdx.x);
+    return;
+  }
   __shared__ __attribute__((aligned(16))) float parts[2][8];
   __shared__ __attribute__((aligned(16))) float meet[ROWS > 1 ? (ROWS - 1) * TPR * 8 : 1];
   const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
@@ -238,7 +287,7 @@ __global__ __launch_bounds__(kGradThreads) void k_rms_norm_grad(NormGradParams p
   for (int v = 0; v < V; ++v) unpack(load_unit(p.weight, min(t + v * TPR, p.units - 1), p.weight_f32), p.weight_f32, w[v]);
   int turn = 0;
   // Every wave makes the same number of rounds: the rows' sums contain a barrier.
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * ROWS; base < p.rows; base += static_cast<int64_t>(gridDim.x) * ROWS) {
+  for (int64_t base = static_cast<int64_t>(block) * ROWS; base < p.rows; base += static_cast<int64_t>(blocks) * ROWS) {
     const bool live = base + slot < p.rows;
     const int64_t row = live ? base + slot : p.rows - 1, first = row * p.units;
     Raw s[V], dy[V], ds[V];
@@ -307,7 +356,7 @@ __global__ __launch_bounds__(kGradThreads) void k_rms_norm_grad(NormGradParams p
         acc[v][6] += b.z;
         acc[v][7] += b.w;
       }
-      store_unit(p.partial, static_cast<int64_t>(blockIdx.x) * p.units + t + v * TPR, true, acc[v]);
+      store_unit(p.partial, static_cast<int64_t>(block) * p.units + t + v * TPR, true, acc[v]);
     }
   }
 }
@@ -346,6 +395,11 @@ int grad_groups(int64_t rows, int32_t units) {
   const int64_t per = kGradThreads / grad_lanes(rows, units);
   return static_cast<int>(std::min<int64_t>((rows + per - 1) / per, 512));
 }
+
+// dweight by workgroups of its own in the same launch, which read dy and s a
+// second time: few rows (333 x 656 in a graph 6.9 -> 3.9 us, 1024 x 2048 10.8 ->
+// 5.9, 1024 x 8192 28.8 -> 23.9; but 2047 x 2048 12.3 -> 15.0).
+bool weight_by_columns(int64_t rows) { return rows <= 1024; }
 
 template <bool DY32, bool S32>
 void run_norm_grad(const NormGradParams &p, int groups, hipStream_t stream) {
@@ -402,6 +456,7 @@ hipError_t launch_rms_norm(const NormLaunch &a, hipStream_t stream) {
 }
 
 size_t norm_grad_ws_bytes(int64_t rows, int32_t cols) {
+  if (weight_by_columns(rows)) return 0;
   return static_cast<size_t>(grad_groups(rows, cols / 8)) * cols * sizeof(float);
 }
 
@@ -417,17 +472,29 @@ hipError_t launch_rms_norm_grad(const NormGradLaunch &a, hipStream_t stream) {
   p.dsum = a.dsum;
   p.rstd = a.rstd;
   p.dx = a.dx;
-  p.partial = a.dweight ? a.ws : nullptr;
   const int groups = grad_groups(a.rows, p.units);
+  const auto run = [&](int grid) {
+    if (a.dy_f32 && a.s_f32) run_norm_grad<true, true>(p, grid, stream);
+    else if (a.dy_f32) run_norm_grad<true, false>(p, grid, stream);
+    else if (a.s_f32) run_norm_grad<false, true>(p, grid, stream);
+    else run_norm_grad<false, false>(p, grid, stream);
+    return hipGetLastError();
+  };
+  if (a.dweight && weight_by_columns(a.rows)) {
+    p.dweight = a.dweight;
+    p.col_groups = (p.units + kColUnits - 1) / kColUnits;
+    if (a.dx != a.dy) return run(p.col_groups + groups);
+    const hipError_t e = run(p.col_groups);  // before dx takes dy's place
+    if (e != hipSuccess || groups == 0) return e;
+    p.col_groups = 0;
+    return run(groups);
+  }
+  p.partial = a.dweight ? a.ws : nullptr;
   if (groups > 0) {
-    if (a.dy_f32 && a.s_f32) run_norm_grad<true, true>(p, groups, stream);
-    else if (a.dy_f32) run_norm_grad<true, false>(p, groups, stream);
-    else if (a.s_f32) run_norm_grad<false, true>(p, groups, stream);
-    else run_norm_grad<false, false>(p, groups, stream);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = run(groups);
     if (e != hipSuccess) return e;
   }
-  if (a.dweight)  // of no rows: zeros
+  if (a.dweight)
     hipLaunchKernelGGL(k_fold_columns, dim3(a.cols / kFoldCols), dim3(256), 0, stream, a.ws, groups, a.cols, a.dweight);
   return hipGetLastError();
 }

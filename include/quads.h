@@ -587,7 +587,8 @@ quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_
  * dx (of s's type) is the gradient of x and of residual alike; dsum (of s's
  * type, or NULL) is the gradient that reaches s past the norm.  The gradient
  * passes the outputs' rounding unchanged.  dweight [cols] fp32, or NULL: then
- * no workspace is needed (else quads_rms_norm_backward_workspace_bytes).  dx
+ * no workspace is needed (else quads_rms_norm_backward_workspace_bytes, 0 with
+ * few rows).  dx
  * may be dsum, or dy if of one type.  rows == 0: dweight = 0.
  * ------------------------------------------------------------------------- */
 #define QUADS_NONE (-1) /* quads_rms_norm_args.q_format: no quantized output */

@@ -165,6 +165,35 @@ def test_norm_backward(rows, cols, types):
     assert none is None and torch.equal(alone, dx)
 
 
+@pytest.mark.parametrize("rows", [1, 127, 128, 129, 511, 513, 1023, 1024, 1025, 3000])
+@pytest.mark.parametrize("cols", [16, 48, 64, 1072])
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_norm_backward_in_place(rows, cols, dtype):
+    """dx written over dy, and over dsum: what the call with a dx of its own gives, and dweight of the dy that was there;
+    rows around the number from which dweight's sums take a launch of their own.  Rows of NaN stay in their row."""
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    s, dy, dsum = (torch.randn(rows, cols, generator=gen, device="cuda").to(dtype) for _ in range(3))
+    w = torch.rand(cols, generator=gen, device="cuda") + 0.5
+    rstd = torch.rsqrt(s.float().square().mean(1) + EPS)
+    dx, dweight = Q.rms_norm_backward(dy, s, w, rstd, dsum=dsum)
+    n = host(s) * host(rstd)[:, None]
+    assert (np.abs(host(dweight) - (host(dy) * n).sum(0)) <= (rows + 4) * U * np.abs(host(dy) * n).sum(0)).all()
+    L, code = Q.load(), Q.F32 if dtype == f32 else Q.BF16
+    nbytes = L.quads_rms_norm_backward_workspace_bytes(rows, cols)
+    for target in (dy.clone(), dsum.clone()):
+        over_dy = torch.equal(target, dy)
+        ws, dw = torch.empty(nbytes + 16, dtype=torch.uint8, device="cuda"), torch.full((cols + 4,), 7.0, device="cuda")
+        st = L.quads_rms_norm_backward(target.data_ptr() if over_dy else dy.data_ptr(), code, s.data_ptr(), code, w.data_ptr(), Q.F32,
+                                       rstd.data_ptr(), dsum.data_ptr() if over_dy else target.data_ptr(), rows, cols,
+                                       target.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes, torch.cuda.current_stream().cuda_stream)
+        assert st == 0 and torch.equal(target, dx) and torch.equal(dw[:cols], dweight) and (dw[cols:] == 7).all()
+    if rows > 1:
+        dy[rows // 2] = float("nan")
+        bad, bad_w = Q.rms_norm_backward(dy, s, w, rstd, dsum=dsum)
+        keep = torch.arange(rows, device="cuda") != rows // 2
+        assert bad[rows // 2].isnan().all() and bad_w.isnan().all() and torch.equal(bad[keep], dx[keep])
+
+
 def test_norm_gradient_is_the_forwards():
     """<dx, v> against a difference of the kernel's own fp32 forward, in a direction v: h = 2^-6 |s| leaves the cubic
     term; both sides of the 64-bit difference come from the oracle, so the kernel's sum is compared with O(h^2) alone."""

@@ -55,7 +55,8 @@ def test_rms_norm_without_rows(L):
 @pytest.mark.parametrize("kw, status, word", [
     (dict(dt=2), ARG, b"dtype"), (dict(st=5), ARG, b"dtype"), (dict(cols=8), SHAPE, b"multiple of 16"),
     (dict(rows=-1), SHAPE, b"row count"), (dict(s=None), ARG, b"null"), (dict(dx=None), ARG, b"null"),
-    (dict(dsum=8), ARG, b"aligned"), (dict(ws=None), WORKSPACE, b"workspace"), (dict(nws=16), WORKSPACE, b"workspace"),
+    (dict(dsum=8), ARG, b"aligned"), (dict(rows=4000, ws=None), WORKSPACE, b"workspace"),
+    (dict(rows=4000, nws=16), WORKSPACE, b"workspace"),
 ])
 def test_rms_norm_backward(L, kw, status, word):
     d = dict(dy=P, dt=1, s=P, st=1, w=P, wt=0, rstd=P, dsum=None, rows=4, cols=64, dx=P, dw=P, ws=P, nws=1 << 20, stream=None)
@@ -65,7 +66,7 @@ def test_rms_norm_backward(L, kw, status, word):
 
 def test_rms_norm_backward_workspace(L):
     f = L.quads_rms_norm_backward_workspace_bytes
-    assert f(4, 64) >= 256 and f(0, 64) == 0 and f(4, 24) == 0 and f(-1, 64) == 0 and f(4, 1 << 20) == 0
+    assert f(4000, 64) >= 256 and f(4, 64) == 0 and f(0, 64) == 0 and f(4, 24) == 0 and f(-1, 64) == 0 and f(4, 1 << 20) == 0
     assert L.quads_rms_norm_backward(None, 1, None, 1, None, 1, None, None, 0, 64, None, None, None, 0, None) == 0
 
 
