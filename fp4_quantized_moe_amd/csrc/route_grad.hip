@@ -217,12 +217,17 @@ __global__ __launch_bounds__(kBalanceThreads) void k_balance_fold(BalanceParams 
   balance_finish(p, sum_p, sum_c, valid_tokens, parts);  // thread t reads its own sums
 }
 
-// One workgroup (and one launch) up to 512 tokens, 128 with more than 128
-// experts; then up to 128.
+// Workgroups by the rounds of tokens and the experts a lane.  One (and one
+// launch) while its rounds cost less than a second launch (512 x 16 6.9 and 7.2
+// us, 128 x 128 5.6 and 6.6; but 192 x 128 7.2 and 6.8, 512 x 128 14.3 and 6.8);
+// then up to 128, and 256 where these would make more than four rounds each
+// (65536 x 128 19.5 -> 15.9 us, 65536 x 256 44 -> 29.5; but 16384 x 128 9.6 ->
+// 10.0, 8192 x 512 16.9 -> 20.7, the fold).
 int balance_groups(int64_t T, int32_t E) {
-  const int64_t at_once = kBalanceThreads / (E <= 128 ? 16 : 64);
-  if (T <= 8 * at_once) return 1;
-  return static_cast<int>(std::min<int64_t>((T + at_once - 1) / at_once, 128));
+  const int lanes = E <= 128 ? 16 : 64, per = (E + lanes - 1) / lanes;
+  const int64_t at_once = kBalanceThreads / lanes, rounds = (T + at_once - 1) / at_once;
+  if (rounds <= 1 || (rounds <= 8 && rounds * per <= 16)) return 1;
+  return static_cast<int>(std::min<int64_t>(rounds, rounds > 4 * 128 ? 256 : 128));
 }
 
 // f(integral_constant<LANES>, integral_constant<PER>) for E experts.

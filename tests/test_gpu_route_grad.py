@@ -94,6 +94,15 @@ def test_router(T, E, top):
     assert (Q.moe_route_backward(logits, ids) == 0).all()
 
 
+@pytest.mark.parametrize("T, E, top", [(512, 16, 2), (513, 16, 2), (128, 128, 8), (129, 128, 8), (64, 200, 3), (65, 200, 3), (17, 1024, 16),
+                                       (32768, 17, 3), (32769, 17, 3), (8193, 200, 4), (9001, 1000, 2)])
+def test_balance_loss_by_one_workgroup_and_many(T, E, top):
+    """Both sides of the sizes at which one workgroup, 128 and 256 take the tokens."""
+    logits, ids, _, mask = make(T, T, E, top)
+    for m in (None, mask):
+        check_balance(logits, ids, m)
+
+
 def test_the_routers_own_choice():
     """counts are the differences of moe_route's offsets, and its weights are the probabilities differentiated."""
     logits, _, dw, _ = make(1, 3000, 64, 8)
