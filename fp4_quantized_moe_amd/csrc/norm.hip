@@ -37,21 +37,32 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// Sum over the TPR lanes of a row: a wave, or four or eight of a workgroup's
-// (`parts`: their meeting place; a barrier).
+// Sum over the TPR lanes of a row, in all of them: 16 (row rotations by 8, 4, 2
+// and 1), a wave, or several of a workgroup's (`parts`: their meeting place; a
+// barrier).
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *parts) {
+  if constexpr (TPR == 16) {
+    const auto step = [&](auto ctrl) {
+      v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    step(std::integral_constant<int, 0x128>{});
+    step(std::integral_constant<int, 0x124>{});
+    step(std::integral_constant<int, 0x122>{});
+    step(std::integral_constant<int, 0x121>{});
+    return v;
+  }
   v = wave_sum(v);
-  if constexpr (TPR == 64) return v;
+  if constexpr (TPR <= 64) return v;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (lane == 0) parts[wave] = v;
   __syncthreads();
   const float4 *row = reinterpret_cast<const float4 *>(parts + (wave & ~(TPR / 64 - 1)));
-  const float4 p = row[0];
-  v = ((p.x + p.y) + p.z) + p.w;
-  if constexpr (TPR == 512) {
-    const float4 q = row[1];
-    v = (((v + q.x) + q.y) + q.z) + q.w;
+  v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < TPR / 256; ++i) {
+    const float4 p = row[i];
+    v = (((v + p.x) + p.y) + p.z) + p.w;
   }
   return v;
 }
@@ -116,12 +127,15 @@ struct NormParams {
 };
 
 // TPR lanes a row, V units a lane.
+template <int TPR>
+constexpr int kNormThreads = TPR < 256 ? 256 : TPR;
 template <int QUANT, int TPR, int V>
-__global__ __launch_bounds__(256) void k_rms_norm(NormParams p) {
-  __shared__ __attribute__((aligned(16))) float parts[4];
-  const int t = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t row = p.base + (TPR == 64 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x);
-  if (TPR == 64 && row >= p.rows) return;  // whole waves, and no barrier with TPR == 64
+__global__ __launch_bounds__(kNormThreads<TPR>) void k_rms_norm(NormParams p) {
+  __shared__ __attribute__((aligned(16))) float parts[16];
+  constexpr int ROWS = kNormThreads<TPR> / TPR;
+  const int t = ROWS == 1 ? threadIdx.x : threadIdx.x % TPR;
+  const int64_t row = p.base + static_cast<int64_t>(blockIdx.x) * ROWS + (ROWS == 1 ? 0 : threadIdx.x / TPR);  // uniform if one
+  if (TPR < 256 && row >= p.rows) return;  // all lanes of a row, and no barrier
   const int64_t first = row * p.units;
 
   Raw x[V], res[V], w[V];
@@ -191,21 +205,34 @@ __global__ __launch_bounds__(256) void k_rms_norm(NormParams p) {
   }
 }
 
-template <int QUANT, int TPR>
+template <int QUANT, int TPR, int V>
 hipError_t run_norm(NormParams p, hipStream_t stream) {
-  constexpr int64_t ROWS = 256 / TPR;  // of a workgroup
-  const int per = (p.units + TPR - 1) / TPR;
-  for (p.base = 0; p.base < p.rows; p.base += kLaunchGroups * ROWS) {
-    const int64_t groups = std::min((p.rows - p.base + ROWS - 1) / ROWS, kLaunchGroups);
-    const dim3 grid(static_cast<unsigned>(groups)), threads(256);
-    if (per <= 1) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 1>), grid, threads, 0, stream, p);
-    else if (per <= 2 || TPR == 64) hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, 2>), grid, threads, 0, stream, p);
-    else if (per <= 4) hipLaunchKernelGGL((k_rms_norm<QUANT, 256, 4>), grid, threads, 0, stream, p);
-    else hipLaunchKernelGGL((k_rms_norm<QUANT, 256, 8>), grid, threads, 0, stream, p);
+  constexpr int64_t ROWS = kNormThreads<TPR> / TPR;  // of a workgroup
+  constexpr int64_t GROUPS = kLaunchGroups * 256 / kNormThreads<TPR>;
+  for (p.base = 0; p.base < p.rows; p.base += GROUPS * ROWS) {
+    const int64_t groups = std::min((p.rows - p.base + ROWS - 1) / ROWS, GROUPS);
+    hipLaunchKernelGGL((k_rms_norm<QUANT, TPR, V>), dim3(static_cast<unsigned>(groups)), dim3(kNormThreads<TPR>), 0, stream, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+// Lanes of a row: the fewest that leave a lane at most two units, so that many
+// rows are under way (8192 x 16384 to bf16 by 256 lanes of eight units 168 us,
+// by 1024 of two 102; 8192 x 8192 52 and 44), and 16 for the shortest (65536 x
+// 128 17 -> 7.7 us with them).  A wave a row only where there are rows to fill
+// the card, and not with four units a lane (16384 x 2048 to bf16 and MXFP8 80
+// us; four waves 67).
+template <int QUANT>
+hipError_t run_norm(const NormParams &p, hipStream_t stream) {
+  if (p.units <= 16) return run_norm<QUANT, 16, 1>(p, stream);
+  if (p.units <= 64 && p.rows >= 2048) return run_norm<QUANT, 64, 1>(p, stream);
+  if (p.units <= 128 && p.rows >= 2048) return run_norm<QUANT, 64, 2>(p, stream);
+  if (p.units <= 256) return run_norm<QUANT, 256, 1>(p, stream);
+  if (p.units <= 512) return run_norm<QUANT, 256, 2>(p, stream);
+  if (p.units <= 1024) return run_norm<QUANT, 512, 2>(p, stream);
+  return run_norm<QUANT, 1024, 2>(p, stream);
 }
 
 // ---- gradient --------------------------------------------------------------------
@@ -384,12 +411,11 @@ __global__ __launch_bounds__(256) void k_fold_columns(const float *partial, int 
   }
 }
 
-// Lanes of a row: a wave where it has at most two units a lane and there are
-// rows to fill the card, else four (16384 x 2048 to bf16 and MXFP8: a wave a
-// row, four units a lane, 80 us; four waves, one unit, 67).
-bool wave_rows(int64_t rows, int32_t units) { return units <= 64 * 2 && rows >= 2048; }
-
-int grad_lanes(int64_t rows, int32_t units) { return units <= 64 * 2 && rows >= 2048 ? 64 : units <= 256 * 4 ? 256 : 512; }
+// As the forward's lanes, but no 1024 (which spills; of 16384 columns 16 rows
+// 8.4 us, so 9.6, 8192 rows 225 and 221).
+int grad_lanes(int64_t rows, int32_t units) {
+  return units <= 16 ? 16 : units <= 128 && rows >= 2048 ? 64 : units <= 512 ? 256 : 512;
+}
 
 int grad_groups(int64_t rows, int32_t units) {
   const int64_t per = kGradThreads / grad_lanes(rows, units);
@@ -403,14 +429,20 @@ bool weight_by_columns(int64_t rows) { return rows <= 1024; }
 
 template <bool DY32, bool S32>
 void run_norm_grad(const NormGradParams &p, int groups, hipStream_t stream) {
-  const dim3 grid(groups), threads(kGradThreads);
   const int lanes = grad_lanes(p.rows, p.units), per = (p.units + lanes - 1) / lanes;
-  if (lanes == 64 && per <= 1) hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 64, 1>), grid, threads, 0, stream, p);
-  else if (lanes == 64) hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 64, 2>), grid, threads, 0, stream, p);
-  else if (lanes == 256 && per <= 1) hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 256, 1>), grid, threads, 0, stream, p);
-  else if (lanes == 256 && per <= 2) hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 256, 2>), grid, threads, 0, stream, p);
-  else if (lanes == 256) hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 256, 4>), grid, threads, 0, stream, p);
-  else hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, 512, 4>), grid, threads, 0, stream, p);
+  const auto go = [&](auto tpr, auto v) {
+    hipLaunchKernelGGL((k_rms_norm_grad<DY32, S32, decltype(tpr)::value, decltype(v)::value>), dim3(groups), dim3(kGradThreads),
+                       0, stream, p);
+  };
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 2> two;
+  if (lanes == 16) go(std::integral_constant<int, 16>{}, one);
+  else if (lanes == 64 && per <= 1) go(std::integral_constant<int, 64>{}, one);
+  else if (lanes == 64) go(std::integral_constant<int, 64>{}, two);
+  else if (lanes == 256 && per <= 1) go(std::integral_constant<int, 256>{}, one);
+  else if (lanes == 256) go(std::integral_constant<int, 256>{}, two);
+  else if (per <= 2) go(std::integral_constant<int, 512>{}, two);
+  else go(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
 }
 
 // ---- MXFP8 back to values ----------------------------------------------------------
@@ -447,11 +479,10 @@ hipError_t launch_rms_norm(const NormLaunch &a, hipStream_t stream) {
   p.codes = a.codes;
   p.scales = a.scales;
   p.rstd = a.rstd;
-  const bool wave = wave_rows(a.rows, p.units);
   switch (a.quant) {
-    case kNormQuantNone: return wave ? run_norm<kNormQuantNone, 64>(p, stream) : run_norm<kNormQuantNone, 256>(p, stream);
-    case kNormQuantMx4: return wave ? run_norm<kNormQuantMx4, 64>(p, stream) : run_norm<kNormQuantMx4, 256>(p, stream);
-    default: return wave ? run_norm<kNormQuantMx8, 64>(p, stream) : run_norm<kNormQuantMx8, 256>(p, stream);
+    case kNormQuantNone: return run_norm<kNormQuantNone>(p, stream);
+    case kNormQuantMx4: return run_norm<kNormQuantMx4>(p, stream);
+    default: return run_norm<kNormQuantMx8>(p, stream);
   }
 }
 

@@ -351,13 +351,20 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineGradParams p) {
     float d[8];
     load8<DOUT_BF16>(p.dout, token * units + u, d);
     if (dots) {
-      float y[SLOTS][8];
+      constexpr int AT_ONCE = SLOTS < 8 ? SLOTS : 8;
 #pragma unroll
-      for (int j = 0; j < SLOTS; ++j) load8<Y_BF16>(p.y, max(row[j], int64_t(0)) * units + u, y[j]);
+      for (int first = 0; first < SLOTS; first += AT_ONCE) {
+        float y[AT_ONCE][8];
 #pragma unroll
-      for (int j = 0; j < SLOTS; ++j)
+        for (int j = 0; j < AT_ONCE; ++j) load8<Y_BF16>(p.y, max(row[first + j], int64_t(0)) * units + u, y[j]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(d[i], y[j][i], dot[j]);
+        for (int j = 0; j < AT_ONCE; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[first + j] = __builtin_fmaf(d[i], y[j][i], dot[first + j]);
+        // The next eight go into the same registers: loaded ahead, 16 slots take 256
+        // of them (4096 x 16 bf16 rows of 2048 242 us, so 120).
+        if constexpr (SLOTS > AT_ONCE) __builtin_amdgcn_sched_barrier(0);
+      }
     }
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j) {

@@ -19,8 +19,8 @@ def seeded(n):
     return torch.Generator(device="cuda").manual_seed(n)
 
 
-# rows of a workgroup, columns: a wave a row and a workgroup a row
-@pytest.mark.parametrize("per, cols", [(4, 16), (1, 1040)])
+# rows of a workgroup, columns: 16 lanes, a wave and a workgroup a row
+@pytest.mark.parametrize("per, cols", [(16, 16), (4, 144), (1, 1040)])
 def test_norm_of_more_rows_than_a_launch(per, cols):
     edge = GROUPS * per
     x = torch.zeros(edge + 2501, cols, dtype=bf, device="cuda")
