@@ -1235,9 +1235,10 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
         if out.shape != g.shape:
             raise QuadsError(f"{what}: out must have g's shape")
     if ws is None:
-        ws = _workspace(L.quads_orthogonalize_workspace_bytes(batch, rows, cols), g.device)
+        nbytes = L.quads_orthogonalize_workspace_bytes(batch, rows, cols)
+        ws = _workspace(nbytes, g.device) if nbytes else None  # none for small matrices
     else:
         _require(what, ws, "ws", torch.uint8, g)
     _on_device(g, L.quads_orthogonalize, what, g.data_ptr(), code, batch, rows, cols, steps, (_c_f32 * 3)(a, b, c), eps,
-               out.data_ptr(), ws.data_ptr(), ws.numel())
+               out.data_ptr(), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return out

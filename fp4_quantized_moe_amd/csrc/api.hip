@@ -955,7 +955,7 @@ quads_status_t quads_orthogonalize(const void *g, quads_dtype_t dt, int64_t batc
   if (batch == 0) return ok();
   if (!g || !out_bf16) return fail(QUADS_ERR_ARG, "orthogonalize: null pointer");
   const size_t need = quads::orthogonalize_ws_bytes(batch, rows, cols);
-  if (ws == nullptr || ws_bytes < need)
+  if (need > 0 && (ws == nullptr || ws_bytes < need))
     return fail(QUADS_ERR_WORKSPACE, "orthogonalize: workspace too small (need %zu)", need);
   quads::OrthogonalLaunch o{};
   o.g = g;

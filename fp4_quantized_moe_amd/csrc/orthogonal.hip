@@ -30,11 +30,10 @@
 
 #include "batched_tile.hpp"
 #include "orthogonal_launch.hpp"
+#include "orthogonal_small.hpp"
 
 namespace quads {
 namespace {
-
-constexpr float kXScale = 2048.0f, kAScale = 1024.0f;
 
 // ---- normalisation -------------------------------------------------------------
 
@@ -50,30 +49,6 @@ struct SplitParams {
   uint16_t *hi, *lo;
 };
 
-__device__ __forceinline__ void load_values(const SplitParams &p, int64_t unit, float (&v)[8]) {
-  if (p.f32) {
-    const float4 *q = static_cast<const float4 *>(p.g) + 2 * unit;
-    const float4 a = q[0], b = q[1];
-    const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = w[i];
-  } else {
-    const uint4 r = static_cast<const uint4 *>(p.g)[unit];
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-}
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
-}
-
 // Part blockIdx.x of matrix blockIdx.y's sum of squares, in 64 bits: squares of
 // fp32 neither overflow nor vanish.
 __global__ __launch_bounds__(kNormThreads) void k_square_sums(SplitParams p) {
@@ -83,7 +58,7 @@ __global__ __launch_bounds__(kNormThreads) void k_square_sums(SplitParams p) {
   double s = 0.0;
   for (int64_t u = blockIdx.x * per + threadIdx.x; u < end; u += kNormThreads) {
     float v[8];
-    load_values(p, base + u, v);
+    load_values(p.g, p.f32, base + u, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += static_cast<double>(v[i]) * static_cast<double>(v[i]);
   }
@@ -108,7 +83,7 @@ __global__ __launch_bounds__(kNormThreads) void k_split(SplitParams p) {
     const int32_t row = first + static_cast<int32_t>(u / p.pad_row_units), col = static_cast<int32_t>(u % p.pad_row_units);
     float v[8] = {}, lo[8];
     if (row < p.rows && col < p.row_units) {
-      load_values(p, (static_cast<int64_t>(blockIdx.y) * p.rows + row) * p.row_units + col, v);
+      load_values(p.g, p.f32, (static_cast<int64_t>(blockIdx.y) * p.rows + row) * p.row_units + col, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(v[i] * scale);
     }
@@ -253,13 +228,64 @@ hipError_t launch_pass(const OrthogonalLaunch &o, hipStream_t stream) {
   return hipSuccess;
 }
 
+// Whether a matrix fits one workgroup's LDS, and in which kernel.
+constexpr int kSmallLds[] = {32704, 81856, 163776};  // five, two or one workgroup a CU
+
+bool small(int64_t rows, int64_t cols) {
+  const int64_t mr = (std::min(rows, cols) + 31) / 32, np = (std::max(rows, cols) + 31) / 32 * 32;
+  return mr <= 4 && small_orthogonal_lds(mr, np) <= kSmallLds[2];
+}
+
+template <int MR>
+hipError_t launch_small(const SmallOrthogonalParams &p, int64_t batch, hipStream_t stream) {
+  const int64_t need = small_orthogonal_lds(MR, p.np);
+  const dim3 grid(static_cast<unsigned>(batch)), threads(kSmallThreads);
+  constexpr int64_t LEAST = small_orthogonal_lds(MR, 32 * MR);
+  if constexpr (LEAST <= kSmallLds[0])
+    if (need <= kSmallLds[0]) {
+      hipLaunchKernelGGL((k_orthogonal_small<MR, kSmallLds[0]>), grid, threads, 0, stream, p);
+      return hipGetLastError();
+    }
+  if constexpr (LEAST <= kSmallLds[1])
+    if (need <= kSmallLds[1]) {
+      hipLaunchKernelGGL((k_orthogonal_small<MR, kSmallLds[1]>), grid, threads, 0, stream, p);
+      return hipGetLastError();
+    }
+  hipLaunchKernelGGL((k_orthogonal_small<MR, kSmallLds[2]>), grid, threads, 0, stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_small(const OrthogonalLaunch &o, hipStream_t stream) {
+  SmallOrthogonalParams p{};
+  p.g = o.g;
+  p.out = o.out;
+  p.f32 = o.g_f32;
+  p.tall = o.rows > o.cols;
+  p.rows = static_cast<int32_t>(o.rows);
+  p.cols = static_cast<int32_t>(o.cols);
+  p.np = static_cast<int32_t>((std::max(o.rows, o.cols) + 31) / 32 * 32);
+  p.steps = o.steps;
+  p.a = o.a;
+  p.b = o.b;
+  p.c = o.c;
+  p.eps = o.eps;
+  switch ((std::min(o.rows, o.cols) + 31) / 32) {
+    case 1: return launch_small<1>(p, o.batch, stream);
+    case 2: return launch_small<2>(p, o.batch, stream);
+    case 3: return launch_small<3>(p, o.batch, stream);
+    default: return launch_small<4>(p, o.batch, stream);
+  }
+}
+
 }  // namespace
 
 size_t orthogonalize_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
+  if (small(rows, cols)) return 0;
   return static_cast<size_t>(layout(pass_of(batch, rows, cols), rows, cols).bytes);
 }
 
 hipError_t launch_orthogonalize(const OrthogonalLaunch &o, hipStream_t stream) {
+  if (small(o.rows, o.cols)) return launch_small(o, stream);
   const int64_t pass = pass_of(o.batch, o.rows, o.cols), elems = o.rows * o.cols;
   for (int64_t first = 0; first < o.batch; first += pass) {
     OrthogonalLaunch part = o;

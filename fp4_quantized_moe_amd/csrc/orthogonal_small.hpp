@@ -1,0 +1,242 @@
+// All Newton-Schulz steps of one small matrix by one workgroup, in LDS.
+//
+// X (m x n, m <= n: a tall G is taken transposed) lies in LDS as hi and lo in
+// fp16, rows of n + 8, and one m x m array holds A and then B.  Scales and
+// roundings are those of the products over tiles, except that lo is kept up to
+// the last step: here it costs no traffic.  Rows and columns behind the matrix,
+// up to multiples of 32, are zeros and stay zeros.
+//
+// A wave makes 32 x 32 tiles.  A = X X^T and A^2 read rows of both operands.
+// B X reads X's columns by transposing reads as the first operand and B's rows
+// as the second, so a lane holds four neighbours of a row of X, and a wave takes
+// whole blocks of 32 columns: what it overwrites no other wave reads.
+//
+// Bound: latency (LDS reads and barriers; 4 waves of a CU that has one matrix).
+#pragma once
+
+#include "batched_tile.hpp"
+
+namespace quads {
+
+constexpr float kXScale = 2048.0f, kAScale = 1024.0f;
+
+// Unit `unit` of 8 values of fp32 or bf16.
+__device__ __forceinline__ void load_values(const void *g, bool f32, int64_t unit, float (&v)[8]) {
+  if (f32) {
+    const float4 *q = static_cast<const float4 *>(g) + 2 * unit;
+    const float4 a = q[0], b = q[1];
+    const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = w[i];
+  } else {
+    const uint4 r = static_cast<const uint4 *>(g)[unit];
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+struct SmallOrthogonalParams {
+  const void *g;
+  uint16_t *out;
+  bool f32, tall;
+  int32_t rows, cols, np;  // np: the longer side, up to a multiple of 32
+  int32_t steps;
+  float a, b, c;
+  double eps;
+};
+
+constexpr int kSmallThreads = 256;
+
+// LDS of a matrix with sides 32 mr and np.
+constexpr int64_t small_orthogonal_lds(int64_t mr, int64_t np) { return 32 * mr * (4 * (np + 8) + 2 * (32 * mr + 8)); }
+
+__device__ __forceinline__ uint2 read_lds8(uint32_t at) {
+  typedef __attribute__((address_space(3))) const u32x2 lds_u32x2;
+  const u32x2 v = *reinterpret_cast<lds_u32x2 *>(static_cast<uintptr_t>(at));
+  return make_uint2(v[0], v[1]);
+}
+__device__ __forceinline__ void write_lds8(uint32_t at, uint32_t lo, uint32_t hi) {
+  typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+  *reinterpret_cast<lds_u32x2 *>(static_cast<uintptr_t>(at)) = u32x2{lo, hi};
+}
+__device__ __forceinline__ void write_lds16(uint32_t at, uint4 v) {
+  typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+  *reinterpret_cast<lds_u32x4 *>(static_cast<uintptr_t>(at)) = u32x4{v.x, v.y, v.z, v.w};
+}
+__device__ __forceinline__ void write_lds2(uint32_t at, uint32_t v) {
+  typedef __attribute__((address_space(3))) uint16_t lds_u16;
+  *reinterpret_cast<lds_u16 *>(static_cast<uintptr_t>(at)) = static_cast<uint16_t>(v);
+}
+
+// Element i of 4 fp16 values.
+__device__ __forceinline__ float half_of(uint2 v, int i) {
+  const f16x2 p = __builtin_bit_cast(f16x2, i < 2 ? v.x : v.y);
+  return static_cast<float>(p[i & 1]);
+}
+
+template <int MR, int BYTES>
+__global__ __launch_bounds__(kSmallThreads) void k_orthogonal_small(SmallOrthogonalParams p) {
+  __shared__ __attribute__((aligned(128))) uint8_t lds[BYTES];
+  __shared__ double parts[kSmallThreads / 64];
+  constexpr int MP = 32 * MR, TILES = MR * MR, OWN = (TILES + 3) / 4;
+  constexpr uint32_t AROW = 2 * (MP + 8);
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), half = lane >> 5, fr = lane & 31;
+  const uint32_t xrow = 2 * (p.np + 8), x0 = lds_address(lds), lo = MP * xrow, a0 = x0 + 2 * lo;  // lo: from hi to lo
+
+  for (uint32_t at = 16 * t; at < 2 * lo; at += 16 * kSmallThreads) write_lds16(x0 + at, make_uint4(0, 0, 0, 0));
+  const uint32_t row_units = p.cols / 8, units = p.rows * row_units;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * units;
+  double ss = 0.0;
+  for (uint32_t u = t; u < units; u += kSmallThreads) {
+    float v[8];
+    load_values(p.g, p.f32, first + u, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += static_cast<double>(v[i]) * static_cast<double>(v[i]);
+  }
+  ss = wave_sum(ss);
+  if (lane == 0) parts[wave] = ss;
+  __syncthreads();
+  const double scale = static_cast<double>(kXScale) / (sqrt(((parts[0] + parts[1]) + parts[2]) + parts[3]) + p.eps);
+  for (uint32_t u = t; u < units; u += kSmallThreads) {
+    const uint32_t row = u / row_units, col = 8 * (u % row_units);
+    float v[8], rest[8];
+    load_values(p.g, p.f32, first + u, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(v[i] * scale);
+    split_f16(v, rest);
+    if (!p.tall) {
+      const uint32_t at = x0 + row * xrow + 2 * col;
+      write_lds16(at, make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7])));
+      write_lds16(at + lo, make_uint4(pack_f16(rest[0], rest[1]), pack_f16(rest[2], rest[3]), pack_f16(rest[4], rest[5]),
+                                      pack_f16(rest[6], rest[7])));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t at = x0 + (col + i) * xrow + 2 * row;
+        write_lds2(at, pack_f16(v[i], v[i]));
+        write_lds2(at + lo, pack_f16(rest[i], rest[i]));
+      }
+    }
+  }
+  __syncthreads();
+
+  // Tile (i, j) of rows' products: a lane has element (row 32 j + fr of the
+  // second, 8 q + 4 half + r of the first's 32 rows) in register 4 q + r.
+  const auto rows_product = [&](uint32_t at, uint32_t stride, int i, int j, int k_end) {
+    f32x16 acc = {};
+    const uint32_t x = at + (32 * i + fr) * stride + 16 * half, y = at + (32 * j + fr) * stride + 16 * half;
+    uint4 f[4] = {read_lds16(x), read_lds16(y), read_lds16(x + 32), read_lds16(y + 32)};
+    for (int k = 0; k < k_end; k += 32) {  // the next reads under way
+      const uint32_t next = k + 32 < k_end ? 2 * (k + 32) : 0;
+      const uint4 n[4] = {read_lds16(x + next), read_lds16(y + next), read_lds16(x + next + 32), read_lds16(y + next + 32)};
+      acc = mfma_f16(f[0], f[1], acc);
+      acc = mfma_f16(f[2], f[3], acc);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = n[e];
+    }
+    return acc;
+  };
+  // Byte of a lane's first four results in a row of A, and from four to four.
+  const auto a_at = [&](int i, int j) { return a0 + (32 * j + fr) * AROW + 2 * (32 * i + 4 * half); };
+
+  for (int step = 0; step < p.steps; ++step) {
+    const bool last = step + 1 == p.steps;
+    for (int tile = wave; tile < TILES; tile += 4) {
+      const int i = tile / MR, j = tile % MR;
+      const f32x16 s = rows_product(x0, xrow, i, j, p.np);
+      constexpr float alpha = kAScale / (kXScale * kXScale);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        write_lds8(a_at(i, j) + 16 * q, pack_f16(alpha * s[4 * q], alpha * s[4 * q + 1]),
+                   pack_f16(alpha * s[4 * q + 2], alpha * s[4 * q + 3]));
+    }
+    __syncthreads();
+
+    uint2 b[OWN][4];  // B takes A's place when all have read A
+    const float alpha = p.c / (kAScale * kAScale), beta = p.b / kAScale;
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      const int tile = wave + 4 * o, i = tile / MR, j = tile % MR;
+      if (tile >= TILES) continue;
+      const f32x16 s = rows_product(a0, AROW, i, j, MP);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint2 in = read_lds8(a_at(i, j) + 16 * q);
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(half_of(in, r), beta, alpha * s[4 * q + r]);
+        b[o][q] = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      const int tile = wave + 4 * o, i = tile / MR, j = tile % MR;
+      if (tile >= TILES) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) write_lds8(a_at(i, j) + 16 * q, b[o][q].x, b[o][q].y);
+    }
+    __syncthreads();
+
+    for (int block = wave; block < p.np / 32; block += 4) {
+      f32x16 acc[MR];
+#pragma unroll
+      for (int r = 0; r < MR; ++r) acc[r] = f32x16{};
+      // Lane 16 g + 4 j + b of a transposing read addresses row j and columns 4 (4 (g % 2) + b) .. of the block, in half g / 2.
+      const uint32_t x = x0 + (8 * half + ((lane >> 2) & 3)) * xrow + 2 * (32 * block + 4 * (4 * ((lane >> 4) & 1) + (lane & 3)));
+#pragma unroll
+      for (int k = 0; k < MP; k += 16) {
+        const uint2 u = read_tr_at(x + k * xrow), v = read_tr_at(x + (k + 4) * xrow);
+#pragma unroll
+        for (int r = 0; r < MR; ++r)
+          acc[r] = mfma_f16(make_uint4(u.x, u.y, v.x, v.y), read_lds16(a0 + (32 * r + fr) * AROW + 2 * k + 16 * half), acc[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < MR; ++r) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = 32 * r + fr, col = 32 * block + 8 * q + 4 * half;
+          const uint32_t at = x0 + row * xrow + 2 * col;
+          const uint2 h = read_lds8(at), l = read_lds8(at + lo);
+          float v[4], rest[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = __builtin_fmaf(half_of(l, e), p.a, __builtin_fmaf(half_of(h, e), p.a, acc[r][4 * q + e]));
+          if (!last) {
+            split_f16(v, rest);
+            write_lds8(at, pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+            write_lds8(at + lo, pack_f16(rest[0], rest[1]), pack_f16(rest[2], rest[3]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= 1.0f / kXScale;
+            const uint32_t w0 = pack_bf16(v[0], v[1]), w1 = pack_bf16(v[2], v[3]);
+            uint16_t *out = p.out + 8 * first;
+            if (!p.tall) {
+              if (row < p.rows && col < p.cols)
+                *reinterpret_cast<u32x2 *>(out + static_cast<int64_t>(row) * p.cols + col) = u32x2{w0, w1};
+            } else if (row < p.cols && col < p.rows) {
+              uint16_t *to = out + static_cast<int64_t>(col) * p.cols + row;
+              to[0] = static_cast<uint16_t>(w0);
+              to[p.cols] = static_cast<uint16_t>(w0 >> 16);
+              to[2 * p.cols] = static_cast<uint16_t>(w1);
+              to[3 * p.cols] = static_cast<uint16_t>(w1 >> 16);
+            }
+          }
+        }
+      }
+    }
+    if (!last) __syncthreads();
+  }
+}
+
+}  // namespace quads

@@ -74,6 +74,36 @@ def test_one_step_bit_for_bit(batch, rows, cols, step):
     assert torch.equal(Q.orthogonalize(x.float() * 2.0 ** -100, steps=1, coefficients=coefficients, eps=0.0), want)
 
 
+# Both sides of the sizes that one workgroup holds, and of those of which five, two and one fit a CU.
+SMALL = [(16, 16), (32, 32), (32, 224), (32, 240), (16, 608), (32, 624), (32, 1248), (32, 1264), (48, 48), (64, 64), (64, 80), (48, 256),
+         (64, 272), (64, 576), (64, 592), (96, 96), (96, 128), (80, 144), (96, 352), (96, 368), (128, 128), (112, 224), (128, 224), (128, 240),
+         (144, 144)]
+SMALL += [(c, r) for r, c in SMALL if r != c]
+
+
+@gpu
+@pytest.mark.parametrize("rows, cols", SMALL)
+def test_small_matrices(rows, cols):
+    for step in ((0.0, 1, 0), (0.0, 0, 1), (1.0, 1, -1)):
+        test_one_step_bit_for_bit(3, rows, cols, step)
+    test_steps_that_keep_the_matrix(2, rows, cols)
+    test_several_steps(3, rows, cols, 2 * min(rows, cols), torch.float32)
+    test_several_steps(2, rows, cols, max(4, min(rows, cols) // 4), torch.bfloat16)
+
+
+@gpu
+def test_many_small_matrices():
+    """More matrices than the card holds workgroups; each has the bits that it has alone, on the side of other values."""
+    for rows, cols in ((32, 96), (96, 32), (128, 208)):
+        g = gradient(9, 3000, rows, cols, 40, "cuda")
+        g[7], g[8, 3, 5] = 0, float("nan")
+        got = Q.orthogonalize(g)
+        assert (got[7] == 0).all() and got[8].isnan().all() and got[9:].isfinite().all()
+        for i in (0, 6, 9, 1500, 2999):
+            assert torch.equal(Q.orthogonalize(g[i]), got[i])
+        assert relative(got[9:40], formula(g[9:40], 5, MUON, 1e-7)) <= 3 * relative(emulated(g[9:40], 5, MUON, 1e-7), formula(g[9:40], 5, MUON, 1e-7)) + 2.0 ** -8
+
+
 @gpu
 @pytest.mark.parametrize("batch, rows, cols", [(2, 64, 96), (2, 96, 64), (6, 272, 400), (6, 400, 272), (70, 512, 528), (70, 528, 512)])
 def test_steps_that_keep_the_matrix(batch, rows, cols):

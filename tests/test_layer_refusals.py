@@ -148,7 +148,7 @@ def test_binding_refuses_cpu_tensors():
     (dict(ws=None), WORKSPACE, b"workspace"), (dict(nws=1000), WORKSPACE, b"workspace"),
 ])
 def test_orthogonalize(L, kw, status, word):
-    d = dict(g=P, dt=0, batch=2, rows=32, cols=48, steps=5, co=(ctypes.c_float * 3)(3.4, -4.8, 2.0), eps=1e-7, out=P, ws=P,
+    d = dict(g=P, dt=0, batch=2, rows=160, cols=208, steps=5, co=(ctypes.c_float * 3)(3.4, -4.8, 2.0), eps=1e-7, out=P, ws=P,
              nws=1 << 20, stream=None)
     assert L.quads_orthogonalize(*{**d, **kw}.values()) == status
     assert word in L.quads_last_error()
@@ -156,7 +156,8 @@ def test_orthogonalize(L, kw, status, word):
 
 def test_orthogonalize_without_matrices(L):
     f = L.quads_orthogonalize_workspace_bytes
-    assert f(2, 32, 48) >= 2 * (3 * 32 * 48 + 2 * 32 * 32) * 2 and f(0, 32, 48) == 0 and f(2, 24, 48) == 0
+    assert f(2, 160, 208) >= 2 * (3 * 160 * 208 + 2 * 160 * 160) * 2 and f(0, 160, 208) == 0 and f(2, 24, 48) == 0
+    assert f(2, 32, 48) == 0  # a workgroup's LDS holds it
     assert L.quads_orthogonalize(None, 0, 0, 32, 48, 5, (ctypes.c_float * 3)(1, 1, 1), 0.0, None, None, 0, None) == 0
     with pytest.raises(Q.QuadsError, match="contiguous and on the GPU"):
         Q.orthogonalize(torch.zeros(32, 32))
