@@ -229,30 +229,34 @@ hipError_t launch_pass(const OrthogonalLaunch &o, hipStream_t stream) {
 }
 
 // Whether a matrix fits one workgroup's LDS, and in which kernel.
-constexpr int kSmallLds[] = {32704, 81856, 163776};  // five, two or one workgroup a CU
+constexpr int kSmallLds[] = {32640, 81792, 163712};  // five, two or one workgroup a CU, with the partial sums
 
 bool small(int64_t rows, int64_t cols) {
   const int64_t mr = (std::min(rows, cols) + 31) / 32, np = (std::max(rows, cols) + 31) / 32 * 32;
   return mr <= 4 && small_orthogonal_lds(mr, np) <= kSmallLds[2];
 }
 
+template <int MR, int CLASS>
+hipError_t launch_small(const SmallOrthogonalParams &p, int64_t batch, hipStream_t stream) {
+  if constexpr (small_orthogonal_lds(MR, 32 * MR) <= kSmallLds[CLASS]) {
+    // Eight waves where a CU has one matrix (one of 128 x 224 60 us with four, so 37;
+    // one of 32 x 224 16 and 12; sixteen 67 and 12), four where it has several (2000
+    // of 96 x 128 192 with eight, so 149).
+    constexpr int MANY = CLASS == 2 ? 8 : 4, FEW = 8;
+    const dim3 grid(static_cast<unsigned>(batch));
+    if (batch <= 256) hipLaunchKernelGGL((k_orthogonal_small<MR, kSmallLds[CLASS], FEW>), grid, dim3(64 * FEW), 0, stream, p);
+    else hipLaunchKernelGGL((k_orthogonal_small<MR, kSmallLds[CLASS], MANY>), grid, dim3(64 * MANY), 0, stream, p);
+    return hipGetLastError();
+  }
+  return hipErrorInvalidConfiguration;  // no such size
+}
+
 template <int MR>
 hipError_t launch_small(const SmallOrthogonalParams &p, int64_t batch, hipStream_t stream) {
   const int64_t need = small_orthogonal_lds(MR, p.np);
-  const dim3 grid(static_cast<unsigned>(batch)), threads(kSmallThreads);
-  constexpr int64_t LEAST = small_orthogonal_lds(MR, 32 * MR);
-  if constexpr (LEAST <= kSmallLds[0])
-    if (need <= kSmallLds[0]) {
-      hipLaunchKernelGGL((k_orthogonal_small<MR, kSmallLds[0]>), grid, threads, 0, stream, p);
-      return hipGetLastError();
-    }
-  if constexpr (LEAST <= kSmallLds[1])
-    if (need <= kSmallLds[1]) {
-      hipLaunchKernelGGL((k_orthogonal_small<MR, kSmallLds[1]>), grid, threads, 0, stream, p);
-      return hipGetLastError();
-    }
-  hipLaunchKernelGGL((k_orthogonal_small<MR, kSmallLds[2]>), grid, threads, 0, stream, p);
-  return hipGetLastError();
+  if (need <= kSmallLds[0]) return launch_small<MR, 0>(p, batch, stream);
+  if (need <= kSmallLds[1]) return launch_small<MR, 1>(p, batch, stream);
+  return launch_small<MR, 2>(p, batch, stream);
 }
 
 hipError_t launch_small(const OrthogonalLaunch &o, hipStream_t stream) {

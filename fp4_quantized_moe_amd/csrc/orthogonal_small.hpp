@@ -11,7 +11,9 @@
 // as the second, so a lane holds four neighbours of a row of X, and a wave takes
 // whole blocks of 32 columns: what it overwrites no other wave reads.
 //
-// Bound: latency (LDS reads and barriers; 4 waves of a CU that has one matrix).
+// Bound: latency (LDS reads, and four barriers a step).  Five steps of one 32 x
+// 32 take 8 us, of 256 of 64 x 128 18, of one 128 x 224 38, of 2000 of 128 x
+// 128 293 (0.29 PFLOP/s); by products over tiles 87, 118, 89 and 724.
 #pragma once
 
 #include "batched_tile.hpp"
@@ -55,8 +57,6 @@ struct SmallOrthogonalParams {
   double eps;
 };
 
-constexpr int kSmallThreads = 256;
-
 // LDS of a matrix with sides 32 mr and np.
 constexpr int64_t small_orthogonal_lds(int64_t mr, int64_t np) { return 32 * mr * (4 * (np + 8) + 2 * (32 * mr + 8)); }
 
@@ -84,20 +84,20 @@ __device__ __forceinline__ float half_of(uint2 v, int i) {
   return static_cast<float>(p[i & 1]);
 }
 
-template <int MR, int BYTES>
-__global__ __launch_bounds__(kSmallThreads) void k_orthogonal_small(SmallOrthogonalParams p) {
+template <int MR, int BYTES, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_orthogonal_small(SmallOrthogonalParams p) {
   __shared__ __attribute__((aligned(128))) uint8_t lds[BYTES];
-  __shared__ double parts[kSmallThreads / 64];
-  constexpr int MP = 32 * MR, TILES = MR * MR, OWN = (TILES + 3) / 4;
+  __shared__ double parts[WAVES];
+  constexpr int MP = 32 * MR, TILES = MR * MR, OWN = (TILES + WAVES - 1) / WAVES, THREADS = 64 * WAVES;
   constexpr uint32_t AROW = 2 * (MP + 8);
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), half = lane >> 5, fr = lane & 31;
   const uint32_t xrow = 2 * (p.np + 8), x0 = lds_address(lds), lo = MP * xrow, a0 = x0 + 2 * lo;  // lo: from hi to lo
 
-  for (uint32_t at = 16 * t; at < 2 * lo; at += 16 * kSmallThreads) write_lds16(x0 + at, make_uint4(0, 0, 0, 0));
+  for (uint32_t at = 16 * t; at < 2 * lo; at += 16 * THREADS) write_lds16(x0 + at, make_uint4(0, 0, 0, 0));
   const uint32_t row_units = p.cols / 8, units = p.rows * row_units;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * units;
   double ss = 0.0;
-  for (uint32_t u = t; u < units; u += kSmallThreads) {
+  for (uint32_t u = t; u < units; u += THREADS) {
     float v[8];
     load_values(p.g, p.f32, first + u, v);
 #pragma unroll
@@ -106,8 +106,10 @@ __global__ __launch_bounds__(kSmallThreads) void k_orthogonal_small(SmallOrthogo
   ss = wave_sum(ss);
   if (lane == 0) parts[wave] = ss;
   __syncthreads();
-  const double scale = static_cast<double>(kXScale) / (sqrt(((parts[0] + parts[1]) + parts[2]) + parts[3]) + p.eps);
-  for (uint32_t u = t; u < units; u += kSmallThreads) {
+  ss = parts[0];
+  for (int w = 1; w < WAVES; ++w) ss += parts[w];
+  const double scale = static_cast<double>(kXScale) / (sqrt(ss) + p.eps);
+  for (uint32_t u = t; u < units; u += THREADS) {
     const uint32_t row = u / row_units, col = 8 * (u % row_units);
     float v[8], rest[8];
     load_values(p.g, p.f32, first + u, v);
@@ -151,7 +153,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_orthogonal_small(SmallOrthogo
 
   for (int step = 0; step < p.steps; ++step) {
     const bool last = step + 1 == p.steps;
-    for (int tile = wave; tile < TILES; tile += 4) {
+    for (int tile = wave; tile < TILES; tile += WAVES) {
       const int i = tile / MR, j = tile % MR;
       const f32x16 s = rows_product(x0, xrow, i, j, p.np);
       constexpr float alpha = kAScale / (kXScale * kXScale);
@@ -166,7 +168,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_orthogonal_small(SmallOrthogo
     const float alpha = p.c / (kAScale * kAScale), beta = p.b / kAScale;
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
-      const int tile = wave + 4 * o, i = tile / MR, j = tile % MR;
+      const int tile = wave + WAVES * o, i = tile / MR, j = tile % MR;
       if (tile >= TILES) continue;
       const f32x16 s = rows_product(a0, AROW, i, j, MP);
 #pragma unroll
@@ -181,14 +183,14 @@ __global__ __launch_bounds__(kSmallThreads) void k_orthogonal_small(SmallOrthogo
     __syncthreads();
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
-      const int tile = wave + 4 * o, i = tile / MR, j = tile % MR;
+      const int tile = wave + WAVES * o, i = tile / MR, j = tile % MR;
       if (tile >= TILES) continue;
 #pragma unroll
       for (int q = 0; q < 4; ++q) write_lds8(a_at(i, j) + 16 * q, b[o][q].x, b[o][q].y);
     }
     __syncthreads();
 
-    for (int block = wave; block < p.np / 32; block += 4) {
+    for (int block = wave; block < p.np / 32; block += WAVES) {
       f32x16 acc[MR];
 #pragma unroll
       for (int r = 0; r < MR; ++r) acc[r] = f32x16{};
