@@ -19,10 +19,10 @@
 // and the long side n: A and A^2 are symmetric, and only tiles on and below the
 // diagonal are computed; each is stored a second time transposed.
 //
-// Measured, 128 matrices of 1024 x 2048 in fp32, five steps, 7.1 ms: k_square_sums
-// 208 us (1.07 GB, 5.2 TB/s), k_split 398 (2.15 GB, 5.4 TB/s); a step's A 340 us
-// (1.01 PFLOP/s with the tiles on the diagonal in full), B 214 (0.80), X 800 in
-// hi and lo (0.69; 3.0 GB at 3.8 TB/s), 697 in hi alone, 634 as the result.
+// Measured, 128 matrices of 1024 x 2048 in fp32, five steps, 7.0 ms: k_square_sums
+// 204 us (1.07 GB, 5.3 TB/s), k_split 398 (2.15 GB, 5.4 TB/s); a step's A 333 us
+// (1.03 PFLOP/s with the tiles on the diagonal in full), B 208 (0.83), X 785 in
+// hi and lo (0.70; 3.0 GB at 3.8 TB/s), 671 in hi alone, 632 as the result.
 // The X products' epilogue moves its planes after a tile's products; with it
 // left out 596 us.  256 matrices of 1024 x 2048 13.9 to 14.3 ms, 128 of 2048 x
 // 1024 in bf16 6.8 to 7.0.

@@ -13,9 +13,9 @@
 // token's logits are held by LANES lanes (16 up to 128 experts, so that a wave
 // has four tokens and their reductions are four DPP steps; else a wave), PER
 // experts a lane: expert q LANES + lane.  Measured: 8192 tokens of 128 experts
-// (4.5 MB read, as much written by the gradient) 4.8 us for k_balance, 4.0 for
+// (4.5 MB read, as much written by the gradient) 4.9 us for k_balance, 4.0 for
 // its fold, 5.9 for k_route_grad, a launch and memory's latency each; 8192 x 8
-// rows of 2048 (873 MB) 174 us for k_combine_grad, 5.0 TB/s, the rate of a copy.
+// rows of 2048 (873 MB) 173 us for k_combine_grad, 5.0 TB/s, the rate of a copy.
 #include <algorithm>
 #include <type_traits>
 
