@@ -78,9 +78,51 @@ def test_norm_of_rows_whose_squares_leave_fp32(rows):
     assert (Q.rms_norm(x, w).y[2] == torch.tensor(1e-30 * 1e3, device="cuda").to(bf)).all()  # eps = 1e-6 alone
 
 
-@pytest.mark.parametrize("batch, rows, cols", [(3, 144, 208), (2, 208, 144), (150, 1024, 2048)])
+@pytest.mark.parametrize("batch, rows, cols", [(3, 144, 208), (2, 208, 144), (150, 1024, 2048), (3, 32, 96), (300, 96, 32)])
 def test_orthogonalize_in_place(batch, rows, cols):
     """out may be g, also where the batch takes two passes."""
     g = torch.randn(batch, rows, cols, generator=seeded(6), device="cuda").to(bf)
     want = Q.orthogonalize(g, steps=2)
     assert Q.orthogonalize(g, steps=2, out=g) is g and torch.equal(g, want)
+
+
+@pytest.mark.parametrize("batch, rows, cols", [(4, 272, 528), (1, 1024, 1040), (5, 64, 96), (300, 96, 64)])
+def test_orthogonalize_in_graphs_that_share_a_workspace(batch, rows, cols):
+    """Two captured calls with one workspace, replayed in turn, and again with other values in the captured inputs."""
+    gs = [torch.randn(batch, rows, cols, generator=seeded(10 + i), device="cuda") for i in range(2)]
+    outs = [torch.empty(batch, rows, cols, dtype=bf, device="cuda") for _ in gs]
+    ws = torch.empty(max(Q.orthogonalize_workspace_bytes(batch, rows, cols), 16), dtype=torch.uint8, device="cuda")
+    want = [Q.orthogonalize(g) for g in gs]
+    torch.cuda.synchronize()
+    graphs = []
+    for g, out in zip(gs, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            Q.orthogonalize(g, out=out, ws=ws)
+        graphs.append(graph)
+    for _ in range(3):
+        for out in outs:
+            out.fill_(3)
+        ws.random_(0, 256)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    gs[0].copy_(gs[1])
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[1])
+
+
+def test_small_matrices_on_two_streams():
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    gs = [torch.randn(700, 48, 160, generator=seeded(20 + i), device="cuda") for i in range(2)]
+    want = [Q.orthogonalize(g) for g in gs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = []
+        for g, s in zip(gs, sides):
+            with torch.cuda.stream(s):
+                got.append(Q.orthogonalize(g))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
