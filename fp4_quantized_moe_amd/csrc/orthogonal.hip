@@ -140,14 +140,6 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
   return l;
 }
 
-// Matrices of a pass: in as few even passes as keep the workspace at 2.7 GB.
-// (256 matrices of 1024 x 2048 take as long in two passes as in one.)
-int64_t pass_of(int64_t batch, int64_t rows, int64_t cols) {
-  const int64_t most = std::max<int64_t>(1, (int64_t(5) << 29) / layout(1, rows, cols).bytes);
-  const int64_t passes = (batch + most - 1) / most;
-  return (batch + passes - 1) / passes;
-}
-
 hipError_t launch_pass(const OrthogonalLaunch &o, hipStream_t stream) {
   const int64_t rows = o.rows, cols = o.cols;
   const bool tall = rows > cols;
@@ -259,7 +251,7 @@ hipError_t launch_small(const SmallOrthogonalParams &p, int64_t batch, hipStream
   return launch_small<MR, 2>(p, batch, stream);
 }
 
-hipError_t launch_small(const OrthogonalLaunch &o, hipStream_t stream) {
+SmallOrthogonalParams small_params(const OrthogonalLaunch &o, int64_t np) {
   SmallOrthogonalParams p{};
   p.g = o.g;
   p.out = o.out;
@@ -267,12 +259,17 @@ hipError_t launch_small(const OrthogonalLaunch &o, hipStream_t stream) {
   p.tall = o.rows > o.cols;
   p.rows = static_cast<int32_t>(o.rows);
   p.cols = static_cast<int32_t>(o.cols);
-  p.np = static_cast<int32_t>((std::max(o.rows, o.cols) + 31) / 32 * 32);
+  p.np = static_cast<int32_t>(np);
   p.steps = o.steps;
   p.a = o.a;
   p.b = o.b;
   p.c = o.c;
   p.eps = o.eps;
+  return p;
+}
+
+hipError_t launch_small(const OrthogonalLaunch &o, hipStream_t stream) {
+  const SmallOrthogonalParams p = small_params(o, (std::max(o.rows, o.cols) + 31) / 32 * 32);
   switch ((std::min(o.rows, o.cols) + 31) / 32) {
     case 1: return launch_small<1>(p, o.batch, stream);
     case 2: return launch_small<2>(p, o.batch, stream);
@@ -281,10 +278,94 @@ hipError_t launch_small(const OrthogonalLaunch &o, hipStream_t stream) {
   }
 }
 
+// Slabs of a matrix with a short side of up to 128 rows that is no small one.
+struct Slabs {
+  int64_t mr, np, slabs;
+  int64_t x, gram[2], partial, bytes;  // workspace
+};
+
+// Columns of a slab, by 32 mr rows: two workgroups a CU, from 96 rows on one.
+constexpr int64_t kSlabColumns[] = {0, 256, 128, 128, 128};
+
+Slabs slabs_of(int64_t batch, int64_t rows, int64_t cols) {
+  Slabs l{};
+  l.mr = (std::min(rows, cols) + 31) / 32;
+  l.np = kSlabColumns[l.mr];
+  l.slabs = (std::max(rows, cols) + l.np - 1) / l.np;
+  const int64_t gram = up256(4 * batch * l.slabs * 32 * l.mr * 32 * l.mr);
+  l.gram[0] = up256(4 * batch * l.slabs * 32 * l.mr * l.np);
+  l.gram[1] = l.gram[0] + gram;
+  l.partial = l.gram[1] + gram;
+  l.bytes = l.partial + up256(8 * batch * parts_of(batch, rows * cols / 8));
+  return l;
+}
+
+// By tiles a short side is padded to 128, and a step takes three launches; in
+// slabs every one of them makes B anew.  Five steps of one 32 x 2048 127 us by
+// tiles, 40 in slabs; of 256 903 and 240; of one 64 x 2048 125 and 58, of 256
+// 925 and 796; of one 128 x 512 95 and 68, of 16 96 and 83, but of 64 114 and 124.
+bool in_slabs(int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t mr = (std::min(rows, cols) + 31) / 32;
+  if (mr > 4 || small(rows, cols)) return false;
+  const int64_t slabs = slabs_of(1, rows, cols).slabs;
+  return mr <= 2 ? slabs <= 32 : batch * slabs <= 128 && slabs <= 16;
+}
+
+// Matrices of a pass: in as few even passes as keep the workspace at 2.7 GB.
+// (256 matrices of 1024 x 2048 take as long in two passes as in one.)
+int64_t pass_of(int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t most = std::max<int64_t>(1, (int64_t(5) << 29) / (in_slabs(batch, rows, cols) ? slabs_of(1, rows, cols).bytes : layout(1, rows, cols).bytes));
+  const int64_t passes = (batch + most - 1) / most;
+  return (batch + passes - 1) / passes;
+}
+
+template <int MR>
+hipError_t launch_slabs(const OrthogonalLaunch &o, hipStream_t stream) {
+  constexpr int CLASS = MR <= 2 ? 1 : 2;
+  static_assert(small_orthogonal_lds(MR, kSlabColumns[MR]) <= kSmallLds[CLASS], "a slab has to fit");
+  const Slabs l = slabs_of(o.batch, o.rows, o.cols);
+  uint8_t *ws = static_cast<uint8_t *>(o.ws);
+  SplitParams s{};
+  s.g = o.g;
+  s.f32 = o.g_f32;
+  s.rows = static_cast<int32_t>(o.rows);
+  s.row_units = static_cast<int32_t>(o.cols / 8);
+  s.partial = reinterpret_cast<double *>(ws + l.partial);
+  const int parts = parts_of(o.batch, o.rows * o.cols / 8);
+  hipLaunchKernelGGL(k_square_sums, dim3(parts, static_cast<unsigned>(o.batch)), dim3(kNormThreads), 0, stream, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  SlabParams p{};
+  p.m = small_params(o, l.np);
+  p.slabs = static_cast<int32_t>(l.slabs);
+  p.parts = parts;
+  p.partial = s.partial;
+  p.x = reinterpret_cast<uint4 *>(ws);
+  for (p.phase = 0; p.phase <= o.steps; ++p.phase) {
+    p.gram = reinterpret_cast<const float4 *>(ws + l.gram[(p.phase + 1) & 1]);
+    p.next_gram = reinterpret_cast<float4 *>(ws + l.gram[p.phase & 1]);
+    hipLaunchKernelGGL((k_orthogonal_slab<MR, kSmallLds[CLASS], 8>), dim3(static_cast<unsigned>(o.batch * l.slabs)), dim3(512), 0,
+                       stream, p);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_slabs(const OrthogonalLaunch &o, hipStream_t stream) {
+  switch ((std::min(o.rows, o.cols) + 31) / 32) {
+    case 1: return launch_slabs<1>(o, stream);
+    case 2: return launch_slabs<2>(o, stream);
+    case 3: return launch_slabs<3>(o, stream);
+    default: return launch_slabs<4>(o, stream);
+  }
+}
+
 }  // namespace
 
 size_t orthogonalize_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
   if (small(rows, cols)) return 0;
+  if (in_slabs(batch, rows, cols)) return static_cast<size_t>(slabs_of(pass_of(batch, rows, cols), rows, cols).bytes);
   return static_cast<size_t>(layout(pass_of(batch, rows, cols), rows, cols).bytes);
 }
 
@@ -296,7 +377,7 @@ hipError_t launch_orthogonalize(const OrthogonalLaunch &o, hipStream_t stream) {
     part.batch = std::min(pass, o.batch - first);
     part.g = static_cast<const uint8_t *>(o.g) + first * elems * (o.g_f32 ? 4 : 2);
     part.out = o.out + first * elems;
-    const hipError_t e = launch_pass(part, stream);
+    const hipError_t e = in_slabs(o.batch, o.rows, o.cols) ? launch_slabs(part, stream) : launch_pass(part, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

@@ -84,39 +84,29 @@ __device__ __forceinline__ float half_of(uint2 v, int i) {
   return static_cast<float>(p[i & 1]);
 }
 
-template <int MR, int BYTES, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_orthogonal_small(SmallOrthogonalParams p) {
-  __shared__ __attribute__((aligned(128))) uint8_t lds[BYTES];
-  __shared__ double parts[WAVES];
-  constexpr int MP = 32 * MR, TILES = MR * MR, OWN = (TILES + WAVES - 1) / WAVES, THREADS = 64 * WAVES;
-  constexpr uint32_t AROW = 2 * (MP + 8);
-  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), half = lane >> 5, fr = lane & 31;
-  const uint32_t xrow = 2 * (p.np + 8), x0 = lds_address(lds), lo = MP * xrow, a0 = x0 + 2 * lo;  // lo: from hi to lo
+// X of 32 MR rows and np columns as hi and lo, and one array for A and B.
+template <int MR, int WAVES>
+struct SmallMatrix {
+  static constexpr int MP = 32 * MR, TILES = MR * MR, OWN = (TILES + WAVES - 1) / WAVES, THREADS = 64 * WAVES;
+  static constexpr uint32_t AROW = 2 * (MP + 8);
+  int np, wave, lane, half, fr;
+  uint32_t x0, xrow, lo, a0;  // lo: from hi to lo
 
-  for (uint32_t at = 16 * t; at < 2 * lo; at += 16 * THREADS) write_lds16(x0 + at, make_uint4(0, 0, 0, 0));
-  const uint32_t row_units = p.cols / 8, units = p.rows * row_units;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * units;
-  double ss = 0.0;
-  for (uint32_t u = t; u < units; u += THREADS) {
-    float v[8];
-    load_values(p.g, p.f32, first + u, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += static_cast<double>(v[i]) * static_cast<double>(v[i]);
+  __device__ __forceinline__ SmallMatrix(uint32_t at, int columns)
+      : np(columns), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), lane(threadIdx.x & 63), half(lane >> 5),
+        fr(lane & 31), x0(at), xrow(2 * (columns + 8)), lo(MP * xrow), a0(at + 2 * lo) {}
+
+  __device__ __forceinline__ void clear() const {
+    for (uint32_t at = 16 * threadIdx.x; at < 2 * lo; at += 16 * THREADS) write_lds16(x0 + at, make_uint4(0, 0, 0, 0));
   }
-  ss = wave_sum(ss);
-  if (lane == 0) parts[wave] = ss;
-  __syncthreads();
-  ss = parts[0];
-  for (int w = 1; w < WAVES; ++w) ss += parts[w];
-  const double scale = static_cast<double>(kXScale) / (sqrt(ss) + p.eps);
-  for (uint32_t u = t; u < units; u += THREADS) {
-    const uint32_t row = u / row_units, col = 8 * (u % row_units);
-    float v[8], rest[8];
-    load_values(p.g, p.f32, first + u, v);
+
+  // Eight neighbours of G's row, times scale, into row `row` of X from `col` on, or (tall) into rows `col` .. of column `row`.
+  __device__ __forceinline__ void put(float (&v)[8], double scale, uint32_t row, uint32_t col, bool tall) const {
+    float rest[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(v[i] * scale);
     split_f16(v, rest);
-    if (!p.tall) {
+    if (!tall) {
       const uint32_t at = x0 + row * xrow + 2 * col;
       write_lds16(at, make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7])));
       write_lds16(at + lo, make_uint4(pack_f16(rest[0], rest[1]), pack_f16(rest[2], rest[3]), pack_f16(rest[4], rest[5]),
@@ -130,11 +120,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_orthogonal_small(SmallOrthogonal
       }
     }
   }
-  __syncthreads();
 
-  // Tile (i, j) of rows' products: a lane has element (row 32 j + fr of the
+  // Tile (i, j) of the products of rows: a lane has element (row 32 j + fr of the
   // second, 8 q + 4 half + r of the first's 32 rows) in register 4 q + r.
-  const auto rows_product = [&](uint32_t at, uint32_t stride, int i, int j, int k_end) {
+  __device__ __forceinline__ f32x16 rows_product(uint32_t at, uint32_t stride, int i, int j, int k_end) const {
     f32x16 acc = {};
     const uint32_t x = at + (32 * i + fr) * stride + 16 * half, y = at + (32 * j + fr) * stride + 16 * half;
     uint4 f[4] = {read_lds16(x), read_lds16(y), read_lds16(x + 32), read_lds16(y + 32)};
@@ -147,25 +136,22 @@ __global__ __launch_bounds__(64 * WAVES) void k_orthogonal_small(SmallOrthogonal
       for (int e = 0; e < 4; ++e) f[e] = n[e];
     }
     return acc;
-  };
-  // Byte of a lane's first four results in a row of A, and from four to four.
-  const auto a_at = [&](int i, int j) { return a0 + (32 * j + fr) * AROW + 2 * (32 * i + 4 * half); };
+  }
+  __device__ __forceinline__ f32x16 gram(int i, int j) const { return rows_product(x0, xrow, i, j, np); }
 
-  for (int step = 0; step < p.steps; ++step) {
-    const bool last = step + 1 == p.steps;
-    for (int tile = wave; tile < TILES; tile += WAVES) {
-      const int i = tile / MR, j = tile % MR;
-      const f32x16 s = rows_product(x0, xrow, i, j, p.np);
-      constexpr float alpha = kAScale / (kXScale * kXScale);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        write_lds8(a_at(i, j) + 16 * q, pack_f16(alpha * s[4 * q], alpha * s[4 * q + 1]),
-                   pack_f16(alpha * s[4 * q + 2], alpha * s[4 * q + 3]));
-    }
+  // Byte of a lane's first four results in a row of A; the next four are 16 on.
+  __device__ __forceinline__ uint32_t a_at(int i, int j) const { return a0 + (32 * j + fr) * AROW + 2 * (32 * i + 4 * half); }
+
+  __device__ __forceinline__ void put_a(int i, int j, int q, float v0, float v1, float v2, float v3) const {
+    constexpr float alpha = kAScale / (kXScale * kXScale);
+    write_lds8(a_at(i, j) + 16 * q, pack_f16(alpha * v0, alpha * v1), pack_f16(alpha * v2, alpha * v3));
+  }
+
+  // A -> b A + c A^2 in its place, when all have read it; barriers before (A is there) and behind.
+  __device__ __forceinline__ void poly(float pb, float pc) const {
     __syncthreads();
-
-    uint2 b[OWN][4];  // B takes A's place when all have read A
-    const float alpha = p.c / (kAScale * kAScale), beta = p.b / kAScale;
+    uint2 b[OWN][4];
+    const float alpha = pc / (kAScale * kAScale), beta = pb / kAScale;
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
       const int tile = wave + WAVES * o, i = tile / MR, j = tile % MR;
@@ -189,8 +175,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_orthogonal_small(SmallOrthogonal
       for (int q = 0; q < 4; ++q) write_lds8(a_at(i, j) + 16 * q, b[o][q].x, b[o][q].y);
     }
     __syncthreads();
+  }
 
-    for (int block = wave; block < p.np / 32; block += WAVES) {
+  // X <- a X + B X; of the last step emit(row, column, the two dwords of four bf16 results) instead.
+  template <class Emit>
+  __device__ __forceinline__ void update(float a, bool last, Emit emit) const {
+    for (int block = wave; block < np / 32; block += WAVES) {
       f32x16 acc[MR];
 #pragma unroll
       for (int r = 0; r < MR; ++r) acc[r] = f32x16{};
@@ -213,7 +203,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_orthogonal_small(SmallOrthogonal
           float v[4], rest[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            v[e] = __builtin_fmaf(half_of(l, e), p.a, __builtin_fmaf(half_of(h, e), p.a, acc[r][4 * q + e]));
+            v[e] = __builtin_fmaf(half_of(l, e), a, __builtin_fmaf(half_of(h, e), a, acc[r][4 * q + e]));
           if (!last) {
             split_f16(v, rest);
             write_lds8(at, pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
@@ -221,23 +211,147 @@ __global__ __launch_bounds__(64 * WAVES) void k_orthogonal_small(SmallOrthogonal
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] *= 1.0f / kXScale;
-            const uint32_t w0 = pack_bf16(v[0], v[1]), w1 = pack_bf16(v[2], v[3]);
-            uint16_t *out = p.out + 8 * first;
-            if (!p.tall) {
-              if (row < p.rows && col < p.cols)
-                *reinterpret_cast<u32x2 *>(out + static_cast<int64_t>(row) * p.cols + col) = u32x2{w0, w1};
-            } else if (row < p.cols && col < p.rows) {
-              uint16_t *to = out + static_cast<int64_t>(col) * p.cols + row;
-              to[0] = static_cast<uint16_t>(w0);
-              to[p.cols] = static_cast<uint16_t>(w0 >> 16);
-              to[2 * p.cols] = static_cast<uint16_t>(w1);
-              to[3 * p.cols] = static_cast<uint16_t>(w1 >> 16);
-            }
+            emit(row, col, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
           }
         }
       }
     }
-    if (!last) __syncthreads();
+  }
+};
+
+// Four results of X's row `row` from column `col` on, at their place in out.
+__device__ __forceinline__ void emit_small(const SmallOrthogonalParams &p, uint16_t *out, int row, int col, uint32_t w0, uint32_t w1) {
+  if (!p.tall) {
+    if (row < p.rows && col < p.cols) *reinterpret_cast<u32x2 *>(out + static_cast<int64_t>(row) * p.cols + col) = u32x2{w0, w1};
+  } else if (row < p.cols && col < p.rows) {
+    uint16_t *to = out + static_cast<int64_t>(col) * p.cols + row;
+    to[0] = static_cast<uint16_t>(w0);
+    to[p.cols] = static_cast<uint16_t>(w0 >> 16);
+    to[2 * p.cols] = static_cast<uint16_t>(w1);
+    to[3 * p.cols] = static_cast<uint16_t>(w1 >> 16);
+  }
+}
+
+template <int MR, int BYTES, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_orthogonal_small(SmallOrthogonalParams p) {
+  using M = SmallMatrix<MR, WAVES>;
+  __shared__ __attribute__((aligned(128))) uint8_t lds[BYTES];
+  __shared__ double parts[WAVES];
+  const M x(lds_address(lds), p.np);
+  x.clear();
+  const uint32_t row_units = p.cols / 8, units = p.rows * row_units;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * units;
+  double ss = 0.0;
+  for (uint32_t u = threadIdx.x; u < units; u += M::THREADS) {
+    float v[8];
+    load_values(p.g, p.f32, first + u, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += static_cast<double>(v[i]) * static_cast<double>(v[i]);
+  }
+  ss = wave_sum(ss);
+  if (x.lane == 0) parts[x.wave] = ss;
+  __syncthreads();
+  ss = parts[0];
+  for (int w = 1; w < WAVES; ++w) ss += parts[w];
+  const double scale = static_cast<double>(kXScale) / (sqrt(ss) + p.eps);
+  for (uint32_t u = threadIdx.x; u < units; u += M::THREADS) {
+    float v[8];
+    load_values(p.g, p.f32, first + u, v);
+    x.put(v, scale, u / row_units, 8 * (u % row_units), p.tall);
+  }
+  __syncthreads();
+
+  for (int step = 0; step < p.steps; ++step) {
+    for (int tile = x.wave; tile < M::TILES; tile += WAVES) {
+      const f32x16 s = x.gram(tile / MR, tile % MR);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x.put_a(tile / MR, tile % MR, q, s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]);
+    }
+    x.poly(p.b, p.c);
+    x.update(p.a, step + 1 == p.steps,
+             [&](int row, int col, uint32_t w0, uint32_t w1) { emit_small(p, p.out + 8 * first, row, col, w0, w1); });
+    __syncthreads();
+  }
+}
+
+// ---- a long matrix in slabs of its columns ------------------------------------------
+// A launch a step: a workgroup has np columns of X.  It adds the slabs' parts of
+// A in their order, makes B (every slab's workgroup the same), its columns of the
+// new X, and their part of the next A.
+
+struct SlabParams {
+  SmallOrthogonalParams m;
+  int32_t slabs, phase;       // phase 0: X from g, and its part of A; then the steps
+  int32_t parts;
+  const double *partial;      // [batch, parts] sums of squares
+  uint4 *x;                   // [batch, slabs, 2, MP, np] fp16: hi, lo
+  const float4 *gram;         // [batch, slabs, MP * MP] of the phase before, and
+  float4 *next_gram;          // of this one
+};
+
+template <int MR, int BYTES, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_orthogonal_slab(SlabParams p) {
+  using M = SmallMatrix<MR, WAVES>;
+  __shared__ __attribute__((aligned(128))) uint8_t lds[BYTES];
+  const M x(lds_address(lds), p.m.np);
+  const int matrix = blockIdx.x / p.slabs, slab = blockIdx.x % p.slabs, np = p.m.np;
+  const int64_t elems = static_cast<int64_t>(p.m.rows) * p.m.cols;
+  const uint32_t row16 = np / 8, plane = M::MP * row16;  // units of 8 halves
+  uint4 *mine = p.x + static_cast<int64_t>(blockIdx.x) * 2 * plane;
+  if (p.phase == 0) {
+    double ss = 0.0;
+    for (int i = x.lane; i < p.parts; i += 64) ss += p.partial[static_cast<int64_t>(matrix) * p.parts + i];
+    ss = wave_sum(ss);
+    const double scale = static_cast<double>(kXScale) / (sqrt(ss) + p.m.eps);
+    x.clear();
+    __syncthreads();
+    const uint32_t lines = p.m.tall ? np : p.m.rows, line_units = p.m.tall ? p.m.cols / 8 : row16;
+    for (uint32_t u = threadIdx.x; u < lines * line_units; u += M::THREADS) {
+      const uint32_t line = u / line_units, unit = u % line_units;
+      const int64_t row = p.m.tall ? static_cast<int64_t>(slab) * np + line : line;
+      const int64_t col = p.m.tall ? 8 * unit : static_cast<int64_t>(slab) * np + 8 * unit;
+      if (row >= p.m.rows || col >= p.m.cols) continue;
+      float v[8];
+      load_values(p.m.g, p.m.f32, (matrix * elems + row * p.m.cols + col) / 8, v);
+      x.put(v, scale, line, 8 * unit, p.m.tall);
+    }
+    __syncthreads();
+  } else {
+    for (uint32_t u = threadIdx.x; u < 2 * plane; u += M::THREADS) {
+      const uint32_t row = u / row16;  // lo's rows follow hi's
+      write_lds16(x.x0 + row * x.xrow + 16 * (u % row16), mine[u]);
+    }
+    const float4 *parts = p.gram + static_cast<int64_t>(matrix) * p.slabs * (M::MP * M::MP / 4);
+    for (int tile = x.wave; tile < M::TILES; tile += WAVES) {
+      float4 sum[4] = {};
+      for (int k = 0; k < p.slabs; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 v = parts[k * (M::MP * M::MP / 4) + (tile * 4 + q) * 64 + x.lane];
+          sum[q].x += v.x;
+          sum[q].y += v.y;
+          sum[q].z += v.z;
+          sum[q].w += v.w;
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x.put_a(tile / MR, tile % MR, q, sum[q].x, sum[q].y, sum[q].z, sum[q].w);
+    }
+    x.poly(p.m.b, p.m.c);
+    const bool last = p.phase == p.m.steps;
+    x.update(p.m.a, last, [&](int row, int col, uint32_t w0, uint32_t w1) {
+      emit_small(p.m, p.m.out + matrix * elems, row, slab * np + col, w0, w1);
+    });
+    if (last) return;
+    __syncthreads();
+  }
+  for (uint32_t u = threadIdx.x; u < 2 * plane; u += M::THREADS)
+    mine[u] = read_lds16(x.x0 + u / row16 * x.xrow + 16 * (u % row16));
+  float4 *part = p.next_gram + static_cast<int64_t>(blockIdx.x) * (M::MP * M::MP / 4);
+  for (int tile = x.wave; tile < M::TILES; tile += WAVES) {
+    const f32x16 s = x.gram(tile / MR, tile % MR);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      part[(tile * 4 + q) * 64 + x.lane] = make_float4(s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]);
   }
 }
 

@@ -78,7 +78,7 @@ def test_norm_of_rows_whose_squares_leave_fp32(rows):
     assert (Q.rms_norm(x, w).y[2] == torch.tensor(1e-30 * 1e3, device="cuda").to(bf)).all()  # eps = 1e-6 alone
 
 
-@pytest.mark.parametrize("batch, rows, cols", [(3, 144, 208), (2, 208, 144), (150, 1024, 2048), (3, 32, 96), (300, 96, 32)])
+@pytest.mark.parametrize("batch, rows, cols", [(3, 144, 208), (2, 208, 144), (150, 1024, 2048), (3, 32, 96), (300, 96, 32), (3, 48, 2000), (400, 1296, 32)])
 def test_orthogonalize_in_place(batch, rows, cols):
     """out may be g, also where the batch takes two passes."""
     g = torch.randn(batch, rows, cols, generator=seeded(6), device="cuda").to(bf)
@@ -86,7 +86,7 @@ def test_orthogonalize_in_place(batch, rows, cols):
     assert Q.orthogonalize(g, steps=2, out=g) is g and torch.equal(g, want)
 
 
-@pytest.mark.parametrize("batch, rows, cols", [(4, 272, 528), (1, 1024, 1040), (5, 64, 96), (300, 96, 64)])
+@pytest.mark.parametrize("batch, rows, cols", [(4, 272, 528), (1, 1024, 1040), (5, 64, 96), (300, 96, 64), (5, 32, 2048), (2, 1040, 128)])
 def test_orthogonalize_in_graphs_that_share_a_workspace(batch, rows, cols):
     """Two captured calls with one workspace, replayed in turn, and again with other values in the captured inputs."""
     gs = [torch.randn(batch, rows, cols, generator=seeded(10 + i), device="cuda") for i in range(2)]
@@ -114,9 +114,9 @@ def test_orthogonalize_in_graphs_that_share_a_workspace(batch, rows, cols):
     assert torch.equal(outs[0], want[1])
 
 
-def test_small_matrices_on_two_streams():
+def test_small_and_long_matrices_on_two_streams():
     sides = [torch.cuda.Stream(), torch.cuda.Stream()]
-    gs = [torch.randn(700, 48, 160, generator=seeded(20 + i), device="cuda") for i in range(2)]
+    gs = [torch.randn(*shape, generator=seeded(20 + i), device="cuda") for i, shape in enumerate(((700, 48, 160), (90, 64, 2048)))]
     want = [Q.orthogonalize(g) for g in gs]
     torch.cuda.synchronize()
     for _ in range(4):

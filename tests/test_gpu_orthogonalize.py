@@ -91,6 +91,19 @@ def test_small_matrices(rows, cols):
     test_several_steps(2, rows, cols, max(4, min(rows, cols) // 4), torch.bfloat16)
 
 
+# Long matrices in slabs of columns: both sides of the sizes and batches that take them, whole and partial last slabs.
+@gpu
+@pytest.mark.parametrize("batch, rows, cols", [(2, 32, 2048), (3, 16, 8192), (1, 16, 8208), (2, 64, 4096), (1, 64, 4112), (2, 48, 640), (300, 64, 592),
+                                               (1, 96, 2048), (1, 96, 2064), (32, 96, 512), (33, 96, 512), (2, 128, 240), (64, 112, 256),
+                                               (65, 112, 256), (1, 128, 1040)])
+def test_slabs(batch, rows, cols):
+    for r, c in ((rows, cols), (cols, rows)):
+        for step in ((0.0, 1, 0), (1.0, 1, -1)):
+            test_one_step_bit_for_bit(batch, r, c, step)
+        test_several_steps(min(batch, 40), r, c, max(4, rows // 4), torch.float32)
+        test_several_steps(batch, r, c, 2 * rows, torch.bfloat16)
+
+
 @gpu
 def test_many_small_matrices():
     """More matrices than the card holds workgroups; each has the bits that it has alone, on the side of other values."""
