@@ -1,4 +1,5 @@
-// All Newton-Schulz steps of one small matrix by one workgroup, in LDS.
+// All Newton-Schulz steps of one small matrix by one workgroup, in LDS; and a
+// step of a long one by a workgroup for each slab of its columns (further down).
 //
 // X (m x n, m <= n: a tall G is taken transposed) lies in LDS as hi and lo in
 // fp16, rows of n + 8, and one m x m array holds A and then B.  Scales and
