@@ -692,8 +692,8 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
  * zeros (NaN with eps 0).
  * rows and cols are multiples of 16, below 2^20; batch <= 65535; 1 <= steps <=
  * 64.  ws: quads_orthogonalize_workspace_bytes(batch, rows, cols) bytes (0 for
- * small matrices); calls
- * in flight at the same time need a workspace each.  The order of every sum is
+ * small matrices; a smaller batch may need more than a larger one); calls in
+ * flight at the same time need a workspace each.  The order of every sum is
  * fixed: repeated calls give the same bits, and matrices of a call do not touch
  * each other; between calls of different sizes the last bits may differ.  out
  * may be g (BF16).  batch == 0: nothing is launched.

@@ -126,3 +126,16 @@ def test_small_and_long_matrices_on_two_streams():
                 got.append(Q.orthogonalize(g))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_orthogonalize_in_slabs_and_passes():
+    """A batch whose slabs take two passes of the workspace: zeros but for matrices on both sides of the passes' edge."""
+    batch, rows, cols = 9000, 32, 2048
+    g = torch.zeros(batch, rows, cols, dtype=bf, device="cuda")
+    at = [0, 4499, 4500, 4501, batch - 1]
+    g[at] = torch.randn(len(at), rows, cols, generator=seeded(30), device="cuda").to(bf)
+    assert Q.orthogonalize_workspace_bytes(batch, rows, cols) < 2.7e9 < 2 * Q.orthogonalize_workspace_bytes(batch, rows, cols)
+    got = Q.orthogonalize(g)
+    assert torch.equal(got[at], Q.orthogonalize(g[at]))
+    got[at] = 0
+    assert not got.any()
