@@ -279,6 +279,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_orthogonal_small(SmallOrthogonal
 // A launch a step: a workgroup has np columns of X.  It adds the slabs' parts of
 // A in their order, makes B (every slab's workgroup the same), its columns of the
 // new X, and their part of the next A.
+//
+// Bound: with few matrices a launch and memory's latency a step (one 32 x 2048
+// 40 us, five steps; one 128 x 2048 110), with many X's traffic and the slabs'
+// parts of A, which every slab reads (256 of 32 x 2048 240 us, of 64 x 2048 796).
 
 struct SlabParams {
   SmallOrthogonalParams m;
