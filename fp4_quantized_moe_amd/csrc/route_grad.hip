@@ -270,7 +270,8 @@ __global__ __launch_bounds__(256) void k_route_grad(RouteGradParams p) {
   for (int q = 0; q < PER; ++q) dp[q] = p.slope && q * LANES + lane < p.E ? g * p.slope[q * LANES + lane] : 0.0f;
   if (p.dw) {
     const bool has = lane < p.top;
-    const int32_t id = has ? p.ids[at * p.top + lane] : -1;
+    int32_t id = has ? p.ids[at * p.top + lane] : -1;
+    if (id >= p.E) id = -1;  // a lane may have a place of that number, where p = 0 times an infinite dw is NaN
     const float w = has ? p.dw[at * p.top + lane] : 0.0f;
     for (int j = 0; j < p.top; ++j) {
       const int32_t e = __shfl(id, j, LANES);
