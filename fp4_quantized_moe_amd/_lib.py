@@ -1188,9 +1188,13 @@ def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dw: torch.Tensor
     return dlogits
 
 
-def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, inverse: torch.Tensor, topk_w: torch.Tensor):
+def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, inverse: torch.Tensor, topk_w: torch.Tensor,
+                         out: torch.Tensor | None = None):
     """quads_moe_combine_backward: dout bf16/fp32 [T, N], y bf16/fp32 [T*top, N]
-    (None: no gradient of the weights) -> (dy bf16 [T*top, N], dw float32 [T, top] or None)."""
+    (None: no gradient of the weights) -> (dy bf16 [T*top, N], dw float32 [T, top] or None).
+    Rows of dy that no slot of inverse names are not written: where slots are
+    dropped (inverse outside [0, T*top)), give dy as `out` with what those rows
+    are to hold, zeros for the products that follow; without it they are undefined."""
     what = "moe_combine_backward"
     d_code = _require_float(what, dout, "dout")
     _require(what, inverse, "inverse", torch.int32, dout)
@@ -1205,10 +1209,15 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor | None, inverse: to
         if tuple(y.shape) != (T * top, N):
             raise QuadsError(f"{what}: y must be [{T * top}, {N}], not {list(y.shape)}")
         dw = torch.empty(T, top, dtype=torch.float32, device=dout.device)
-    dy = torch.empty(T * top, N, dtype=torch.bfloat16, device=dout.device)
+    if out is None:
+        out = torch.empty(T * top, N, dtype=torch.bfloat16, device=dout.device)
+    else:
+        if out.dtype != torch.bfloat16 or tuple(out.shape) != (T * top, N):
+            raise QuadsError(f"{what}: out must be bfloat16 [{T * top}, {N}], not {out.dtype} {list(out.shape)}")
+        _require(what, out, "out", torch.bfloat16, dout)
     _on_device(dout, load().quads_moe_combine_backward, what, dout.data_ptr(), d_code, None if y is None else y.data_ptr(),
-               y_code, inverse.data_ptr(), topk_w.data_ptr(), T, top, N, dy.data_ptr(), None if dw is None else dw.data_ptr())
-    return dy, dw
+               y_code, inverse.data_ptr(), topk_w.data_ptr(), T, top, N, out.data_ptr(), None if dw is None else dw.data_ptr())
+    return out, dw
 
 
 # ---- orthogonalised updates --------------------------------------------------------

@@ -29,3 +29,25 @@ def test_ids_past_the_experts_take_no_gradient(E, value):
     assert want.isfinite().all()
     assert torch.equal(Q.moe_route_backward(logits, ids, dw=loud, slope=b.slope), want)
     assert torch.equal(Q.moe_route_backward(logits, ids, dw=loud, slope=b.slope, mask=mask), torch.where(mask[:, None], want, 0.0))
+
+
+@pytest.mark.parametrize("T", [20, 1200])
+@pytest.mark.parametrize("want_dw", [True, False])
+def test_dropped_slots_into_the_callers_rows(T, want_dw):
+    """With `out` the rows that no slot names keep what the caller put there, here zeros; without drops it is the same call."""
+    dout, y, inverse, w = combine_inputs(11, T, 4, 176, f32, bf)
+    full, dw_full = Q.moe_combine_backward(dout, y, inverse, w)
+    gone = torch.rand(T, 4, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") < 0.3
+    rows = inverse[gone].long()
+    dropped = inverse.clone()
+    dropped[gone] = torch.where(torch.arange(len(rows), device="cuda") % 2 == 0, -5, 2 ** 31 - 1).int()
+    out = torch.zeros(4 * T, 176, dtype=bf, device="cuda")
+    dy, dw = Q.moe_combine_backward(dout, y if want_dw else None, dropped, w, out=out)
+    assert dy is out
+    want = full.clone()
+    want[rows] = 0
+    assert torch.equal(dy, want) and (dw is None if not want_dw else torch.equal(dw, torch.where(gone, 0.0, dw_full)))
+    assert torch.equal(Q.moe_combine_backward(dout, None, inverse, w, out=out)[0], full)
+    for bad, word in ((out[:-1], "out must"), (out.float(), "out must"), (out.t().contiguous().t(), "contiguous"), (out[:, :160].contiguous(), "out must")):
+        with pytest.raises(Q.QuadsError, match=word):
+            Q.moe_combine_backward(dout, y, inverse, w, out=bad)
