@@ -330,7 +330,8 @@ __device__ __forceinline__ void load8(const void *p, int64_t unit, float (&v)[8]
 
 // WAVES waves share a token; its row of dout is read once for its SLOTS >= top
 // slots.  A slot whose row number lies outside y has no row: nothing is
-// written for it but dw = 0.
+// written for it but dw = 0.  Tokens write in no order: a row that two of them
+// name gets units of both.
 template <int SLOTS, int WAVES, bool DOUT_BF16, bool Y_BF16>
 __global__ __launch_bounds__(256) void k_combine_grad(CombineGradParams p) {
   __shared__ float parts[4][SLOTS];

@@ -559,7 +559,8 @@ quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_
 /* ---------------------------------------------------------------------------
  * What a training step of the layer needs around the experts, and the norm in
  * front of it.  All of them: sums and statistics in fp32 or more, each output
- * rounded once; sums in a fixed order, so repeated calls give the same bits.
+ * rounded once; sums in a fixed order, so repeated calls give the same bits
+ * (but in rows that quads_moe_combine_backward's slots name twice).
  * NaN and infinities are defined: they go where the formulas take them.
  *
  * quads_rms_norm -- the residual stream's addition and its root-mean-square
@@ -658,8 +659,10 @@ quads_status_t quads_rms_norm_backward(const void *dy, quads_dtype_t dy_dtype, c
  * dy [T*top, N] bf16 is the dy of quads_moe_gated_backward_bf16 and
  * quads_moe_wgrad_bf16.  dw NULL: not computed, and y may be NULL.  A slot
  * whose inverse lies outside [0, T*top) has no row: its dw is 0.  A row that
- * no slot names is left as it was; one that several name gets the dy of one of
- * them (quads_moe_route names each once).  N % 16 == 0, top <= 16.
+ * no slot names is left as it was.  In one that several name each element is
+ * that of one of them, of another one from element to element and from call to
+ * call: inverse should name no row twice (quads_moe_route's does not).
+ * N % 16 == 0, top <= 16.
  * ------------------------------------------------------------------------- */
 size_t quads_moe_balance_loss_workspace_bytes(int64_t T, int32_t E);
 quads_status_t quads_moe_balance_loss(const float *logits, const int32_t *ids, const uint8_t *mask, int64_t T, int32_t E,

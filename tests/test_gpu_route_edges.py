@@ -51,3 +51,24 @@ def test_dropped_slots_into_the_callers_rows(T, want_dw):
     for bad, word in ((out[:-1], "out must"), (out.float(), "out must"), (out.t().contiguous().t(), "contiguous"), (out[:, :160].contiguous(), "out must")):
         with pytest.raises(Q.QuadsError, match=word):
             Q.moe_combine_backward(dout, y, inverse, w, out=bad)
+
+
+@pytest.mark.parametrize("T, N", [(30, 160), (30, 2064), (1500, 160), (1500, 2064)])
+def test_a_row_named_by_several_slots(T, N):
+    """Each of its elements is that of one of them; rows named once and every dw are as without it."""
+    dout, y, inverse, w = combine_inputs(12, T, 4, N, f32, f32)
+    inverse[1::2, 3] = inverse[0::2, 0]  # two tokens name the row
+    inverse[0::3, 2] = inverse[0::3, 1]  # one token names it twice
+    dy, dw = Q.moe_combine_backward(dout, y, inverse, w)
+    rows = inverse.long()
+    fit, named = torch.zeros(4 * T, N, dtype=torch.bool, device="cuda"), torch.zeros(4 * T, dtype=torch.bool, device="cuda")
+    for j in range(4):  # a slot of every other token at a time: no row occurs twice
+        want = (w[:, j, None] * dout).to(bf)
+        for half in (0, 1):
+            r = rows[half::2, j]
+            assert len(r.unique()) == len(r)
+            fit[r] |= dy[r] == want[half::2]
+            named[r] = True
+        terms = dout.double() * y[rows[:, j]].double()
+        assert ((dw[:, j].double() - terms.sum(1)).abs() <= (N + 2) * U * terms.abs().sum(1)).all()
+    assert fit[named].all()
