@@ -44,6 +44,30 @@ bool misaligned(std::initializer_list<const void *> ptrs) {
   return false;
 }
 
+// An array of a call; a null one has no bytes.
+struct Span {
+  const void *p;
+  int64_t bytes;
+};
+
+// Whether an output meets an input or another output.
+bool overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  const auto meet = [](const Span &a, const Span &b) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && (p < q ? q - p < static_cast<uintptr_t>(a.bytes) : p - q < static_cast<uintptr_t>(b.bytes));
+  };
+  for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span *i = ins.begin(); i != ins.end(); ++i)
+      if (meet(*o, *i)) return true;
+    for (const Span *q = o + 1; q != outs.end(); ++q)
+      if (meet(*o, *q)) return true;
+  }
+  return false;
+}
+
+// `in` less the case that a call allows: `out` in its very place, of its type.
+Span unless(bool allowed, const Span &in, const void *out) { return Span{allowed && in.p == out ? nullptr : in.p, in.bytes}; }
+
 bool mul_ok(int64_t a, int64_t b, int64_t lim) { return a >= 0 && b >= 0 && (a == 0 || b <= lim / a); }
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
@@ -787,6 +811,16 @@ quads_status_t quads_rms_norm(const quads_rms_norm_args *a, void *stream) {
   if (a->rows == 0) return ok();
   if (!a->x || !a->weight || (a->residual && !a->sum) || (quantized && (!a->q_codes || !a->q_scales)))
     return fail(QUADS_ERR_ARG, "rms_norm: null pointer");
+  const int64_t n = a->rows * a->cols;
+  const auto size = [](int32_t t) { return t == QUADS_F32 ? 4 : 2; };
+  const Span x{a->x, n * size(a->x_dtype)}, residual{a->residual, n * size(a->residual_dtype)}, weight{a->weight, a->cols * size(a->weight_dtype)};
+  const Span sum{a->sum, residual.bytes}, y{a->y_bf16, 2 * n}, codes{a->q_codes, a->q_format == QUADS_MXFP4 ? n / 2 : n}, scales{a->q_scales, n / 32},
+      rstd{a->rstd, 4 * a->rows};
+  const bool x_bf16 = a->x_dtype == QUADS_BF16, residual_bf16 = a->residual_dtype == QUADS_BF16;
+  if (overlap({sum, y, codes, scales, rstd}, {weight}) || overlap({codes, scales, rstd}, {x, residual}) ||
+      overlap({sum}, {unless(a->x_dtype == a->residual_dtype, x, a->sum), unless(true, residual, a->sum)}) ||
+      overlap({y}, {unless(x_bf16, x, a->y_bf16), unless(residual_bf16, residual, a->y_bf16)}))
+    return fail(QUADS_ERR_ARG, "rms_norm: an output overlaps an input or another output");
   quads::NormLaunch g{};
   g.rows = a->rows;
   g.cols = static_cast<int32_t>(a->cols);
@@ -842,6 +876,14 @@ quads_status_t quads_rms_norm_backward(const void *dy, quads_dtype_t dy_dtype, c
   const size_t need = dweight ? quads::norm_grad_ws_bytes(rows, static_cast<int32_t>(cols)) : 0;
   if (need > 0 && (ws == nullptr || ws_bytes < need))
     return fail(QUADS_ERR_WORKSPACE, "rms_norm_backward: workspace too small (need %zu)", need);
+  const int64_t n = rows * cols;
+  const auto size = [](int32_t t) { return t == QUADS_F32 ? 4 : 2; };
+  const Span out{dx, n * size(s_dtype)}, sums{dweight, 4 * cols}, space{need > 0 ? ws : nullptr, static_cast<int64_t>(need)};
+  const Span dy_in{dy, n * size(dy_dtype)}, s_in{s, out.bytes}, dsum_in{dsum, out.bytes}, rstd_in{rstd, 4 * rows},
+      weight_in{weight, cols * size(weight_dtype)};
+  if (overlap({out, sums, space}, {rstd_in, weight_in}) || overlap({sums, space}, {dy_in, s_in, dsum_in}) ||
+      overlap({out}, {unless(dy_dtype == s_dtype, dy_in, dx), unless(true, s_in, dx), unless(true, dsum_in, dx)}))
+    return fail(QUADS_ERR_ARG, "rms_norm_backward: an output overlaps an input or another output");
   quads::NormGradLaunch g{};
   g.rows = rows;
   g.cols = static_cast<int32_t>(cols);

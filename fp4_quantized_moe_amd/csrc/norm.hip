@@ -514,8 +514,8 @@ hipError_t launch_rms_norm_grad(const NormGradLaunch &a, hipStream_t stream) {
   if (a.dweight && weight_by_columns(a.rows)) {
     p.dweight = a.dweight;
     p.col_groups = (p.units + kColUnits - 1) / kColUnits;
-    if (a.dx != a.dy) return run(p.col_groups + groups);
-    const hipError_t e = run(p.col_groups);  // before dx takes dy's place
+    if (a.dx != a.dy && a.dx != a.s) return run(p.col_groups + groups);
+    const hipError_t e = run(p.col_groups);  // before dx takes the place of what they read
     if (e != hipSuccess || groups == 0) return e;
     p.col_groups = 0;
     return run(groups);

@@ -572,7 +572,8 @@ quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_
  * cols]; with q_format QUADS_MXFP4 or QUADS_MXFP8 (cols % 32 == 0) the fp32 y
  * in that format, q_codes and q_scales (MXFP4: what quads_moe_mxfp4_gemm
  * takes; flags QUADS_MX_SCALE_EVEN as in quads_quantize_mxfp4); rstd [rows]
- * fp32 receives r for the backward.  sum may be residual or x (of its type).
+ * fp32 receives r for the backward.  sum may be residual or x (of its type),
+ * y_bf16 may be x or residual (BF16).
  * The squares are added in fp32: a row that holds a magnitude of 2e19 or more
  * has r = 0, one of nothing above 1e-23 r = 1 / sqrt(eps).
  *
@@ -589,8 +590,9 @@ quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_
  * type, or NULL) is the gradient that reaches s past the norm.  The gradient
  * passes the outputs' rounding unchanged.  dweight [cols] fp32, or NULL: then
  * no workspace is needed (else quads_rms_norm_backward_workspace_bytes, 0 with
- * few rows).  dx
- * may be dsum, or dy if of one type.  rows == 0: dweight = 0.
+ * few rows).  dx may be s, dsum, or dy if of one type.  rows == 0: dweight = 0.
+ * Here as in quads_rms_norm an output that overlaps an input in any other way,
+ * or another output, is refused (QUADS_ERR_ARG).
  * ------------------------------------------------------------------------- */
 #define QUADS_NONE (-1) /* quads_rms_norm_args.q_format: no quantized output */
 #define QUADS_MXFP8 3

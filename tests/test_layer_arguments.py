@@ -34,3 +34,31 @@ def test_orthogonalize_takes_the_documented_sizes(L, batch, rows, cols):
 def test_orthogonalize_refuses_more(L, batch, rows, cols):
     for r, c in ((rows, cols), (cols, rows)):
         assert L.quads_orthogonalize_workspace_bytes(batch, r, c) == 0 and b"overflow" in L.quads_last_error()
+
+
+N8 = 8 * 64  # elements of the small calls below; every array has a place of its own, from which a case moves one
+AT = {name: P + (1 << 20) * i for i, name in enumerate("x residual weight sum y_bf16 q_codes q_scales rstd dy s w dsum dx dw ws".split())}
+
+
+@pytest.mark.parametrize("kw", [
+    dict(sum=AT["x"], x_dtype=0), dict(sum=AT["x"] + 16), dict(sum=AT["residual"] + 2 * N8 - 16), dict(sum=AT["weight"] - 2 * N8 + 16),
+    dict(y_bf16=AT["sum"]), dict(y_bf16=AT["x"], x_dtype=0), dict(y_bf16=AT["x"] - 16), dict(y_bf16=AT["residual"], residual_dtype=0),
+    dict(y_bf16=AT["weight"]), dict(q_codes=AT["x"]), dict(q_codes=AT["y_bf16"]), dict(q_scales=AT["q_codes"]), dict(rstd=AT["q_scales"]),
+    dict(rstd=AT["x"] + 64), dict(q_codes=AT["sum"] + 2 * N8 - 16), dict(q_scales=AT["residual"] + 16)])
+def test_rms_norm_refuses_overlaps(L, kw):
+    a = Q._RmsNormArgs()
+    base = dict(struct_size=ctypes.sizeof(a), x_dtype=1, residual_dtype=1, weight_dtype=1, q_format=3, rows=8, cols=64, eps=1e-6)
+    base.update({k: AT[k] for k in ("x", "residual", "weight", "sum", "y_bf16", "q_codes", "q_scales", "rstd")})
+    for k, v in {**base, **kw}.items():
+        setattr(a, k, v)
+    assert L.quads_rms_norm(ctypes.byref(a), None) == ARG and b"overlap" in L.quads_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dx=AT["dy"], dt=0), dict(dx=AT["dy"], st=0), dict(dx=AT["dy"] + 16), dict(dx=AT["s"] + 16), dict(dx=AT["s"] - 16),
+    dict(dx=AT["dsum"] + 32), dict(dx=AT["w"]), dict(dx=AT["rstd"]), dict(dw=AT["dx"]), dict(dw=AT["s"]), dict(dw=AT["dy"]), dict(dw=AT["w"]),
+    dict(ws=AT["dy"], rows=2000), dict(ws=AT["dx"] + 2 * 2000 * 64 - 16, rows=2000), dict(ws=AT["dw"] - 64, rows=2000)])
+def test_rms_norm_backward_refuses_overlaps(L, kw):
+    d = dict(dy=AT["dy"], dt=1, s=AT["s"], st=1, w=AT["w"], wt=0, rstd=AT["rstd"], dsum=AT["dsum"], rows=8, cols=64, dx=AT["dx"], dw=AT["dw"],
+             ws=AT["ws"], nws=1 << 20, stream=None)
+    assert L.quads_rms_norm_backward(*{**d, **kw}.values()) == ARG and b"overlap" in L.quads_last_error()
