@@ -998,6 +998,11 @@ quads_status_t quads_orthogonalize(const void *g, quads_dtype_t dt, int64_t batc
   const size_t need = quads::orthogonalize_ws_bytes(batch, rows, cols);
   if (need > 0 && (ws == nullptr || ws_bytes < need))
     return fail(QUADS_ERR_WORKSPACE, "orthogonalize: workspace too small (need %zu)", need);
+  const int64_t n = batch * rows * cols;
+  const Span in{g, n * (dt == QUADS_F32 ? 4 : 2)};
+  const Span out{out_bf16, 2 * n}, space{need > 0 ? ws : nullptr, static_cast<int64_t>(need)};
+  if (overlap({out, space}, {unless(dt == QUADS_BF16, in, out_bf16)}) || overlap({space}, {in}))
+    return fail(QUADS_ERR_ARG, "orthogonalize: out or the workspace overlaps g or each other");
   quads::OrthogonalLaunch o{};
   o.g = g;
   o.g_f32 = dt == QUADS_F32;

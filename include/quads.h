@@ -701,7 +701,8 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
  * flight at the same time need a workspace each.  The order of every sum is
  * fixed: repeated calls give the same bits, and matrices of a call do not touch
  * each other; between calls of different sizes the last bits may differ.  out
- * may be g (BF16).  batch == 0: nothing is launched.
+ * may be g (BF16); out or ws overlapping g in any other way, or each other, is
+ * refused (QUADS_ERR_ARG).  batch == 0: nothing is launched.
  * ------------------------------------------------------------------------- */
 size_t quads_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
 quads_status_t quads_orthogonalize(const void *g, quads_dtype_t dt, int64_t batch, int64_t rows, int64_t cols,

@@ -62,3 +62,22 @@ def test_rms_norm_backward_refuses_overlaps(L, kw):
     d = dict(dy=AT["dy"], dt=1, s=AT["s"], st=1, w=AT["w"], wt=0, rstd=AT["rstd"], dsum=AT["dsum"], rows=8, cols=64, dx=AT["dx"], dw=AT["dw"],
              ws=AT["ws"], nws=1 << 20, stream=None)
     assert L.quads_rms_norm_backward(*{**d, **kw}.values()) == ARG and b"overlap" in L.quads_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(out=P), dict(out=P + 4 * 2 * 160 * 208 - 16), dict(out=P + 16, dt=1), dict(out=P - 16, dt=1), dict(ws=P),
+                                dict(ws=P, out=P, dt=1), dict(ws=P + (4 << 20) + 16), dict(ws=P + (4 << 20) - 4096), dict(ws=P - 4096)])
+@pytest.mark.parametrize("tall", [False, True])
+def test_orthogonalize_refuses_overlaps(L, kw, tall):
+    """g of fp32 under a bf16 out half its size: later passes and other matrices would read results."""
+    d = dict(g=P, dt=0, batch=2, rows=160, cols=208, steps=5, co=(ctypes.c_float * 3)(3.4, -4.8, 2.0), eps=1e-7, out=P + (4 << 20),
+             ws=P + (8 << 20), nws=1 << 20, stream=None)
+    d.update(kw)
+    if tall:
+        d["rows"], d["cols"] = d["cols"], d["rows"]
+    assert L.quads_orthogonalize(*d.values()) == ARG and b"overlap" in L.quads_last_error()
+
+
+def test_orthogonalize_of_small_matrices_refuses_overlaps(L):
+    for kw in (dict(out=P), dict(out=P + 32)):
+        d = dict(g=P, dt=0, batch=2, rows=32, cols=48, steps=5, co=(ctypes.c_float * 3)(3.4, -4.8, 2.0), eps=1e-7, out=P, ws=None, nws=0, stream=None)
+        assert L.quads_orthogonalize(*{**d, **kw}.values()) == ARG and b"overlap" in L.quads_last_error()
