@@ -924,6 +924,9 @@ quads_status_t quads_moe_balance_loss(const float *logits, const int32_t *ids, c
   const size_t need = quads::balance_ws_bytes(T, E);
   if (need > 0 && (ws == nullptr || ws_bytes < need))
     return fail(QUADS_ERR_WORKSPACE, "balance_loss: workspace too small (need %zu)", need);
+  if (overlap({{loss, 4}, {counts, 4 * E}, {slope, 4 * E}, {need > 0 ? ws : nullptr, static_cast<int64_t>(need)}},
+              {{logits, 4 * T * E}, {ids, 4 * T * top}, {mask, T}}))
+    return fail(QUADS_ERR_ARG, "balance_loss: an output overlaps an input or another output");
   const quads::BalanceLaunch a{logits, ids, mask, T, E, top, coef, loss, counts, slope, ws};
   return device_status(quads::launch_balance(a, static_cast<hipStream_t>(stream)), "balance_loss");
 }
@@ -937,6 +940,9 @@ quads_status_t quads_moe_route_backward(const float *logits, const int32_t *ids,
     return fail(QUADS_ERR_ARG, "route_backward: arrays must be 16-byte aligned");
   if (T == 0) return ok();
   if (!logits || !dlogits || (dw && !ids)) return fail(QUADS_ERR_ARG, "route_backward: null pointer");
+  const Span out{dlogits, 4 * T * E};
+  if (overlap({out}, {unless(true, {logits, out.bytes}, dlogits), {ids, dw ? 4 * T * top : 0}, {mask, T}, {dw, 4 * T * top}, {slope, 4 * E}, {dloss, 4}}))
+    return fail(QUADS_ERR_ARG, "route_backward: dlogits overlaps an input");
   const quads::RouteGradLaunch a{logits, ids, mask, dw, slope, dloss, T, E, top, dlogits};
   return device_status(quads::launch_route_grad(a, static_cast<hipStream_t>(stream)), "route_backward");
 }
@@ -953,6 +959,11 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
     return fail(QUADS_ERR_ARG, "combine_backward: arrays must be 16-byte aligned");
   if (T == 0) return ok();
   if (!dout || !inverse || !topk_w || !dy_bf16 || (dw && !y)) return fail(QUADS_ERR_ARG, "combine_backward: null pointer");
+  const Span rows{dy_bf16, 2 * T * top * N}, weights{dw, 4 * T * top};
+  const Span y_in{dw ? y : nullptr, T * top * N * (y_dtype == QUADS_F32 ? 4 : 2)};
+  if (overlap({rows, weights}, {{dout, T * N * (dout_dtype == QUADS_F32 ? 4 : 2)}, {inverse, 4 * T * top}, {topk_w, 4 * T * top}}) ||
+      overlap({rows}, {unless(y_dtype == QUADS_BF16, y_in, dy_bf16)}) || overlap({weights}, {y_in}))
+    return fail(QUADS_ERR_ARG, "combine_backward: an output overlaps an input or another output");
   quads::CombineGradLaunch a{};
   a.dout = dout;
   a.y = y;

@@ -665,6 +665,10 @@ quads_status_t quads_rms_norm_backward(const void *dy, quads_dtype_t dy_dtype, c
  * that of one of them, of another one from element to element and from call to
  * call: inverse should name no row twice (quads_moe_route's does not).
  * N % 16 == 0, top <= 16.
+ *
+ * dlogits may be logits, dy may be y (BF16, no row named twice); an output that
+ * overlaps an input in any other way, or another output, is refused
+ * (QUADS_ERR_ARG).
  * ------------------------------------------------------------------------- */
 size_t quads_moe_balance_loss_workspace_bytes(int64_t T, int32_t E);
 quads_status_t quads_moe_balance_loss(const float *logits, const int32_t *ids, const uint8_t *mask, int64_t T, int32_t E,

@@ -50,3 +50,28 @@ def test_norm_gradient_over_the_stream(rows, cols, dy_type, s_type):
     st = L.quads_rms_norm_backward(dy.data_ptr(), code(dy_type), s.data_ptr(), code(s_type), w.data_ptr(), Q.F32, rstd.data_ptr(),
                                    dsum.data_ptr(), rows, cols, s.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes, stream())
     assert st == 0 and torch.equal(s, dx) and torch.equal(dw, dweight)
+
+
+@pytest.mark.parametrize("T, E, top", [(1, 3, 1), (777, 12, 3), (3000, 100, 8), (70, 1000, 16)])
+def test_router_gradient_over_the_logits(T, E, top):
+    logits = 2 * torch.randn(T, E, generator=seeded(T + E), device="cuda")
+    ids = torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :top].int().contiguous()
+    dw, b = torch.randn(T, top, generator=seeded(1), device="cuda"), Q.moe_balance_loss(logits, ids, 0.01)
+    want = Q.moe_route_backward(logits, ids, dw=dw, slope=b.slope)
+    assert Q.load().quads_moe_route_backward(logits.data_ptr(), ids.data_ptr(), None, dw.data_ptr(), b.slope.data_ptr(), None, T, E, top,
+                                             logits.data_ptr(), stream()) == 0
+    assert torch.equal(logits, want)
+
+
+@pytest.mark.parametrize("T, top, N", [(1, 3, 16), (333, 3, 656), (1100, 16, 528), (1100, 5, 2064), (40, 8, 2048)])
+@pytest.mark.parametrize("drop", [False, True])
+def test_combine_gradient_over_the_rows(T, top, N, drop):
+    """dy in the place of y, also with slots that have no row (their rows keep y)."""
+    inverse = torch.randperm(T * top, generator=seeded(2), device="cuda").int().view(T, top)
+    dout, y = torch.randn(T, N, generator=seeded(3), device="cuda"), torch.randn(T * top, N, generator=seeded(4), device="cuda").to(bf)
+    w = torch.rand(T, top, generator=seeded(5), device="cuda")
+    if drop:
+        inverse[torch.rand(T, top, generator=seeded(6), device="cuda") < 0.3] = -1
+    dy, dw = Q.moe_combine_backward(dout, y, inverse, w, out=y.clone())
+    got, dw_got = Q.moe_combine_backward(dout, y, inverse, w, out=y)
+    assert got is y and torch.equal(got, dy) and torch.equal(dw_got, dw)

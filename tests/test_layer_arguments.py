@@ -81,3 +81,30 @@ def test_orthogonalize_of_small_matrices_refuses_overlaps(L):
     for kw in (dict(out=P), dict(out=P + 32)):
         d = dict(g=P, dt=0, batch=2, rows=32, cols=48, steps=5, co=(ctypes.c_float * 3)(3.4, -4.8, 2.0), eps=1e-7, out=P, ws=None, nws=0, stream=None)
         assert L.quads_orthogonalize(*{**d, **kw}.values()) == ARG and b"overlap" in L.quads_last_error()
+
+
+# places for the router's and the combine's arrays
+PLACE = {name: P + (1 << 20) * i for i, name in enumerate("logits ids mask loss counts slope ws dw dloss dlogits dout y inv w dy".split())}
+
+
+@pytest.mark.parametrize("kw", [dict(loss="logits"), dict(counts="ids"), dict(slope="mask"), dict(ws="logits"), dict(ws="counts"), dict(loss="slope"),
+                                dict(counts="loss"), dict(slope="counts"), dict(loss=PLACE["logits"] + 4 * 5000 * 8 - 16), dict(ws=PLACE["ids"] - 1024)])
+def test_balance_loss_refuses_overlaps(L, kw):
+    d = dict(logits="logits", ids="ids", mask="mask", T=5000, E=8, top=2, coef=0.01, loss="loss", counts="counts", slope="slope", ws="ws",
+             nws=1 << 20, stream=None)
+    assert L.quads_moe_balance_loss(*[PLACE.get(v, v) for v in {**d, **kw}.values()]) == ARG and b"overlap" in L.quads_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(dlogits=PLACE["logits"] + 16), dict(dlogits=PLACE["logits"] - 16), dict(dlogits="ids"), dict(dlogits="mask"), dict(dlogits="dw"),
+                                dict(dlogits=PLACE["slope"] - 4 * 500 * 8 + 16), dict(dlogits="dloss")])
+def test_route_backward_refuses_overlaps(L, kw):
+    d = dict(logits="logits", ids="ids", mask="mask", dw="dw", slope="slope", dloss="dloss", T=500, E=8, top=2, dlogits="dlogits", stream=None)
+    assert L.quads_moe_route_backward(*[PLACE.get(v, v) for v in {**d, **kw}.values()]) == ARG and b"overlap" in L.quads_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(dy="dout"), dict(dy="y"), dict(dy=PLACE["y"] + 16, yt=1), dict(dy=PLACE["y"] - 32, yt=1), dict(dy="inv"), dict(dy="w"),
+                                dict(dw="w"), dict(dw="inv"), dict(dw="dy"), dict(dw="y"), dict(dw=PLACE["dout"] + 4 * 50 * 32 - 16),
+                                dict(dy=PLACE["dout"] + 16, y=None, dw=None)])
+def test_combine_backward_refuses_overlaps(L, kw):
+    d = dict(dout="dout", dt=0, y="y", yt=0, inv="inv", w="w", T=50, top=2, N=32, dy="dy", dw="dw", stream=None)
+    assert L.quads_moe_combine_backward(*[PLACE.get(v, v) for v in {**d, **kw}.values()]) == ARG and b"overlap" in L.quads_last_error()
