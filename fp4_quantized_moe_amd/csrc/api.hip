@@ -918,7 +918,7 @@ quads_status_t quads_moe_balance_loss(const float *logits, const int32_t *ids, c
                                       size_t ws_bytes, void *stream) {
   const quads_status_t st = route_shape("balance_loss", T, E, top);
   if (st != QUADS_OK) return st;
-  if (misaligned({logits, ids, mask, loss, counts, slope, ws}))
+  if (misaligned({logits, ids, loss, counts, slope, ws}))  // mask is read by bytes
     return fail(QUADS_ERR_ARG, "balance_loss: arrays must be 16-byte aligned");
   if (!loss || !counts || !slope || (T > 0 && (!logits || !ids))) return fail(QUADS_ERR_ARG, "balance_loss: null pointer");
   const size_t need = quads::balance_ws_bytes(T, E);
@@ -936,8 +936,9 @@ quads_status_t quads_moe_route_backward(const float *logits, const int32_t *ids,
                                         float *dlogits, void *stream) {
   const quads_status_t st = route_shape("route_backward", T, E, top);
   if (st != QUADS_OK) return st;
-  if (misaligned({logits, ids, mask, dw, slope, dloss, dlogits}))
+  if (misaligned({logits, ids, dw, slope, dlogits}))  // mask is read by bytes
     return fail(QUADS_ERR_ARG, "route_backward: arrays must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(dloss) % 4) return fail(QUADS_ERR_ARG, "route_backward: dloss must be 4-byte aligned");
   if (T == 0) return ok();
   if (!logits || !dlogits || (dw && !ids)) return fail(QUADS_ERR_ARG, "route_backward: null pointer");
   const Span out{dlogits, 4 * T * E};

@@ -652,7 +652,8 @@ quads_status_t quads_rms_norm_backward(const void *dy, quads_dtype_t dy_dtype, c
  * the combine weights (NULL: none; quads_moe_route's topk_w are the chosen
  * probabilities), slope [E] that of the loss above (NULL: none), dloss [1]
  * (device; NULL: 1) what the loss is multiplied by.  E <= 1024, 1 <= top <=
- * min(E, 16).
+ * min(E, 16).  mask may begin at any byte, dloss at any float: a row of a
+ * batch's masks, one number of a buffer.
  *
  * quads_moe_combine_backward -- gradient of quads_moe_combine, from dout [T,
  * N] (F32 or BF16), y [T*top, N] (F32 or BF16), inverse and topk_w:

@@ -72,3 +72,18 @@ def test_a_row_named_by_several_slots(T, N):
         terms = dout.double() * y[rows[:, j]].double()
         assert ((dw[:, j].double() - terms.sum(1)).abs() <= (N + 2) * U * terms.abs().sum(1)).all()
     assert fit[named].all()
+
+
+@pytest.mark.parametrize("T", [1, 37, 3000])
+def test_masks_and_loss_gradients_that_begin_anywhere(T):
+    """A row of a batch's mask, and one number out of a buffer of the losses' gradients."""
+    logits, ids, dw, mask = make(T, T, 24, 3)
+    b = Q.moe_balance_loss(logits, ids, COEF, mask=mask)
+    buffer, masks = torch.linspace(-2, 2, 9, device="cuda"), torch.ones(T + 20, dtype=torch.bool, device="cuda")
+    for at in (1, 2, 3, 7, 16):
+        m, g = masks[at:at + T], buffer[at % 9:at % 9 + 1]
+        m.copy_(mask)
+        got = Q.moe_balance_loss(logits, ids, COEF, mask=m)
+        assert all(torch.equal(x, y) for x, y in zip(got, b))
+        want = Q.moe_route_backward(logits, ids, dw=dw, slope=b.slope, dloss=g.clone(), mask=mask)
+        assert torch.equal(Q.moe_route_backward(logits, ids, dw=dw, slope=b.slope, dloss=g, mask=m), want)

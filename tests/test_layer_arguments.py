@@ -108,3 +108,8 @@ def test_route_backward_refuses_overlaps(L, kw):
 def test_combine_backward_refuses_overlaps(L, kw):
     d = dict(dout="dout", dt=0, y="y", yt=0, inv="inv", w="w", T=50, top=2, N=32, dy="dy", dw="dw", stream=None)
     assert L.quads_moe_combine_backward(*[PLACE.get(v, v) for v in {**d, **kw}.values()]) == ARG and b"overlap" in L.quads_last_error()
+
+
+def test_dloss_is_a_float(L):
+    for at in (1, 2, 3, 18):
+        assert L.quads_moe_route_backward(P, P, None, P, P, P + at, 8, 4, 2, P, None) == ARG and b"4-byte aligned" in L.quads_last_error()
