@@ -101,11 +101,11 @@ struct BalanceParams {
 __device__ __forceinline__ void balance_finish(const BalanceParams &p, const float *sum_p, const int32_t *count, int32_t n,
                                                float *parts) {
   const int t = threadIdx.x;
-  const float inv = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-  const float scale = p.coef * static_cast<float>(p.E) / static_cast<float>(p.top) * inv * inv;
+  // In 64 bits: what fp32 rounds off here is off by the same for all experts, and adds up in the loss.
+  const double tokens = n, scale = n > 0 ? static_cast<double>(p.coef) * p.E / (tokens * tokens * p.top) : 0.0;
   float l = 0.0f;
   if (t < p.E) {  // E <= 1024 threads
-    const float slope = scale * static_cast<float>(count[t]);
+    const float slope = static_cast<float>(scale * count[t]);
     p.counts[t] = count[t];
     p.slope[t] = slope;
     l = slope * sum_p[t];

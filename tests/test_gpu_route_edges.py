@@ -87,3 +87,18 @@ def test_masks_and_loss_gradients_that_begin_anywhere(T):
         assert all(torch.equal(x, y) for x, y in zip(got, b))
         want = Q.moe_route_backward(logits, ids, dw=dw, slope=b.slope, dloss=g.clone(), mask=mask)
         assert torch.equal(Q.moe_route_backward(logits, ids, dw=dw, slope=b.slope, dloss=g, mask=m), want)
+
+
+# tokens whose number, its reciprocal and the square of that all round, for one workgroup and for several
+@pytest.mark.parametrize("T, E, top", [(7, 4, 1), (333, 12, 3), (6554, 128, 8), (8191, 100, 7), (100003, 8, 2), (3001, 1000, 16)])
+@pytest.mark.parametrize("coef", [0.01, 1.0, 0.3])
+def test_slope_is_rounded_once(T, E, top, coef):
+    """slope is the fp32 value nearest to coef E counts / (top n^2): half a step, u, and what the 64-bit quotients add (4 times
+    2^-53).  coef enters as the fp32 value that the call takes."""
+    logits, ids, _, mask = make(T + E, T, E, top)
+    c32 = float(np.float32(coef))
+    for m in (None, mask):
+        got = Q.moe_balance_loss(logits, ids, coef, mask=m)
+        _, counts, slope = O.balance_loss(host(logits), ids.cpu().numpy(), c32, None if m is None else m.cpu().numpy())
+        assert got.counts.tolist() == counts.tolist()
+        assert (np.abs(host(got.slope) - slope) <= (U + 2.0 ** -51) * slope).all()
