@@ -692,14 +692,22 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
  *   `steps` times  X <- a X + (b A + c A^2) X  with A = X X^T
  * (for rows > cols the same from the right, with X^T X), and written as bf16
  * to out [batch, rows, cols].  |g|_F is summed in 64 bits.  The products take
- * fp16 operands and add in fp32; X is kept to 22 bits between the steps (11
- * before the last; entries below 2^-25 to 2^-36), so the result is within about
- * 2e-3 of the formula's (relative, 2-norm) before its rounding to bf16, also
- * for matrices of low rank.  coefficients: the host's a, b, c.  Entries of X, A and b A + c A^2 have to stay below 31, 63
- * and 65504 (they are below 5 for coefficients that keep the singular values
- * below 1.3, as 3.4445, -4.775, 2.0315 do); past that they become infinities
- * and NaN.  A matrix with NaN or infinities gives NaN throughout, one of zeros
- * zeros (NaN with eps 0).
+ * fp16 operands and add in fp32, A and b A + c A^2 are kept in fp16, X to 22
+ * bits between the steps (fewer in entries below 2^-25, none below 2^-36) and
+ * to 11 before the last.
+ * With five steps of 3.4445, -4.775, 2.0315 and |g|_F above 1e-4 eps the result
+ * is within 4e-3 of the formula's (relative, Frobenius norm) before its
+ * rounding to bf16, whatever g's rank; mostly within 1 to 2e-3.  Further steps
+ * add to that: up to 3e-2 after ten.  In directions that g lacks each step
+ * multiplies the rounding of X by a, so with these coefficients and a g of low
+ * rank the result passes 1e-2 at about ten steps and is noise there from about
+ * fourteen on (in fp32 throughout it would be no later).  No bound is given past
+ * ten steps, or for other coefficients with an a of that size.
+ * coefficients: the host's a, b, c.  Entries of X, A and b A + c A^2 have to
+ * stay below 31, 63 and 65504 (they are below 5 for coefficients that keep the
+ * singular values below 1.3, as 3.4445, -4.775, 2.0315 do); past that they
+ * become infinities and NaN.  A matrix with NaN or infinities gives NaN
+ * throughout, one of zeros zeros (NaN with eps 0).
  * rows and cols are multiples of 16, below 2^20; batch <= 65535; batch rows
  * cols <= 2^39; 1 <= steps <= 64.  ws: quads_orthogonalize_workspace_bytes(batch, rows, cols) bytes (0 for
  * small matrices; a smaller batch may need more than a larger one); calls in
