@@ -1235,7 +1235,8 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
     what = "orthogonalize"
     code = _require_float(what, g, "g")
     batch, rows, cols = _batch_rows_cols(what, g.shape)
-    a, b, c = coefficients
+    if len(coefficients) != 3:
+        raise QuadsError(f"{what}: coefficients must be three, not {len(coefficients)}")
     L = load()
     if out is None:
         out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
@@ -1248,6 +1249,6 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=(3.4445, -4.7750
         ws = _workspace(nbytes, g.device) if nbytes else None  # none for small matrices
     else:
         _require(what, ws, "ws", torch.uint8, g)
-    _on_device(g, L.quads_orthogonalize, what, g.data_ptr(), code, batch, rows, cols, steps, (_c_f32 * 3)(a, b, c), eps,
+    _on_device(g, L.quads_orthogonalize, what, g.data_ptr(), code, batch, rows, cols, steps, (_c_f32 * 3)(*coefficients), eps,
                out.data_ptr(), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return out

@@ -77,3 +77,12 @@ def test_many_steps_as_far_as_their_roundings(rows, cols, steps):
         bound = 3 * relative(emulated(g, steps, MUON, 1e-7), want) + 2.0 ** -8
         got = relative(Q.orthogonalize(g, steps=steps), want)
         assert got <= bound < 0.1, (name, got, bound)
+
+
+@gpu
+def test_coefficients_are_three():
+    g = torch.randn(2, 32, 48, device="cuda")
+    for bad in ((), (1.0, 2.0), (1.0, 2.0, 3.0, 4.0)):
+        with pytest.raises(Q.QuadsError, match="coefficients must be three"):
+            Q.orthogonalize(g, coefficients=bad)
+    assert torch.equal(Q.orthogonalize(g, coefficients=list(MUON)), Q.orthogonalize(g))
