@@ -222,8 +222,11 @@ hipError_t run_norm(NormParams p, hipStream_t stream) {
 // rows are under way (8192 x 16384 to bf16 by 256 lanes of eight units 168 us,
 // by 1024 of two 102; 8192 x 8192 52 and 44), and 16 for the shortest (65536 x
 // 128 17 -> 7.7 us with them).  A wave a row only where there are rows to fill
-// the card, and not with four units a lane (16384 x 2048 to bf16 and MXFP8 80
-// us; four waves 67).
+// the card (a bf16 stream to bf16 and MXFP8: 2048 x 1024 5.3 us by a wave, 5.9 by
+// 256 lanes, 4096 x 1024 8.2 and 9.5, but 1024 x 1024 4.4 and 4.15, 256 x 1024
+// 3.8 and 3.0; up to 512 columns the wave is ahead with fewer rows too, 1024 x
+// 512 3.0 and 3.8, 256 x 512 2.8 and 2.9, which the rule leaves), and not with
+// four units a lane (16384 x 2048 to bf16 and MXFP8 80 us; four waves 67).
 template <int QUANT>
 hipError_t run_norm(const NormParams &p, hipStream_t stream) {
   if (p.units <= 16) return run_norm<QUANT, 16, 1>(p, stream);

@@ -12,9 +12,12 @@
 // as the second, so a lane holds four neighbours of a row of X, and a wave takes
 // whole blocks of 32 columns: what it overwrites no other wave reads.
 //
-// Bound: latency (LDS reads, and four barriers a step).  Five steps of one 32 x
-// 32 take 8 us, of 256 of 64 x 128 18, of one 128 x 224 38, of 2000 of 128 x
-// 128 293 (0.29 PFLOP/s); by products over tiles 87, 118, 89 and 724.
+// Bound: latency (LDS reads, and four barriers a step).  Waves wait for 48 to 64%
+// of their cycles; of 2000 of 128 x 128 the matrix cores are busy for 20% and the
+// LDS for 41% of the time and 12% more with bank conflicts, of 256 of 64 x 128 for
+// 9, 28 and 10%.  Five steps of one 32 x 32 take 8 us, of 256 of 64 x 128 18, of
+// one 128 x 224 38, of 2000 of 128 x 128 293 (0.29 PFLOP/s); by products over
+// tiles 87, 118, 89 and 724.
 #pragma once
 
 #include "batched_tile.hpp"
@@ -282,7 +285,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_orthogonal_small(SmallOrthogonal
 //
 // Bound: with few matrices a launch and memory's latency a step (one 32 x 2048
 // 40 us, five steps; one 128 x 2048 110), with many X's traffic and the slabs'
-// parts of A, which every slab reads (256 of 32 x 2048 240 us, of 64 x 2048 796).
+// parts of A, which every slab reads (256 of 32 x 2048 240 us, of 64 x 2048 796:
+// 671 MB read and 201 written a step, where X in and out is 134 each).
 
 struct SlabParams {
   SmallOrthogonalParams m;

@@ -462,6 +462,11 @@ hipError_t launch_combine_grad(const CombineGradLaunch &a, hipStream_t stream) {
   // Four waves a token where one each would leave the card idle, or where all
   // four have whole lines to read (8192 x 8 rows of 2048 198 -> 174 us, 4096 x 16
   // of 2048 205 -> 177; but 16384 x 8 of 512 92 -> 102, of 1024 in bf16 129 -> 137).
+  // Around 1024 tokens, all in bf16, one wave and four: 512 x 8 of 1024 5.7 and
+  // 5.0, 64 x 8 of 1536 5.8 and 3.7, 768 x 8 of 512 4.55 and 4.57, 1024 x 8 of 512
+  // 4.9 and 6.6, of 1024 7.5 and 8.9, of 1536 10.9 and 11.3.  With two slots the
+  // sides meet elsewhere: four waves are ahead up to 1500 tokens of 1024 (1024 x
+  // 2 3.6 and 3.4), and nowhere at 512 (768 x 2 2.8 and 3.0), which the rule leaves.
   return a.T < 1024 || a.N >= 2048 ? run_combine_grad<4>(a, stream) : run_combine_grad<1>(a, stream);
 }
 
