@@ -986,7 +986,7 @@ static quads_status_t orthogonalize_shape(int64_t batch, int64_t rows, int64_t c
     return fail(QUADS_ERR_SHAPE, "orthogonalize: rows and cols must be positive multiples of 16");
   if (rows >= (1 << 20) || cols >= (1 << 20)) return fail(QUADS_ERR_SHAPE, "orthogonalize: rows and cols must be below 2^20");
   if (batch < 0 || batch > 65535) return fail(QUADS_ERR_SHAPE, "orthogonalize: batch must be in [0, 65535]");
-  if (!mul_ok(batch, rows * cols, kMaxElems / 2)) return fail(QUADS_ERR_SHAPE, "orthogonalize: size overflow");
+  if (!mul_ok(batch, rows * cols, int64_t(1) << 39)) return fail(QUADS_ERR_SHAPE, "orthogonalize: size overflow");
   return QUADS_OK;
 }
 

@@ -593,10 +593,10 @@ hipError_t launch_batched_tiles(const BatchedParams &p, hipStream_t stream) {
 // by 256: 4 of 2048 x 2048 1090 and 892 us, 16 of 1024 x 2048 1095 and 1000, 64
 // of 512 x 1024 744 and 746; but 2 of 2048 x 2048 595 and 725, 4 of 1024 x 2048
 // 326 and 547, 64 of 528 x 784 755 and 902; 8 of 1024 x 2048 573 and 632, 530 with
-// each product by the rule; 128 of 528 x 784 1737 and 1673, which it misses).  The smallest where all of them run at once: one
-// matrix of 1024 x 1024 in five steps 198 -> 140 us, of 512 x 512 138 -> 98, 8 of
-// 512 x 512 144 -> 128; beyond, one of 2048 x 2048 takes 375 us with 128 x 128
-// and 653 with it.
+// each product by the rule; 128 of 528 x 784 1737 and 1673, which it misses).
+// The smallest where all of them run at once: one matrix of 1024 x 1024 in five
+// steps 198 -> 140 us, of 512 x 512 138 -> 98, 8 of 512 x 512 144 -> 128; beyond,
+// one of 2048 x 2048 takes 375 us with 128 x 128 and 653 with it.
 template <bool XT, bool WT, int EPI>
 hipError_t launch_batched(const BatchedParams &p, hipStream_t stream) {
   constexpr bool SYM = EPI == kEpiGram || EPI == kEpiPoly;

@@ -709,7 +709,8 @@ quads_status_t quads_moe_combine_backward(const void *dout, quads_dtype_t dout_d
  * become infinities and NaN.  A matrix with NaN or infinities gives NaN
  * throughout, one of zeros zeros (NaN with eps 0).
  * rows and cols are multiples of 16, below 2^20; batch <= 65535; batch rows
- * cols <= 2^39; 1 <= steps <= 64.  ws: quads_orthogonalize_workspace_bytes(batch, rows, cols) bytes (0 for
+ * cols <= 2^39; 1 <= steps <= 64.
+ * ws: quads_orthogonalize_workspace_bytes(batch, rows, cols) bytes (0 for
  * small matrices; a smaller batch may need more than a larger one); calls in
  * flight at the same time need a workspace each.  The order of every sum is
  * fixed: repeated calls give the same bits, and matrices of a call do not touch
