@@ -851,6 +851,9 @@ quads_status_t quads_dequantize_mxfp8(quads_mxfp8_t q, void *out, quads_dtype_t 
   if (misaligned({q.codes, q.scales, out})) return fail(QUADS_ERR_ARG, "dequantize_mxfp8: arrays must be 16-byte aligned");
   if (q.rows == 0) return ok();
   if (!q.codes || !q.scales || !out) return fail(QUADS_ERR_ARG, "dequantize_mxfp8: null pointer");
+  const int64_t n = q.batch * q.rows * q.cols;
+  if (overlap({{out, n * (dt == QUADS_F32 ? 4 : 2)}}, {{q.codes, n}, {q.scales, n / 32}}))
+    return fail(QUADS_ERR_ARG, "dequantize_mxfp8: out overlaps q");
   return device_status(quads::launch_mx8_dequantize(q.codes, q.scales, q.batch * q.rows * q.cols, out, dt == QUADS_BF16,
                                                     static_cast<hipStream_t>(stream)),
                        "dequantize_mxfp8");

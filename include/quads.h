@@ -582,7 +582,8 @@ quads_status_t quads_moe_gated_backward_bf16(const void *dy_bf16, const void *w_
  * takes E = floor(log2 a) - 8, at least -127, and its elements the E4M3 value
  * nearest to y * 2^-E, ties to even, saturating at 448.  A block with NaN or
  * infinities gets byte 255 and codes 0.  quads_dequantize_mxfp8: the values
- * `q` stands for, bf16 or fp32 (exact where the type holds them).
+ * `q` stands for, bf16 or fp32 (exact where the type holds them); out may not
+ * overlap q (QUADS_ERR_ARG).
  *
  * quads_rms_norm_backward -- with n = s rstd and d = dy weight:
  *   dx = rstd (d - n mean(d n)) + dsum,   dweight = sum over rows of dy n.

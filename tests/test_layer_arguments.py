@@ -113,3 +113,10 @@ def test_combine_backward_refuses_overlaps(L, kw):
 def test_dloss_is_a_float(L):
     for at in (1, 2, 3, 18):
         assert L.quads_moe_route_backward(P, P, None, P, P, P + at, 8, 4, 2, P, None) == ARG and b"4-byte aligned" in L.quads_last_error()
+
+
+@pytest.mark.parametrize("out", [P, P + 496, P - 1008, P + (1 << 20), P + (1 << 20) - 16])
+def test_dequantize_mxfp8_refuses_overlaps(L, out):
+    """Values are two or four bytes, codes one: later codes would be read from values."""
+    for dtype in (0, 1):
+        assert L.quads_dequantize_mxfp8(Q._MXFP4(P, P + (1 << 20), 2, 4, 64), out, dtype, None) == ARG and b"overlap" in L.quads_last_error()
